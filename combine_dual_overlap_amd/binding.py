@@ -20,6 +20,8 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_MISALIGNED, MOE_ERR_WO
 MOE_F32, MOE_BF16, MOE_FP8_E4M3FN = 0, 1, 2
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 DBO_SCHED_UNSPLIT, DBO_SCHED_SERIAL, DBO_SCHED_DBO, DBO_SCHED_DBO_LATE_EVENT, DBO_SCHED_DBO_RECV_HOOK = 0, 1, 2, 3, 4
+MOE_GEMM_NT, MOE_GEMM_NN, MOE_GEMM_TN = 0, 1, 2
+GEMM_KINDS = {"nt": MOE_GEMM_NT, "nn": MOE_GEMM_NN, "tn": MOE_GEMM_TN}
 SCHEDULES = {"unsplit": 0, "serial": 1, "dbo": 2, "dbo_late_event": 3, "dbo_recv_hook": 4}
 
 EXPORTED = [
@@ -30,6 +32,8 @@ EXPORTED = [
     "moe_layer_workspace_size", "moe_layer_workspace_layout", "dbo_moe_layer", "moe_status_string",
     "moe_quant_fp8_rows", "moe_dispatch_fp8", "moe_ffn_fp8_workspace_size", "moe_grouped_ffn_fp8",
     "moe_dispatch_send", "moe_dispatch_recv", "moe_dispatch_noalloc_max_workspace", "moe_dispatch_noalloc",
+    "moe_grouped_gemm_workspace_size", "moe_grouped_gemm", "moe_grouped_swiglu", "moe_grouped_swiglu_backward",
+    "moe_combine_backward", "moe_route_backward", "moe_adamw_step",
 ]
 
 
@@ -54,6 +58,18 @@ class dbo_opts(ctypes.Structure):
     _fields_ = [("schedule", ctypes.c_int32), ("min_tokens_to_split", ctypes.c_int32),
                 ("split_at", ctypes.c_int32), ("comm_cu_budget", ctypes.c_int32),
                 ("ffn_tile_m", ctypes.c_int32)]
+
+
+class moe_adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("master", ctypes.c_void_p), ("n", ctypes.c_int64), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32)]
+
+
+class moe_adamw_params(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("seed", ctypes.c_uint32)]
 
 
 class MoEError(RuntimeError):
@@ -111,6 +127,15 @@ def lib():
             "moe_dispatch_recv": (_i32, [_vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp, _vp]),
             "moe_grouped_ffn_fp8": (_i32, [_vp, _vp, _i32, _i32, _vp, _i32, _i64, _vp, _vp, _vp, _vp,
                                            _vp, _i32, _vp, _sz, _vp]),
+            "moe_grouped_gemm_workspace_size": (_sz, [_i32, _i32, _i32, _i64, _i32, _i32]),
+            "moe_grouped_gemm": (_i32, [_i32, _vp, _vp, _i32, _vp, _i32, _i64, _i32, _i32, _vp, _i32, _i32, _vp,
+                                        _sz, _vp]),
+            "moe_grouped_swiglu": (_i32, [_vp, _vp, _i32, _vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp]),
+            "moe_grouped_swiglu_backward": (_i32, [_vp, _vp, _vp, _i32, _vp, _i32, _i64, _i32, _i32, _vp, _vp]),
+            "moe_combine_backward": (_i32, [_vp, _vp, _i32, _i64, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp]),
+            "moe_route_backward": (_i32, [_vp, _i64, _vp, _vp, ctypes.POINTER(moe_route_params), _vp, _i32, _vp]),
+            "moe_adamw_step": (_i32, [ctypes.POINTER(moe_adamw_tensor), _i32, ctypes.POINTER(moe_adamw_params),
+                                      _vp, _vp, _vp, _vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -277,6 +302,180 @@ def moe_combine(y_perm, T, k, inv, topk_w, out, shared_out=None, stream=None):
     H = out.shape[1]
     _check(lib().moe_combine(ptr(y_perm), dtype_code(out), T, H, k, ptr(inv), ptr(topk_w), ptr(shared_out),
                              ptr(out), stream_handle(stream)), "moe_combine")
+
+
+# ------------------------------------------------------------------ training
+# The calls below check shapes, types and devices, and run on the tensors'
+# device: `stream` defaults to that device's current stream.
+
+def _need(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _same_device(*ts):
+    d = ts[0].device
+    for t in ts[1:]:
+        if t is not None and t.device != d:
+            raise ValueError(f"tensors on {d} and {t.device}")
+    return d
+
+
+def _call(fn: str, device, stream, *args):
+    f = getattr(lib(), fn)
+    if device.index == torch.cuda.current_device():
+        _check(f(*args, stream_handle(stream)), fn)
+    else:
+        with torch.cuda.device(device):
+            _check(f(*args, stream_handle(stream)), fn)
+
+
+def _groups(offsets, experts: int) -> int:
+    """E_loc of a grouped call: offsets [E_loc + 1] int32, or None for one dense group."""
+    if offsets is None:
+        return 1
+    _need(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.numel() == experts + 1,
+          f"offsets: expected int32 [{experts + 1}]")
+    return experts
+
+
+def _gemm_sizes(kind: str, a, b, offsets, c):
+    """(kind code, E_loc, cap_rows, N, K) of a moe_grouped_gemm call, shapes and types checked."""
+    _need(kind in GEMM_KINDS, f"kind: one of {sorted(GEMM_KINDS)}")
+    _need(a.dim() == 2 and a.dtype == b.dtype, "a: a 2-d tensor of b's type")
+    cap = a.shape[0]
+    if kind == "tn":
+        _need(b.dim() == 2 and b.shape[0] == cap and c.dim() == 3, "tn: a [rows, N], b [rows, K], c [E, N, K]")
+        E, N, K = c.shape
+        _need(a.shape[1] == N and b.shape[1] == K, "tn: a [rows, N], b [rows, K], c [E, N, K]")
+    else:
+        _need(b.dim() == 3 and c.dim() == 2 and c.shape[0] == cap, f"{kind}: a [rows, K], b of 3 axes, c [rows, N]")
+        E, N, K = b.shape[0], c.shape[1], a.shape[1]
+        _need(tuple(b.shape[1:]) == ((N, K) if kind == "nt" else (K, N)), f"{kind}: b [E, N, K] (nt) or [E, K, N] (nn)")
+    if offsets is None:
+        _need(E == 1, "offsets None: one group")
+    return GEMM_KINDS[kind], _groups(offsets, E), cap, N, K
+
+
+def moe_grouped_gemm_workspace_size(kind: str, a, b, offsets, c) -> int:
+    """Bytes of workspace of moe_grouped_gemm on these tensors (0: none needed)."""
+    code, E, cap, N, K = _gemm_sizes(kind, a, b, offsets, c)
+    return lib().moe_grouped_gemm_workspace_size(code, dtype_code(a), E, cap, N, K)
+
+
+def moe_grouped_gemm(kind: str, a, b, offsets, c, ws=None, accumulate=False, stream=None):
+    """Matrix products grouped by expert; rows [offsets[e], offsets[e+1]) belong to expert e.
+
+    "nt": c [rows, N] = a [rows, K] b[e]^T, b [E, N, K].  "nn": the same with b [E, K, N].
+    "tn": c [E, N, K] = a[rows of e]^T b[rows of e], a [rows, N], b [rows, K].
+    offsets None: one group of all rows.  accumulate: c += product."""
+    code, E, cap, N, K = _gemm_sizes(kind, a, b, offsets, c)
+    d = _same_device(a, b, c, offsets, ws)
+    _call("moe_grouped_gemm", d, stream, code, ptr(a), ptr(b), dtype_code(a), ptr(offsets), E, cap, N, K, ptr(c),
+          dtype_code(c), int(bool(accumulate)), ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+
+
+def moe_grouped_swiglu(x_perm, w13, offsets, h, gu=None, stream=None):
+    """h [rows, I] = silu(x g^T) * (x u^T) with w13 [E, 2I, H]; gu [rows, 2I] (optional) gets the pre-activations."""
+    rows, H = x_perm.shape
+    E, I = w13.shape[0], h.shape[1]
+    _need(tuple(w13.shape) == (E, 2 * I, H) and h.shape[0] == rows, "w13 [E, 2I, H], h [rows, I]")
+    _need(gu is None or tuple(gu.shape) == (rows, 2 * I), "gu [rows, 2I]")
+    _need(x_perm.dtype == w13.dtype == h.dtype and (gu is None or gu.dtype == h.dtype), "one type for every tensor")
+    _need(offsets is not None or E == 1, "offsets None: one group")
+    d = _same_device(x_perm, w13, h, gu, offsets)
+    _call("moe_grouped_swiglu", d, stream, ptr(x_perm), ptr(w13), dtype_code(x_perm), ptr(offsets),
+          _groups(offsets, E), rows, H, I, ptr(gu), ptr(h))
+
+
+def moe_grouped_swiglu_backward(dy_perm, w2, gu, offsets, dgu, stream=None):
+    """dgu [rows, 2I] from dy_perm [rows, H], w2 [E, H, I] and the pre-activations gu [rows, 2I] (dgu may be gu)."""
+    rows, H = dy_perm.shape
+    E, I = w2.shape[0], w2.shape[2]
+    _need(w2.shape[1] == H and tuple(gu.shape) == (rows, 2 * I) and gu.shape == dgu.shape,
+          "dy_perm [rows, H], w2 [E, H, I], gu and dgu [rows, 2I]")
+    _need(dy_perm.dtype == w2.dtype == gu.dtype == dgu.dtype, "one type for every tensor")
+    _need(offsets is not None or E == 1, "offsets None: one group")
+    d = _same_device(dy_perm, w2, gu, dgu, offsets)
+    _call("moe_grouped_swiglu_backward", d, stream, ptr(dy_perm), ptr(w2), ptr(gu), dtype_code(dy_perm), ptr(offsets),
+          _groups(offsets, E), rows, H, I, ptr(dgu))
+
+
+def moe_combine_backward(dout, y_perm, inv, topk_w, dy_perm, dtopk_w, stream=None):
+    """dy_perm [rows, H] and dtopk_w [T, k] of moe_combine's out [T, H]; inv [T*k], topk_w [T, k] as it took them."""
+    T, H = dout.shape
+    k, cap = topk_w.shape[1], y_perm.shape[0]
+    _need(y_perm.dim() == 2 and y_perm.shape[1] == H and y_perm.shape == dy_perm.shape, "y_perm and dy_perm [rows, H]")
+    _need(dout.dtype == y_perm.dtype == dy_perm.dtype, "one type for dout, y_perm and dy_perm")
+    _need(topk_w.shape == dtopk_w.shape and topk_w.shape[0] == T and inv.numel() == T * k, "topk_w, dtopk_w, inv: T x k")
+    _need(inv.dtype == torch.int32 and topk_w.dtype == dtopk_w.dtype == torch.float32, "inv int32; weights float32")
+    d = _same_device(dout, y_perm, inv, topk_w, dy_perm, dtopk_w)
+    _call("moe_combine_backward", d, stream, ptr(dout), ptr(y_perm), dtype_code(dout), T, H, k, cap, ptr(inv),
+          ptr(topk_w), ptr(dy_perm), ptr(dtopk_w))
+
+
+def moe_route_backward(logits, topk_ids, dtopk_w, params: moe_route_params, dlogits, stream=None):
+    """dlogits [T, E] (float32 or bfloat16) of moe_route_topk's weights, from its logits, ids and dtopk_w [T, k]."""
+    T, E = logits.shape
+    _need(E == params.E and tuple(dlogits.shape) == (T, E), "logits and dlogits [T, E] with params.E experts")
+    _need(tuple(topk_ids.shape) == (T, params.k) and dtopk_w.shape == topk_ids.shape, "topk_ids and dtopk_w [T, k]")
+    _need(logits.dtype == dtopk_w.dtype == torch.float32 and topk_ids.dtype == torch.int32,
+          "logits and dtopk_w float32, topk_ids int32")
+    d = _same_device(logits, topk_ids, dtopk_w, dlogits)
+    _call("moe_route_backward", d, stream, ptr(logits), T, ptr(topk_ids), ptr(dtopk_w), ctypes.byref(params),
+          ptr(dlogits), dtype_code(dlogits))
+
+
+def adamw_params(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, seed=0) -> moe_adamw_params:
+    return moe_adamw_params(lr, beta1, beta2, eps, weight_decay, seed & 0xFFFFFFFF)
+
+
+class AdamWTable:
+    """The tensors of an optimizer as moe_adamw_step takes them.  Holds references: the tensors live as long as it."""
+
+    def __init__(self, entries, device, keep):
+        self.entries, self.device, self.keep = entries, device, keep
+
+
+def moe_adamw_table(params, grads, m, v, m_scale=None, v_scale=None, master=None) -> AdamWTable:
+    """Lists of tensors, one entry per parameter.  params float32 or bfloat16; grads likewise; m and v float32, or
+    8-bit codes (float8_e4m3fn or uint8) with m_scale and v_scale uint8 [ceil(n / 128)]; master float32 or None."""
+    n = len(params)
+    _need(n > 0, "no tensors")
+    cols = [params, grads, m, v, m_scale, v_scale, master]
+    for c in cols:
+        _need(c is None or len(c) == n, "lists of one length")
+    entries = (moe_adamw_tensor * n)()
+    device = params[0].device
+    for i in range(n):
+        p, g, mi, vi, ms, vs, ma = (None if c is None else c[i] for c in cols)
+        size = p.numel()
+        _need(g.numel() == size and mi.numel() == size and vi.numel() == size and (ma is None or ma.numel() == size),
+              f"tensor {i}: sizes differ")
+        eight = mi.dtype != torch.float32
+        _need(p.dtype in (torch.float32, torch.bfloat16) and g.dtype in (torch.float32, torch.bfloat16) and
+              mi.dtype == vi.dtype and mi.dtype in (torch.float32, torch.uint8, torch.float8_e4m3fn) and
+              (ma is None or (ma.dtype == torch.float32 and p.dtype == torch.bfloat16)), f"tensor {i}: types")
+        _need(eight == (ms is not None) == (vs is not None), f"tensor {i}: scales go with 8-bit states")
+        if eight:
+            _need(ms.dtype == vs.dtype == torch.uint8 and ms.numel() == vs.numel() == (size + 127) // 128,
+                  f"tensor {i}: scales uint8 [ceil(n / 128)]")
+        _same_device(params[0], p, g, mi, vi, ms, vs, ma)
+        entries[i] = moe_adamw_tensor(ptr(p), ptr(g), ptr(mi), ptr(vi), ptr(ms), ptr(vs), ptr(ma), size,
+                                      dtype_code(p), dtype_code(g), dtype_code(mi))
+    return AdamWTable(entries, device, cols)
+
+
+def moe_adamw_step(table: AdamWTable, hp: moe_adamw_params, step, lr_scale=None, grad_scale=None, stream=None):
+    """One update of the table's tensors.  step: int32 device scalar, 1 at the first update; lr_scale and grad_scale:
+    float32 device scalars or None."""
+    _need(step.dtype == torch.int32 and step.numel() == 1, "step: one int32")
+    for s in (lr_scale, grad_scale):
+        _need(s is None or (s.dtype == torch.float32 and s.numel() == 1), "lr_scale, grad_scale: one float32")
+        _need(s is None or s.device == table.device, "lr_scale, grad_scale: on the tensors' device")
+    _need(step.device == table.device, "step: on the tensors' device")
+    _call("moe_adamw_step", table.device, stream, table.entries, len(table.entries), ctypes.byref(hp), ptr(step),
+          ptr(lr_scale), ptr(grad_scale))
 
 
 class DboContext:

@@ -13,7 +13,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdbomoe.so")
-SOURCES = ["route.hip", "dispatch.hip", "ffn.hip", "combine.hip", "layer.hip"]
+SOURCES = ["route.hip", "dispatch.hip", "ffn.hip", "combine.hip", "layer.hip", "grouped_gemm.hip", "backward.hip",
+           "adamw.hip"]
 ARCH = "gfx950"
 
 

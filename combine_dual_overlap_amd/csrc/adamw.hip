@@ -1,0 +1,385 @@
+// AdamW over many tensors in few launches, for gfx950.
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,  g = grad * grad_scale
+//   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v / (1 - b2^t)) + eps)
+// in fp32, each operation rounded by itself.  HBM-bound: every tensor is read
+// once and written once.
+//
+// 8-bit states: blocks of 128 consecutive elements hold E4M3 codes and one
+// E8M0 byte b (scale 2^(b-127), the smallest with max <= 448 * scale), as the
+// fp8 rows of the dispatch do.  The second moment is stored as its square
+// root, which halves its range in powers of two.  Codes are rounded
+// stochastically: a step changes a state by less than half a code's distance
+// for almost every element (b2 = 0.999 changes sqrt(v) by 0.05 %, a code is
+// up to 12 % away), so rounding to nearest would hold it where it is.  A
+// nonzero sqrt(v) never becomes code 0, or the next step would divide by eps
+// alone.  bf16 parameters without an fp32 master are rounded stochastically
+// for the same reason.
+//
+// Random numbers: two 32-bit hashes of (seed, step, tensor, element), so the
+// result depends on nothing else.  mix() is two rounds of xor-shift and
+// multiplication, a bijection of 32-bit words.
+#include <math.h>
+
+#include "common.h"
+
+namespace dbomoe {
+
+constexpr int kAdamTensors = 48;      // tensors per launch: the table is a kernel argument
+constexpr int kAdamGroup = 2048;      // elements a workgroup takes at a time (8 a thread)
+
+struct AdamTensor {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  uint8_t* ms;
+  uint8_t* vs;
+  float* master;
+  int64_t n;
+  uint32_t key;                       // 0x85ebca77 * the tensor's number
+  int32_t first;                      // first workgroup
+};
+
+struct AdamArgs {
+  AdamTensor t[kAdamTensors];
+  int32_t count;
+  int32_t groups;                     // groups of kAdamGroup elements per workgroup
+  uint32_t seed;
+  float b1, omb1, b2, omb2, eps;
+  double lr, wd, log_b1, log_b2;
+  const int32_t* step;
+  const float* lr_scale;
+  const float* grad_scale;
+};
+static_assert(sizeof(AdamArgs) <= 4096, "kernel argument");
+
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x7feb352du;
+  x ^= x >> 15;
+  x *= 0x846ca68bu;
+  return x ^ (x >> 16);
+}
+
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+// E8M0 byte -> scale; byte 0 is 2^-127, a denormal.
+__device__ __forceinline__ float e8m0(uint8_t b) { return __uint_as_float(b ? static_cast<uint32_t>(b) << 23 : 0x400000u); }
+
+// max over the 16 lanes that share a block of 128 elements
+__device__ __forceinline__ float block_max(float v) {
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, kWave));
+  return v;
+}
+
+__device__ __forceinline__ int block_exponent(float top) {
+  const uint32_t b = __float_as_uint(top);
+  const int e = static_cast<int>(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return e < -127 ? -127 : e;
+}
+
+// |x| * 2^-e to an E4M3 code by stochastic rounding: floor(value / code step + r / 2^20), r of 20 bits.
+__device__ __forceinline__ uint32_t encode(float x, float inv, uint32_t r, bool keep) {
+  const float y = fabsf(x) * inv;
+  uint32_t c;
+  if (y < 0.015625f)                                      // below 2^-6 the codes are 2^-9 apart
+    c = (static_cast<uint32_t>(y * 536870912.f) + r) >> 20;
+  else
+    c = ((__float_as_uint(y) + r) >> 20) - 960u;
+  c = c > 0x7fu ? 0x7fu : c;                              // infinities and NaN
+  if (keep && y > 0.f && c == 0) c = 1;
+  return c | ((__float_as_uint(x) >> 24) & 0x80u);
+}
+
+template <int N> struct Bytes { uint8_t b[N]; };
+
+// 8 elements from index i on; those behind n read as zero.
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* base, int64_t i, int64_t n, float* x) {
+  if (i + 8 <= n) {
+    if constexpr (BF16) {
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(static_cast<const bf16_t*>(base) + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[2 * j] = __uint_as_float(v[j] << 16);
+        x[2 * j + 1] = __uint_as_float(v[j] & 0xffff0000u);
+      }
+    } else {
+      const f32x4_t* s = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(base) + i);
+      const f32x4_t a = s[0], b = s[1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[j] = a[j];
+        x[4 + j] = b[j];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] = 0.f;
+      if (i + j < n) x[j] = BF16 ? bf16_to_f32(static_cast<const bf16_t*>(base)[i + j]) : static_cast<const float*>(base)[i + j];
+    }
+  }
+}
+
+__device__ __forceinline__ void store8_f32(float* base, int64_t i, int64_t n, const float* x) {
+  if (i + 8 <= n) {
+    f32x4_t* d = reinterpret_cast<f32x4_t*>(base + i);
+    d[0] = f32x4_t{x[0], x[1], x[2], x[3]};
+    d[1] = f32x4_t{x[4], x[5], x[6], x[7]};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j < n) base[i + j] = x[j];
+  }
+}
+
+__device__ __forceinline__ void store8_bf16(bf16_t* base, int64_t i, int64_t n, const uint32_t* h) {
+  if (i + 8 <= n) {
+    *reinterpret_cast<u32x4_t*>(base + i) =
+        u32x4_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j < n) base[i + j] = static_cast<bf16_t>(h[j]);
+  }
+}
+
+__device__ __forceinline__ uint64_t load8_codes(const uint8_t* base, int64_t i, int64_t n) {
+  if (i + 8 <= n) return *reinterpret_cast<const uint64_t*>(base + i);
+  uint64_t v = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (i + j < n) v |= static_cast<uint64_t>(base[i + j]) << (8 * j);
+  return v;
+}
+
+__device__ __forceinline__ void store8_codes(uint8_t* base, int64_t i, int64_t n, const uint32_t* c) {
+  if (i + 8 <= n) {
+    const uint32_t lo = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, hi = c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24;
+    *reinterpret_cast<uint64_t*>(base + i) = static_cast<uint64_t>(hi) << 32 | lo;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j < n) base[i + j] = static_cast<uint8_t>(c[j]);
+  }
+}
+
+__device__ __forceinline__ void decode8(uint64_t q, float scale, float* x) {
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int v = static_cast<int>(q >> (32 * w));
+    const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(v, false);
+    const auto b = __builtin_amdgcn_cvt_pk_f32_fp8(v, true);
+    x[4 * w] = a[0] * scale;
+    x[4 * w + 1] = a[1] * scale;
+    x[4 * w + 2] = b[0] * scale;
+    x[4 * w + 3] = b[1] * scale;
+  }
+}
+
+enum AdamParam { PARAM_F32 = 0, PARAM_BF16 = 1, PARAM_MASTER = 2 };
+
+template <bool EIGHT, int PARAM, bool GRAD_BF16>
+__global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
+#pragma clang fp contract(off)
+  // this workgroup's tensor: the last whose first workgroup is not behind it
+  int lo = 0, hi = a.count - 1;
+  const int blk = blockIdx.x;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.t[mid].first <= blk)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const AdamTensor& t = a.t[lo];
+  const int64_t n = t.n;
+  const int step = max(*a.step, 1);
+  const float gs = a.grad_scale ? *a.grad_scale : 1.f;
+  const double lr = a.lr * (a.lr_scale ? static_cast<double>(*a.lr_scale) : 1.0);
+  const float step_size = static_cast<float>(lr / -expm1(step * a.log_b1));
+  const float rbc2 = static_cast<float>(1.0 / sqrt(-expm1(step * a.log_b2)));
+  const float decay = static_cast<float>(1.0 - lr * a.wd);
+  const uint32_t key0 = mix(mix(a.seed + 0x9e3779b9u * static_cast<uint32_t>(step)) + t.key);
+
+  const int64_t begin = static_cast<int64_t>(blk - t.first) * a.groups * kAdamGroup + threadIdx.x * 8;
+  for (int it = 0; it < a.groups; ++it) {
+    const int64_t i = begin + it * kAdamGroup;
+    // the 16 lanes of a block of 128 stay together: they meet in block_max
+    if (i - (threadIdx.x & 15) * 8 >= n) break;
+    float g[8], m[8], v[8], p[8], root[8];
+    load8<GRAD_BF16>(t.g, i, n, g);
+    if constexpr (EIGHT) {
+      const uint64_t qm = load8_codes(static_cast<const uint8_t*>(t.m), i, n);
+      const uint64_t qv = load8_codes(static_cast<const uint8_t*>(t.v), i, n);
+      decode8(qm, e8m0(t.ms[i >> 7]), m);
+      decode8(qv, e8m0(t.vs[i >> 7]), v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = v[j] * v[j];
+    } else {
+      load8<false>(t.m, i, n, m);
+      load8<false>(t.v, i, n, v);
+    }
+    if constexpr (PARAM == PARAM_MASTER)
+      load8<false>(t.master, i, n, p);
+    else
+      load8<PARAM == PARAM_BF16>(t.p, i, n, p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float gj = g[j] * gs;
+      m[j] = m[j] * a.b1 + gj * a.omb1;
+      v[j] = v[j] * a.b2 + (gj * a.omb2) * gj;
+      root[j] = sqrtf(v[j]);
+      p[j] = p[j] * decay - step_size * (m[j] / (root[j] * rbc2 + a.eps));
+    }
+    uint32_t one[8], two[8];
+    if constexpr (EIGHT || PARAM == PARAM_BF16) {
+      const uint32_t key = key0 ^ (static_cast<uint32_t>(i >> 32) * 0x9e3779b9u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        one[j] = mix(static_cast<uint32_t>(i + j) ^ key);
+        two[j] = mix(one[j] + 0x9e3779b9u);
+      }
+    }
+    if constexpr (EIGHT) {
+      float tm = 0.f, tv = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        tm = fmaxf(tm, fabsf(m[j]));
+        tv = fmaxf(tv, root[j]);
+      }
+      const int em = block_exponent(block_max(tm)), ev = block_exponent(block_max(tv));
+      const float im = pow2f(-em), iv = pow2f(-ev);
+      uint32_t cm[8], cv[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        cm[j] = encode(m[j], im, one[j] >> 12, false);
+        cv[j] = encode(root[j], iv, two[j] >> 12, true);
+      }
+      store8_codes(static_cast<uint8_t*>(t.m), i, n, cm);
+      store8_codes(static_cast<uint8_t*>(t.v), i, n, cv);
+      if ((threadIdx.x & 15) == 0) {
+        t.ms[i >> 7] = static_cast<uint8_t>(em + 127);
+        t.vs[i >> 7] = static_cast<uint8_t>(ev + 127);
+      }
+    } else {
+      store8_f32(static_cast<float*>(t.m), i, n, m);
+      store8_f32(static_cast<float*>(t.v), i, n, v);
+    }
+    if constexpr (PARAM == PARAM_F32) {
+      store8_f32(static_cast<float*>(t.p), i, n, p);
+    } else {
+      uint32_t h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (PARAM == PARAM_BF16) {
+          const uint32_t u = __float_as_uint(p[j]);
+          const uint32_t r = (one[j] & 0xfffu) << 4 | (two[j] & 0xfu);
+          h[j] = (u & 0x7f800000u) == 0x7f800000u ? f32_to_bf16(p[j]) : (u + r) >> 16;
+        } else {
+          h[j] = f32_to_bf16(p[j]);
+        }
+      }
+      store8_bf16(static_cast<bf16_t*>(t.p), i, n, h);
+      if constexpr (PARAM == PARAM_MASTER) store8_f32(t.master, i, n, p);
+    }
+  }
+}
+
+template <bool EIGHT, int PARAM>
+static void adamw_launch(const AdamArgs& a, bool gbf16, unsigned blocks, hipStream_t s) {
+  if (gbf16)
+    hipLaunchKernelGGL((k_adamw<EIGHT, PARAM, true>), dim3(blocks), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_adamw<EIGHT, PARAM, false>), dim3(blocks), dim3(256), 0, s, a);
+}
+
+}  // namespace dbomoe
+
+using namespace dbomoe;
+
+extern "C" moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n_tensors, const moe_adamw_params* hp,
+                                     const int32_t* step, const float* lr_scale, const float* grad_scale,
+                                     void* stream) {
+  if (!hp || n_tensors < 0 || (n_tensors > 0 && !tensors)) return MOE_ERR_INVALID_ARG;
+  if (!(hp->lr >= 0) || !(hp->beta1 >= 0 && hp->beta1 < 1) || !(hp->beta2 >= 0 && hp->beta2 < 1) || !(hp->eps > 0) ||
+      !(hp->weight_decay >= 0) || !isfinite(hp->lr) || !isfinite(hp->eps) || !isfinite(hp->weight_decay))
+    return MOE_ERR_INVALID_ARG;
+  if (n_tensors == 0) return MOE_OK;
+  if (!step) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(step) || !aligned16(lr_scale) || !aligned16(grad_scale)) return MOE_ERR_MISALIGNED;
+  int64_t total = 0;
+  for (int i = 0; i < n_tensors; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.n < 0) return MOE_ERR_INVALID_ARG;
+    if ((t.param_dtype != MOE_F32 && t.param_dtype != MOE_BF16) ||
+        (t.grad_dtype != MOE_F32 && t.grad_dtype != MOE_BF16) ||
+        (t.state_dtype != MOE_F32 && t.state_dtype != MOE_FP8_E4M3FN) || t.n > (int64_t{1} << 36))
+      return MOE_ERR_UNSUPPORTED;
+    if (t.master && t.param_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if (t.n == 0) continue;
+    const bool eight = t.state_dtype == MOE_FP8_E4M3FN;
+    if (!t.param || !t.grad || !t.m || !t.v || (eight != (t.m_scale != nullptr)) || (eight != (t.v_scale != nullptr)))
+      return MOE_ERR_INVALID_ARG;
+    if (t.param == t.grad || t.m == t.v || t.param == t.master) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(t.param) || !aligned16(t.grad) || !aligned16(t.m) || !aligned16(t.v) || !aligned16(t.master))
+      return MOE_ERR_MISALIGNED;
+    total += (t.n + kAdamGroup - 1) / kAdamGroup;
+  }
+  AdamArgs a{};
+  a.groups = total >= 8192 ? 4 : 1;
+  a.seed = hp->seed;
+  a.b1 = static_cast<float>(hp->beta1);
+  a.omb1 = static_cast<float>(1.0 - hp->beta1);
+  a.b2 = static_cast<float>(hp->beta2);
+  a.omb2 = static_cast<float>(1.0 - hp->beta2);
+  a.eps = static_cast<float>(hp->eps);
+  a.lr = hp->lr;
+  a.wd = hp->weight_decay;
+  a.log_b1 = log(hp->beta1);
+  a.log_b2 = log(hp->beta2);
+  a.step = step;
+  a.lr_scale = lr_scale;
+  a.grad_scale = grad_scale;
+  const hipStream_t s = as_stream(stream);
+  // One launch per 48 tensors of one combination of types (and 2^24
+  // workgroups: a grid holds fewer than 2^32 threads).
+  for (int combo = 0; combo < 12; ++combo) {
+    const bool eight = combo & 1, gbf16 = combo & 2;
+    const int kind = combo >> 2;
+    int64_t blocks = 0;
+    a.count = 0;
+    auto flush = [&]() -> moe_status {
+      if (a.count == 0) return MOE_OK;
+      const unsigned nb = static_cast<unsigned>(blocks);
+      if (kind == PARAM_F32)
+        eight ? adamw_launch<true, PARAM_F32>(a, gbf16, nb, s) : adamw_launch<false, PARAM_F32>(a, gbf16, nb, s);
+      else if (kind == PARAM_BF16)
+        eight ? adamw_launch<true, PARAM_BF16>(a, gbf16, nb, s) : adamw_launch<false, PARAM_BF16>(a, gbf16, nb, s);
+      else
+        eight ? adamw_launch<true, PARAM_MASTER>(a, gbf16, nb, s) : adamw_launch<false, PARAM_MASTER>(a, gbf16, nb, s);
+      a.count = 0;
+      blocks = 0;
+      DBOMOE_CHECK_LAUNCH();
+      return MOE_OK;
+    };
+    for (int i = 0; i < n_tensors; ++i) {
+      const moe_adamw_tensor& t = tensors[i];
+      const int tk = t.master ? PARAM_MASTER : t.param_dtype == MOE_BF16 ? PARAM_BF16 : PARAM_F32;
+      if (t.n == 0 || tk != kind || (t.state_dtype == MOE_FP8_E4M3FN) != eight || (t.grad_dtype == MOE_BF16) != gbf16)
+        continue;
+      const int64_t per = static_cast<int64_t>(a.groups) * kAdamGroup, nb = (t.n + per - 1) / per;
+      if (a.count == kAdamTensors || blocks + nb >= (1 << 24)) {
+        const moe_status st = flush();
+        if (st != MOE_OK) return st;
+      }
+      a.t[a.count++] = AdamTensor{t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.master, t.n,
+                                  0x85ebca77u * static_cast<uint32_t>(i), static_cast<int32_t>(blocks)};
+      blocks += nb;
+    }
+    const moe_status st = flush();
+    if (st != MOE_OK) return st;
+  }
+  return MOE_OK;
+}

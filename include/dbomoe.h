@@ -279,6 +279,136 @@ moe_status moe_combine(const void* y_perm, moe_dtype act, int64_t T, int32_t H, 
                        void* out, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Training: the gradients of the layer's steps and the optimizer's step.
+ *
+ * moe_grouped_gemm - matrix products grouped by expert with ragged row counts.
+ * Expert e owns rows [offsets[e], offsets[e+1]) of the row operands
+ * (offsets from moe_dispatch, starting at 0 and not decreasing; what lies
+ * outside [0, cap_rows] is cut off), or NULL with E_loc == 1: all cap_rows rows.
+ *   MOE_GEMM_NT  c[r, n]    = sum_k a[r, k] b[e, n, k]   a [cap_rows, K],
+ *                b [E_loc, N, K], c [cap_rows, N]: a linear layer's output
+ *   MOE_GEMM_NN  c[r, n]    = sum_k a[r, k] b[e, k, n]   a [cap_rows, K],
+ *                b [E_loc, K, N], c [cap_rows, N]: the gradient of its input
+ *                (a the output's gradient, b the weights as NT takes them)
+ *   MOE_GEMM_TN  c[e, n, k] = sum_r a[r, n] b[r, k]      a [cap_rows, N],
+ *                b [cap_rows, K], c [E_loc, N, K]: the gradient of its weights
+ *   ab   MOE_BF16 or MOE_F32 (a and b); ct MOE_F32, or MOE_BF16 with ab bf16
+ *   accumulate  0: c = product; 1: c = c + product, rounded once
+ *   ws   moe_grouped_gemm_workspace_size(...) bytes of the same arguments (fp32
+ *        partial products where the output has few tiles and the reduction is
+ *        long; 0 bytes otherwise, then ws may be NULL)
+ * Sums are fp32, rounded once to ct, and do not depend on timing.  NT / NN
+ * leave c's rows outside the experts' ranges untouched; TN writes zeros for an
+ * expert without rows (accumulate: leaves it as it is).  N and K are multiples
+ * of 8 (bf16) or 4 (fp32), else MOE_ERR_MISALIGNED.  E_loc <= 256.  c must not
+ * overlap a, b or ws.
+ *
+ * moe_grouped_swiglu - the NT product with w13 [E_loc, 2I, H] (gate rows over
+ * up rows, as moe_grouped_ffn) with SwiGLU in its epilogue:
+ *   gu = x_perm w13^T  [cap_rows, 2I] act out, or NULL: the pre-activations
+ *        that the backward pass needs
+ *   h  = silu(g) * u   [cap_rows, I] act out, from the fp32 sums
+ * moe_grouped_swiglu_backward - through the down projection and SwiGLU: the NN
+ * product dh = dy_perm w2 (w2 [E_loc, H, I]) stays in registers;
+ *   dgu[r, i]     = dh u s (1 + g (1 - s))   s = sigmoid(g), (g, u) from gu
+ *   dgu[r, I + i] = dh g s
+ *   dgu [cap_rows, 2I] act out; may be gu itself.
+ * Both: act MOE_BF16 or MOE_F32 for every operand; the rules of
+ * moe_grouped_gemm for offsets, rows, sizes and alignment.
+ * ------------------------------------------------------------------------- */
+typedef enum { MOE_GEMM_NT = 0, MOE_GEMM_NN = 1, MOE_GEMM_TN = 2 } moe_gemm_kind;
+size_t moe_grouped_gemm_workspace_size(moe_gemm_kind kind, moe_dtype ab, int32_t E_loc, int64_t cap_rows,
+                                       int32_t N, int32_t K);
+moe_status moe_grouped_gemm(moe_gemm_kind kind, const void* a, const void* b, moe_dtype ab,
+                            const int32_t* offsets, int32_t E_loc, int64_t cap_rows, int32_t N, int32_t K,
+                            void* c, moe_dtype ct, int32_t accumulate, void* ws, size_t ws_bytes,
+                            void* stream);
+moe_status moe_grouped_swiglu(const void* x_perm, const void* w13, moe_dtype act, const int32_t* offsets,
+                              int32_t E_loc, int64_t cap_rows, int32_t H, int32_t I, void* gu, void* h,
+                              void* stream);
+moe_status moe_grouped_swiglu_backward(const void* dy_perm, const void* w2, const void* gu, moe_dtype act,
+                                       const int32_t* offsets, int32_t E_loc, int64_t cap_rows, int32_t H,
+                                       int32_t I, void* dgu, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_combine_backward - gradients of moe_combine.
+ *   dout [T, H] act; y_perm [cap_rows, H] act and inv, topk_w as moe_combine took them
+ *   dy_perm  [cap_rows, H] act out: dy_perm[inv[t*k+j]] = topk_w[t, j] * dout[t]
+ *            (rows no pair points at are untouched)
+ *   dtopk_w  [T, k] fp32 out: <dout[t], y_perm[inv[t*k+j]]>, 0 where inv is
+ *            outside [0, cap_rows)
+ * The gradient of shared_out is dout itself; the gradient of moe_dispatch's x
+ * is moe_combine of the rows' gradients with all weights 1.
+ * ------------------------------------------------------------------------- */
+moe_status moe_combine_backward(const void* dout, const void* y_perm, moe_dtype act, int64_t T, int32_t H,
+                                int32_t k, int64_t cap_rows, const int32_t* inv, const float* topk_w,
+                                void* dy_perm, float* dtopk_w, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_route_backward - gradient of moe_route_topk's weights in its logits
+ * (the selection itself has none).
+ *   logits [T, E] fp32 (moe_route_topk's logits_out), topk_ids [T, k] its ids,
+ *   dtopk_w [T, k] fp32; params as given to moe_route_topk
+ *   dlogits [T, E] out, fp32 or bf16 (dl): rounded once
+ * Ids outside [0, E) contribute nothing; an id that occurs twice in a row
+ * counts twice.  A softmax row without a finite logit gets zeros.  The bias's
+ * gradient is the sum of dlogits over tokens; x's and w_router's are
+ * moe_grouped_gemm products (NN and TN) of dlogits with offsets NULL.
+ * ------------------------------------------------------------------------- */
+moe_status moe_route_backward(const float* logits, int64_t T, const int32_t* topk_ids, const float* dtopk_w,
+                              const moe_route_params* params, void* dlogits, moe_dtype dl, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_adamw_step - one AdamW update of n_tensors tensors.
+ *   g = grad * grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ * computed in fp32, with lr = hp.lr * lr_scale and t = *step >= 1.
+ *   tensors  HOST array, read during the call; per tensor:
+ *     param   [n] fp32 or bf16, updated
+ *     grad    [n] fp32 or bf16
+ *     master  [n] fp32 or NULL (bf16 param only): the parameter in fp32,
+ *             updated; param receives it rounded to nearest.  A bf16 param
+ *             without master is rounded stochastically.
+ *     state_dtype MOE_F32: m, v [n] fp32, m_scale and v_scale NULL
+ *     state_dtype MOE_FP8_E4M3FN: m holds E4M3 codes of m and v codes of
+ *             sqrt(v), [n] bytes each, in blocks of 128 consecutive elements
+ *             with one E8M0 byte each in m_scale, v_scale [ceil(n/128)] (any
+ *             byte alignment).  A block's scale 2^(b-127) is the smallest with
+ *             max <= 448 * scale; codes are rounded stochastically, and a
+ *             nonzero sqrt(v) never to 0.  All bytes zero is the state before
+ *             the first step.
+ *   step, lr_scale, grad_scale  DEVICE scalars (lr_scale, grad_scale may be
+ *     NULL = 1), so that a captured step can be replayed as they change
+ *   hp.seed  seeds the stochastic rounding.  With mix(x) = { x ^= x >> 16;
+ *     x *= 0x7feb352d; x ^= x >> 15; x *= 0x846ca68b; x ^= x >> 16 } on 32-bit
+ *     words, element i of tensor number q uses
+ *       key = mix(mix(seed + 0x9e3779b9 * t) + 0x85ebca77 * q),
+ *       a = mix((uint32)i ^ key ^ 0x9e3779b9 * (i >> 32)),  b = mix(a + 0x9e3779b9);
+ *     m's code takes a >> 12, sqrt(v)'s b >> 12 (20 bits each), a bf16 param
+ *     (a & 0xfff) << 4 | (b & 0xf) (16 bits).
+ * Tensors of n == 0 are skipped; tensors must not overlap.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  uint8_t* m_scale;
+  uint8_t* v_scale;
+  float* master;
+  int64_t n;                    /* <= 2^36 */
+  moe_dtype param_dtype, grad_dtype, state_dtype;
+} moe_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;   /* lr, wd >= 0; 0 <= beta < 1; eps > 0 */
+  uint32_t seed;
+} moe_adamw_params;
+
+moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n_tensors, const moe_adamw_params* hp,
+                          const int32_t* step, const float* lr_scale, const float* grad_scale, void* stream);
+
+/* ---------------------------------------------------------------------------
  * dbo_moe_layer - the whole layer under Dual-Batch Overlap.
  * ------------------------------------------------------------------------- */
 typedef struct {
