@@ -127,7 +127,7 @@ def lib():
             "moe_dispatch_recv": (_i32, [_vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp, _vp]),
             "moe_grouped_ffn_fp8": (_i32, [_vp, _vp, _i32, _i32, _vp, _i32, _i64, _vp, _vp, _vp, _vp,
                                            _vp, _i32, _vp, _sz, _vp]),
-            "moe_grouped_gemm_workspace_size": (_sz, [_i32, _i32, _i32, _i64, _i32, _i32]),
+            "moe_grouped_gemm_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i64, _i32, _i32]),
             "moe_grouped_gemm": (_i32, [_i32, _vp, _vp, _i32, _vp, _i32, _i64, _i32, _i32, _vp, _i32, _i32, _vp,
                                         _sz, _vp]),
             "moe_grouped_swiglu": (_i32, [_vp, _vp, _i32, _vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp]),
@@ -360,7 +360,7 @@ def _gemm_sizes(kind: str, a, b, offsets, c):
 def moe_grouped_gemm_workspace_size(kind: str, a, b, offsets, c) -> int:
     """Bytes of workspace of moe_grouped_gemm on these tensors (0: none needed)."""
     code, E, cap, N, K = _gemm_sizes(kind, a, b, offsets, c)
-    return lib().moe_grouped_gemm_workspace_size(code, dtype_code(a), E, cap, N, K)
+    return lib().moe_grouped_gemm_workspace_size(code, dtype_code(a), int(offsets is None), E, cap, N, K)
 
 
 def moe_grouped_gemm(kind: str, a, b, offsets, c, ws=None, accumulate=False, stream=None):

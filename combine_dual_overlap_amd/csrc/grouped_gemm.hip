@@ -33,11 +33,20 @@ struct GgParams {
 
 struct GgTile {
   int e, m_off, nt, split;
+  int m_n;                 // positions of the tile on the first axis
   int rows;                // the expert's rows
   int64_t row0;            // its first row
 };
 
 static __device__ __attribute__((aligned(16))) uint32_t g_zero16[4];   // source of the zeros behind a reduction's end
+
+// The lane number, opaque to the compiler: what is computed from it inside a
+// loop stays there instead of occupying registers around the main loop.
+__device__ __forceinline__ int fresh_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
 
 // Rows of expert e, kept inside the row operands whatever the offsets hold.
 __device__ __forceinline__ void gg_rows(const GgParams& p, int e, int& o, int& n) {
@@ -58,19 +67,52 @@ template <int KIND, int BM>
 __device__ __forceinline__ bool gg_locate(const GgParams& p, int* s_loc, GgTile& t) {
   const int b = blockIdx.x;
   if constexpr (KIND == MOE_GEMM_TN) {
-    const int per_e = p.m_tiles * p.n_tiles;
-    const int64_t R = static_cast<int64_t>(p.E) * per_e;
-    const int64_t per = (R + 7) / 8;
-    const int64_t L = (b & 7) * per + (b >> 3);
-    if ((b >> 3) >= per || L >= R) return false;
-    t.e = static_cast<int>(L / per_e);
-    const int l = static_cast<int>(L % per_e);
-    t.m_off = (l % p.m_tiles) * BM;
-    t.nt = l / p.m_tiles;
-    int o, n;
-    gg_rows(p, t.e, o, n);
-    t.row0 = o;
-    t.rows = n;
+    // Every expert's tiles are spread over the XCDs, the experts of most rows
+    // first (in classes of a factor of two), so that no XCD is left with a
+    // large expert at the end: with Zipf-distributed rows (largest expert 29 %
+    // of them) a contiguous run of experts per XCD took 3.5 times as long.
+    const int per_e = p.m_tiles * p.n_tiles, per_x = (per_e + 7) / 8;
+    int k = (b >> 3) / per_x;                         // the expert's place in that order
+    if (k >= p.E) return false;
+    const int l = ((b + k) & 7) * per_x + (b >> 3) % per_x;
+    if (l >= per_e) return false;
+    const int lane = threadIdx.x & 63;
+    int cls[4], o4[4], n4[4], top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o4[i] = n4[i] = 0;
+      if (lane * 4 + i < p.E) gg_rows(p, lane * 4 + i, o4[i], n4[i]);
+      cls[i] = lane * 4 + i >= p.E ? -1 : n4[i] == 0 ? 0 : 32 - __clz((n4[i] + 31) / 32);
+      top = max(top, cls[i]);
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) top = max(top, __shfl_xor(top, d, kWave));
+    int e = 0;
+    for (int c = __builtin_amdgcn_readfirstlane(top); c >= 0; --c) {
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t has = __ballot(cls[i] == c);
+        const int count = __popcll(has);
+        if (!found && k < count) {
+          const bool mine = cls[i] == c && __popcll(has & lanemask_lt()) == k;
+          const int src = __builtin_amdgcn_readfirstlane(__ffsll(static_cast<unsigned long long>(__ballot(mine))) - 1);
+          e = src * 4 + i;
+          t.row0 = __builtin_amdgcn_readlane(o4[i], src);
+          t.rows = __builtin_amdgcn_readlane(n4[i], src);
+          found = true;
+        }
+        if (!found) k -= count;
+      }
+      if (found) break;
+    }
+    t.e = e;
+    // bands of four tiles along the first axis: an XCD's share is compact
+    const int band = l / (4 * p.n_tiles), r = l - band * 4 * p.n_tiles;
+    const int high = min(4, p.m_tiles - 4 * band);
+    t.m_off = (4 * band + r % high) * BM;
+    t.m_n = min(BM, p.N - t.m_off);
+    t.nt = r / high;
   } else {
     if (threadIdx.x < kWave) {
       const int lane = threadIdx.x;
@@ -96,8 +138,16 @@ __device__ __forceinline__ bool gg_locate(const GgParams& p, int* s_loc, GgTile&
           if (L >= acc * p.n_tiles && L < (acc + t4[i]) * p.n_tiles) {
             const int l = L - acc * p.n_tiles;
             s_loc[1] = lane * 4 + i;
-            s_loc[2] = l % t4[i];
-            s_loc[3] = l / t4[i];
+            // bands of eight row tiles: what runs together on an XCD is about
+            // as high as wide
+            const int band = l / (8 * p.n_tiles), r = l - band * 8 * p.n_tiles;
+            const int high = min(8, t4[i] - 8 * band);
+            // the expert's rows in tiles of equal height (a multiple of 32
+            // where tiles are higher than that)
+            const int height = BM <= 32 ? BM : ((n4[i] + t4[i] - 1) / t4[i] + 31) / 32 * 32;
+            s_loc[2] = (8 * band + r % high) * height;
+            s_loc[3] = r / high;
+            s_loc[6] = min(height, n4[i] - s_loc[2]);
             s_loc[4] = o4[i];
             s_loc[5] = n4[i];
           }
@@ -108,12 +158,19 @@ __device__ __forceinline__ bool gg_locate(const GgParams& p, int* s_loc, GgTile&
     __syncthreads();
     if (!s_loc[0]) return false;
     t.e = s_loc[1];
-    t.m_off = s_loc[2] * BM;
+    t.m_off = s_loc[2];
+    t.m_n = s_loc[6];
     t.nt = s_loc[3];
     t.row0 = s_loc[4];
     t.rows = s_loc[5];
     __syncthreads();                // read by all before the scratch is reused
   }
+  t.e = __builtin_amdgcn_readfirstlane(t.e);
+  t.m_off = __builtin_amdgcn_readfirstlane(t.m_off);
+  t.m_n = __builtin_amdgcn_readfirstlane(t.m_n);
+  t.nt = __builtin_amdgcn_readfirstlane(t.nt);
+  t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+  t.row0 = __builtin_amdgcn_readfirstlane(static_cast<int>(t.row0));
   t.split = blockIdx.y;
   return true;
 }
@@ -171,25 +228,102 @@ __device__ __forceinline__ void store_swiglu(const GgParams& p, int64_t row, int
 }
 
 // d silu(g)/dg = s (1 + g (1 - s)), s the sigmoid of g
-template <bool F32>
-__device__ __forceinline__ void store_swiglu_bwd(const GgParams& p, int64_t row, int col, const f32x4_t& dh) {
-  const int64_t gi = row * 2 * p.N + col;
-  const f32x4_t g = load4<F32>(p.gu, gi), u = load4<F32>(p.gu, gi + p.N);
-  f32x4_t dg, du;
+__device__ __forceinline__ void swiglu_bwd(const f32x4_t& dh, const f32x4_t& g, const f32x4_t& u, f32x4_t& dg,
+                                           f32x4_t& du) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float s = 1.0f / (1.0f + __expf(-g[i]));
     dg[i] = dh[i] * u[i] * (s * (1.0f + g[i] * (1.0f - s)));
     du[i] = dh[i] * (g[i] * s);
   }
+}
+
+template <bool F32>
+__device__ __forceinline__ void store_swiglu_bwd(const GgParams& p, int64_t row, int col, const f32x4_t& dh) {
+  const int64_t gi = row * 2 * p.N + col;
+  const f32x4_t g = load4<F32>(p.gu, gi), u = load4<F32>(p.gu, gi + p.N);
+  f32x4_t dg, du;
+  swiglu_bwd(dh, g, u, dg, du);
   store4<F32>(p.C, gi, dg);
   store4<F32>(p.C, gi + p.N, du);
+}
+
+// Eight columns of a bf16 row.
+__device__ __forceinline__ void store8(void* base, int64_t i, const f32x4_t& a, const f32x4_t& b) {
+  *reinterpret_cast<u32x4_t*>(static_cast<bf16_t*>(base) + i) =
+      u32x4_t{cvt_bf16x2(a[0], a[1]), cvt_bf16x2(a[2], a[3]), cvt_bf16x2(b[0], b[1]), cvt_bf16x2(b[2], b[3])};
+}
+
+__device__ __forceinline__ void load8(const void* base, int64_t i, f32x4_t& a, f32x4_t& b) {
+  const u32x4_t v = *reinterpret_cast<const u32x4_t*>(static_cast<const bf16_t*>(base) + i);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    a[2 * k] = __uint_as_float(v[k] << 16);
+    a[2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
+    b[2 * k] = __uint_as_float(v[2 + k] << 16);
+    b[2 * k + 1] = __uint_as_float(v[2 + k] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ void store_c8(const GgParams& p, int64_t i, f32x4_t a, f32x4_t b) {
+  if (p.part || p.c_f32) {
+    store_c(p, i, a);
+    store_c(p, i + 4, b);
+  } else {
+    if (p.accumulate) {
+      f32x4_t c, d;
+      load8(p.C, i, c, d);
+      a += c;
+      b += d;
+    }
+    store8(p.C, i, a, b);
+  }
+}
+
+__device__ __forceinline__ void store_swiglu8(const GgParams& p, int64_t row, int col, const f32x4_t& g0,
+                                              const f32x4_t& g1, const f32x4_t& u0, const f32x4_t& u1) {
+  f32x4_t a, b;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = silu_f32(g0[i]) * u0[i];
+    b[i] = silu_f32(g1[i]) * u1[i];
+  }
+  store8(p.C, row * p.N + col, a, b);
+  if (p.gu_out) {
+    store8(p.gu_out, row * 2 * p.N + col, g0, g1);
+    store8(p.gu_out, row * 2 * p.N + p.N + col, u0, u1);
+  }
+}
+
+__device__ __forceinline__ void store_swiglu_bwd8(const GgParams& p, int64_t row, int col, const f32x4_t& d0,
+                                                  const f32x4_t& d1) {
+  const int64_t gi = row * 2 * p.N + col;
+  f32x4_t g[2], u[2], dg[2], du[2];
+  load8(p.gu, gi, g[0], g[1]);
+  load8(p.gu, gi + p.N, u[0], u[1]);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) swiglu_bwd(k ? d1 : d0, g[k], u[k], dg[k], du[k]);
+  store8(p.C, gi, dg[0], dg[1]);
+  store8(p.C, gi + p.N, du[0], du[1]);
 }
 
 // ---- bf16 -------------------------------------------------------------------
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
+
+// LDS DMA from a uniform base plus a 32-bit byte offset per lane (see lds_dma16).
+__device__ __forceinline__ void lds_dma16_at(uint32_t lds_addr, const void* base, uint32_t off) {
+  const uint32_t a = __builtin_amdgcn_readfirstlane(lds_addr);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(a), "v"(off), "s"(base)
+               : "memory");
+}
+
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
 
 // One operand's tile of BT output-axis positions x BK of the reduction, staged
 // by LDS DMA.  RCONT: the reduction axis is the contiguous one in memory; LDS
@@ -200,17 +334,21 @@ typedef short s16x8_t __attribute__((ext_vector_type(8)));
 // Swizzles, so that the addresses of one read spread over the banks: RCONT
 // XORs the 16-byte chunk with the row; the other XORs the 32-byte chunk with
 // (step & 3) + 4 * (step >> 3 & 1), the eight steps that half a wave reads.
-template <bool RCONT, int BT, int BK, int NW>
+// USED: positions that hold anything (RCONT only: the others are not loaded).
+template <bool RCONT, int BT, int BK, int NW, int USED = BT>
 struct Operand {
-  static constexpr int ROWS = RCONT ? BT : BK, COLS = RCONT ? BK : BT;
+  static constexpr int ROWS = RCONT ? USED : BK, COLS = RCONT ? BK : BT;
   static constexpr int CPR = COLS / 8, RPD = 64 / CPR;     // 16-byte chunks per row, rows per DMA
-  static constexpr int NQ = ROWS / RPD / NW;               // DMAs per wave and stage
+  static constexpr int NQ = (ROWS + RPD * NW - 1) / (RPD * NW);   // DMAs per wave and stage
   static constexpr int BYTES = BT * BK * 2;
-  static_assert(NQ >= 1 && NQ * NW * RPD == ROWS, "DMA split");
+  static_assert(NQ * NW * RPD <= (RCONT ? BT : BK), "DMA split");
   static_assert(RCONT || COLS >= 128, "transposing reads: 8 chunks of 32 bytes");
 
-  const bf16_t* src[NQ];
-  int step[NQ];             // reduction step of this lane's chunk inside the stage
+  // RCONT: the XOR that row r puts on its 16-byte chunks
+  static __device__ __forceinline__ int swz(int r) { return BK == 32 ? (r >> 2) & 3 : r & 7; }
+
+  const bf16_t* base;       // uniform
+  uint32_t off[NQ];         // this lane's chunks: byte offsets from the stage's base
   int64_t advance;          // elements per stage
 
   // base: element (0, 0) of the tile's matrix; t0: first output-axis position;
@@ -218,42 +356,42 @@ struct Operand {
   // positions on the output axis (positions behind it read a valid one: their
   // outputs are not stored).
   template <typename RowOf>
-  __device__ __forceinline__ void init(const bf16_t* base, int64_t ld, int t0, int limit, RowOf row) {
+  __device__ __forceinline__ void init(const bf16_t* first, int64_t ld, int t0, int limit, RowOf row) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int lr = lane / CPR, pos = lane % CPR;
+    base = first;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      const int R = RPD * (wave * NQ + i) + lr;
+      const int R = RPD * (i * NW + wave) + lr;
       if constexpr (RCONT) {
-        const int c = pos ^ (R & 7);
-        step[i] = c * 8;
-        src[i] = base + static_cast<int64_t>(row(R)) * ld + c * 8;
+        off[i] = (static_cast<uint32_t>(row(R)) * static_cast<uint32_t>(ld) + (pos ^ swz(R)) * 8) * 2;
       } else {
         const int key = (R & 3) | ((R >> 3 & 1) << 2);
         int col = t0 + (((pos >> 1) ^ key) << 4) + (pos & 1) * 8;
         col = min(col, limit - 8);
-        step[i] = R;
-        src[i] = base + static_cast<int64_t>(R) * ld + col;
+        off[i] = (static_cast<uint32_t>(R) * static_cast<uint32_t>(ld) + col) * 2;
       }
     }
     advance = RCONT ? BK : static_cast<int64_t>(BK) * ld;
   }
 
   __device__ __forceinline__ void issue(uint32_t lds, int ks) const {
-    const int wave = threadIdx.x >> 6;
-    const int64_t off = ks * advance;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bf16_t* at = base + ks * advance;
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) lds_dma16(lds + (wave * NQ + i) * 1024, src[i] + off);
+    for (int i = 0; i < NQ; ++i) lds_dma16_at(lds + (i * NW + wave) * 1024, at, off[i]);
   }
 
-  // the stage that holds the reduction's end: `left` of its steps exist
+  // the stage that holds the reduction's end: `left` of its steps exist, the rest are zeros
   __device__ __forceinline__ void issue_tail(uint32_t lds, int ks, int left) const {
-    const int wave = threadIdx.x >> 6;
-    const int64_t off = ks * advance;
+    const int lane = fresh_lane();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint8_t* at = reinterpret_cast<const uint8_t*>(base + ks * advance);
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      const void* ptr = step[i] < left ? static_cast<const void*>(src[i] + off) : g_zero16;
-      lds_dma16(lds + (wave * NQ + i) * 1024, ptr);
+      const int R = RPD * (i * NW + wave) + lane / CPR;
+      const int step = RCONT ? ((lane % CPR) ^ swz(R)) * 8 : R;
+      lds_dma16(lds + (i * NW + wave) * 1024, step < left ? static_cast<const void*>(at + off[i]) : g_zero16);
     }
   }
 
@@ -262,7 +400,8 @@ struct Operand {
     const int lane = threadIdx.x & 63;
     const bf16_t* T = reinterpret_cast<const bf16_t*>(tile);
     if constexpr (RCONT) {
-      return *reinterpret_cast<const bf16x8_t*>(&T[lds_off_k<BK>(pos + (lane & 15), kk * 4 + (lane >> 4))]);
+      const int r = pos + (lane & 15);
+      return *reinterpret_cast<const bf16x8_t*>(&T[r * BK + (((kk * 4 + (lane >> 4)) ^ swz(r)) << 3)]);
     } else {
       const int g = lane >> 4, L = lane & 15;
       const int key = (L >> 2) | ((g & 1) << 2);
@@ -276,20 +415,17 @@ struct Operand {
   }
 };
 
-// Tile BM x BN, BK reduction steps per stage, WM x WN waves, a ring of NBUF
-// stages (stage s in buffer s % NBUF, issued NBUF - 1 stages ahead).
-template <int KIND, int EPI, int BM, int BN, int BK, int WAVES_M, int WAVES_N, int NBUF, int MINW>
-__global__ __launch_bounds__(WAVES_M * WAVES_N * 64, MINW) void k_grouped_gemm(GgParams p) {
+// Tile BM x BN, BK reduction steps per stage, WAVES_M x WAVES_N waves, a ring
+// of NBUF stages (stage s in buffer s % NBUF).  TM: 16-position subtiles of
+// the first axis per wave that hold anything.
+template <int KIND, int EPI, int BM, int BN, int BK, int WAVES_M, int WAVES_N, int NBUF, int TM>
+__device__ __forceinline__ void gg_tile(const GgParams& p, const GgTile& t, uint8_t* lds) {
   constexpr int NW = WAVES_M * WAVES_N;
-  constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 16, TN = WN / 16;
-  using OpA = Operand<KIND != MOE_GEMM_TN, BM, BK, NW>;
+  constexpr int WM = TM * 16, WN = BN / WAVES_N, TN = WN / 16;
+  using OpA = Operand<KIND != MOE_GEMM_TN, BM, BK, NW, TM * 16 * WAVES_M>;
   using OpB = Operand<KIND == MOE_GEMM_NT, BN, BK, NW>;
   constexpr int NDMA = OpA::NQ + OpB::NQ, STAGE = OpA::BYTES + OpB::BYTES;
-  static_assert((NBUF - 2) * NDMA < 64, "vmcnt");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[NBUF * STAGE];
-
-  GgTile t;
-  if (!gg_locate<KIND, BM>(p, reinterpret_cast<int*>(lds), t)) return;
+  static_assert((NBUF - 1) * NDMA < 64, "vmcnt");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
@@ -299,7 +435,9 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, MINW) void k_grouped_gemm(G
   // split reduction: stages [kt0, kt0 + KT)
   const int per_split = (KT_all + p.splits - 1) / p.splits;
   const int kt0 = min(t.split * per_split, KT_all);
-  const int KT = min(per_split, KT_all - kt0);
+  const int end = min(red, (kt0 + per_split) * BK);              // reduction steps behind it are zeros
+  int KT = min(per_split, KT_all - kt0);
+  if (BK == 32) KT += KT & 1;                                    // the main loop takes two such stages at a time
 
   OpA a;
   OpB b;
@@ -307,25 +445,25 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, MINW) void k_grouped_gemm(G
     a.init(static_cast<const bf16_t*>(p.A) + t.row0 * p.N, p.N, t.m_off, p.N, [](int) { return 0; });
     b.init(static_cast<const bf16_t*>(p.B) + t.row0 * p.K, p.K, t.nt * BN, p.K, [](int) { return 0; });
   } else {
-    a.init(static_cast<const bf16_t*>(p.A) + t.row0 * p.K, p.K, 0, 0,
-           [&](int r) { return min(t.m_off + r, t.rows - 1); });
+    a.init(static_cast<const bf16_t*>(p.A) + (t.row0 + t.m_off) * p.K, p.K, 0, 0,
+           [&](int r) { return min(r, t.rows - 1 - t.m_off); });
     const int brows = EPI == EPI_SWIGLU ? 2 * p.N : p.N;
     const bf16_t* B = static_cast<const bf16_t*>(p.B) + static_cast<int64_t>(t.e) * brows * p.K;
     if constexpr (KIND == MOE_GEMM_NN)
       b.init(B, p.N, t.nt * BN, p.N, [](int) { return 0; });
     else if constexpr (EPI == EPI_SWIGLU)       // half a tile of gate rows, then the matching up rows
-      b.init(B, p.K, 0, 0, [&](int r) {
-        return min(t.nt * (BN / 2) + r % (BN / 2), p.N - 1) + (r < BN / 2 ? 0 : p.N);
+      b.init(B + static_cast<int64_t>(t.nt * (BN / 2)) * p.K, p.K, 0, 0, [&](int r) {
+        return min(r % (BN / 2), p.N - 1 - t.nt * (BN / 2)) + (r < BN / 2 ? 0 : p.N);
       });
     else
-      b.init(B, p.K, 0, 0, [&](int r) { return min(t.nt * BN + r, p.N - 1); });
+      b.init(B + static_cast<int64_t>(t.nt * BN) * p.K, p.K, 0, 0, [&](int r) { return min(r, p.N - 1 - t.nt * BN); });
   }
   const uint32_t lds0 = static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)(lds)));
   __builtin_amdgcn_s_waitcnt(0);           // from here on only counted DMAs are in flight
   auto issue = [&](int kt) {
     const uint32_t at = lds0 + (kt % NBUF) * STAGE;
-    const int ks = kt0 + kt, left = red - ks * BK;
+    const int ks = kt0 + kt, left = end - ks * BK;
     if (left >= BK) {
       a.issue(at, ks);
       b.issue(at + OpA::BYTES, ks);
@@ -349,60 +487,148 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, MINW) void k_grouped_gemm(G
     else
       return wn * WN + tn * 16;
   };
-  auto compute = [&](int kt) {
-    const uint8_t* sA = lds + (kt % NBUF) * STAGE;
-    const uint8_t* sB = sA + OpA::BYTES;
+  // The reduction advances in steps of 32.  The first operand's fragment of
+  // subtile i is read again, for the next step, as soon as this step's MFMAs
+  // have taken it, and the second operand's fragments of the next step are
+  // read ahead into a second set: LDS reads are spread between the MFMAs and
+  // 192 registers hold a 128 x 64 wave tile.  In a stage's last step half of
+  // the MFMAs run before the barrier that hands the stage's buffer back.
+  constexpr int KK = BK / 32;
+  bf16x8_t af[TM], bfr[2][TN];
+  auto at_a = [&](int kt) { return lds + (kt % NBUF) * STAGE; };
+  auto read_a = [&](int kt, int kk, int i) { af[i] = OpA::frag(at_a(kt), wm * WM + i * 16, kk); };
+  auto read_b = [&](int kt, int kk, int set) {
 #pragma unroll
-    for (int kk = 0; kk < BK / 32; ++kk) {
-      bf16x8_t af[TM], bfr[TN];
+    for (int j = 0; j < TN; ++j) bfr[set][j] = OpB::frag(at_a(kt) + OpA::BYTES, b_pos(j), kk);
+  };
+  auto mfmas = [&](int i, int set) {
 #pragma unroll
-      for (int i = 0; i < TM; ++i) af[i] = OpA::frag(sA, wm * WM + i * 16, kk);
+    for (int j = 0; j < TN; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bfr[set][j], af[i], acc[i][j], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Stage kt, whose first step's fragments of the second operand are in set
+  // `first`.  (The last stage reads a stage that does not exist: bytes of the
+  // ring that nothing uses.)
+  auto stage = [&](int kt, auto first) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j) bfr[j] = OpB::frag(sB, b_pos(j), kk);
+    for (int kk = 0; kk < KK; ++kk) {
+      const int set = (decltype(first)::value + kk) & 1;
+      if (kk + 1 < KK) {
+        read_b(kt, kk + 1, set ^ 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < TM; ++i) {
+          mfmas(i, set);
+          read_a(kt, kk + 1, i);
+        }
+      } else {
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bfr[j], af[i], acc[i][j], 0, 0, 0);
+        for (int i = 0; i < TM / 2; ++i) mfmas(i, set);
+        // this wave's reads of the stage are done, and its DMAs of the next
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wait_stages<NDMA, NBUF - 2>(min(KT - 1, kt + NBUF - 1) - (kt + 1));
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (kt + NBUF < KT) issue(kt + NBUF);
+        read_b(kt + 1, 0, set ^ 1);
+#pragma unroll
+        for (int i = 0; i < TM / 2; ++i) read_a(kt + 1, 0, i);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = TM / 2; i < TM; ++i) {
+          mfmas(i, set);
+          read_a(kt + 1, 0, i);
+        }
+      }
     }
   };
-
-  const int pre = min(NBUF - 1, KT);
-  for (int s = 0; s < pre; ++s) issue(s);
-  wait_stages<NDMA, NBUF - 2>(pre - 1);
-  __syncthreads();
-  for (int kt = 0; kt < KT; ++kt) {
-    if (kt + NBUF - 1 < KT) issue(kt + NBUF - 1);
-    compute(kt);
-    wait_stages<NDMA, NBUF - 2>(min(KT - 1, kt + NBUF - 1) - (kt + 1));
+  if (KT > 0) {
+    const int pre = min(NBUF, KT);
+    for (int s = 0; s < pre; ++s) issue(s);
+    wait_stages<NDMA, NBUF - 1>(pre - 1);
     __syncthreads();
-  }
-
-  const int m_lim = KIND == MOE_GEMM_TN ? p.N : t.rows;
+    read_b(0, 0, 0);
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int m = t.m_off + wm * WM + i * 16 + (lane & 15);
-    if (m >= m_lim) continue;
-    if constexpr (EPI == EPI_SWIGLU) {
-#pragma unroll
-      for (int j = 0; j < TN / 2; ++j) {
-        const int col = t.nt * (BN / 2) + wn * (WN / 2) + j * 16 + (lane >> 4) * 4;
-        if (col < nout) store_swiglu<false>(p, t.row0 + m, col, acc[i][j], acc[i][j + TN / 2]);
-      }
+    for (int i = 0; i < TM; ++i) read_a(0, 0, i);
+    using Set0 = std::integral_constant<int, 0>;
+    using Set1 = std::integral_constant<int, 1>;
+    if constexpr (KK % 2 == 0) {
+#pragma unroll 1
+      for (int kt = 0; kt < KT; ++kt) stage(kt, Set0{});
     } else {
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const int col = t.nt * BN + wn * WN + j * 16 + (lane >> 4) * 4;
-        if (col >= nout) continue;
-        if constexpr (EPI == EPI_SWIGLU_BWD)
-          store_swiglu_bwd<false>(p, t.row0 + m, col, acc[i][j]);
-        else if constexpr (KIND == MOE_GEMM_TN)
-          store_c(p, (static_cast<int64_t>(t.e) * p.N + m) * p.K + col, acc[i][j]);
-        else
-          store_c(p, (t.row0 + m) * p.N + col, acc[i][j]);
+#pragma unroll 1
+      for (int kt = 0; kt < KT; kt += 2) {
+        stage(kt, Set0{});
+        stage(kt + 1, Set1{});
       }
     }
   }
+
+  // Epilogue.  An accumulator lane holds four columns of one of 16 rows, 32
+  // bytes of a bf16 row; the wave turns 16 rows at a time through LDS (16-byte
+  // chunks XORed with the row) so that each lane has eight columns and eight
+  // neighbouring lanes fill a 128-byte line.
+  __syncthreads();                                   // the ring is free
+  float* turn = reinterpret_cast<float*>(lds) + wave * 16 * WN;
+  constexpr int CH = WN / 4;                         // 16-byte chunks of a row
+  constexpr int OUT = EPI == EPI_SWIGLU ? WN / 16 : WN / 8;   // lanes per row
+  auto chunk = [&](int r, int c) { return reinterpret_cast<f32x4_t*>(turn + r * WN + ((c ^ (r & (CH - 1))) << 2)); };
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) *chunk(lane & 15, j * 4 + (lane >> 4)) = acc[i][j];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+    for (int h = 0; h < (16 * OUT + 63) / 64; ++h) {
+      const int r = (h * 64 + lane) / OUT, q = lane % OUT;
+      if (16 * OUT < 64 && r >= 16) continue;
+      const int in = wm * WM + i * 16 + r, m = t.m_off + in;
+      const f32x4_t v0 = *chunk(r, 2 * q), v1 = *chunk(r, 2 * q + 1);
+      if constexpr (EPI == EPI_SWIGLU) {
+        const f32x4_t u0 = *chunk(r, CH / 2 + 2 * q), u1 = *chunk(r, CH / 2 + 2 * q + 1);
+        const int col = t.nt * (BN / 2) + wn * (WN / 2) + q * 8;
+        if (in < t.m_n && col < nout) store_swiglu8(p, t.row0 + m, col, v0, v1, u0, u1);
+      } else {
+        const int col = t.nt * BN + wn * WN + q * 8;
+        if (in < t.m_n && col < nout) {
+          if constexpr (EPI == EPI_SWIGLU_BWD)
+            store_swiglu_bwd8(p, t.row0 + m, col, v0, v1);
+          else if constexpr (KIND == MOE_GEMM_TN)
+            store_c8(p, (static_cast<int64_t>(t.e) * p.N + m) * p.K + col, v0, v1);
+          else
+            store_c8(p, (t.row0 + m) * p.N + col, v0, v1);
+        }
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <int KIND, int EPI, int BM, int BN, int BK, int WAVES_M, int WAVES_N, int NBUF, int TM>
+__device__ __forceinline__ void gg_tile_of(int tm, const GgParams& p, const GgTile& t, uint8_t* lds) {
+  if constexpr (TM == 1) {
+    gg_tile<KIND, EPI, BM, BN, BK, WAVES_M, WAVES_N, NBUF, 1>(p, t, lds);
+  } else {
+    if (tm == TM)
+      gg_tile<KIND, EPI, BM, BN, BK, WAVES_M, WAVES_N, NBUF, TM>(p, t, lds);
+    else
+      gg_tile_of<KIND, EPI, BM, BN, BK, WAVES_M, WAVES_N, NBUF, TM - 1>(tm, p, t, lds);
+  }
+}
+
+template <int KIND, int EPI, int BM, int BN, int BK, int WAVES_M, int WAVES_N, int NBUF, int MINW>
+__global__ __launch_bounds__(WAVES_M * WAVES_N * 64, MINW) void k_grouped_gemm(GgParams p) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[NBUF * (BM + BN) * BK * 2];
+  GgTile t;
+  if (!gg_locate<KIND, BM>(p, reinterpret_cast<int*>(lds), t)) return;
+  constexpr int TM = BM / WAVES_M / 16;
+  if constexpr (KIND == MOE_GEMM_TN)
+    gg_tile<KIND, EPI, BM, BN, BK, WAVES_M, WAVES_N, NBUF, TM>(p, t, lds);
+  else
+    gg_tile_of<KIND, EPI, BM, BN, BK, WAVES_M, WAVES_N, NBUF, TM>((t.m_n + 16 * WAVES_M - 1) / (16 * WAVES_M), p, t, lds);
 }
 
 // ---- fp32 -------------------------------------------------------------------
@@ -496,11 +722,10 @@ __global__ __launch_bounds__(256) void k_grouped_gemm_f32(GgParams p) {
     }
   }
 
-  const int m_lim = KIND == MOE_GEMM_TN ? p.N : t.rows;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int m = t.m_off + wm * 32 + i * 16 + (lane & 15);
-    if (m >= m_lim) continue;
+    const int in = wm * 32 + i * 16 + (lane & 15), m = t.m_off + in;
+    if (in >= t.m_n) continue;
     if constexpr (EPI == EPI_SWIGLU) {
       const int col = t.nt * (BN / 2) + wn * 16 + (lane >> 4) * 4;
       if (col < nout) store_swiglu<true>(p, t.row0 + m, col, acc[i][0], acc[i][1]);
@@ -541,50 +766,57 @@ __global__ __launch_bounds__(256) void k_join_splits(GgParams p, int64_t quads, 
 
 // ---- host -------------------------------------------------------------------
 
-// Parts the reduction is cut into: doubled while the grid has fewer than 256
-// workgroups and each part keeps at least 256 steps, at most 16.
-static int gg_splits(int kind, int E, int64_t cap, int N, int K, int BM, int BN) {
-  int64_t tiles, red;
-  if (kind == MOE_GEMM_TN) {
-    tiles = static_cast<int64_t>(E) * ((N + BM - 1) / BM) * ((K + BN - 1) / BN);
-    red = cap / E;
-  } else {
-    tiles = (cap + BM - 1) / BM * ((N + BN - 1) / BN);
-    red = K;
-  }
-  int S = 1;
-  while (S < 16 && tiles * S < 256 && red / (2 * S) >= 256) S *= 2;
-  return S;
+// Tile and reduction parts of a call, from its sizes alone (the workspace
+// query makes the same choice).
+struct GgPlan { int BM, BN, splits; int64_t tiles; };
+
+static int64_t gg_tiles(int kind, int epi, int E, int64_t cap, bool dense, int N, int K, int BM, int BN) {
+  const int64_t mt = (N + BM - 1) / BM, nt = kind == MOE_GEMM_TN ? (K + BN - 1) / BN
+                                           : epi == EPI_SWIGLU   ? (N + BN / 2 - 1) / (BN / 2)
+                                                                 : (N + BN - 1) / BN;
+  if (kind == MOE_GEMM_TN) return E * ((mt * nt + 7) / 8 * 8);      // each XCD's share of an expert is rounded up
+  return max_row_tiles(cap, E, BM, dense) * nt;
 }
 
-struct GgTileShape { int BM, BN; };
-static GgTileShape gg_shape(int kind, bool f32, int64_t cap, int E) {
-  if (f32) return {64, 64};
-  if (kind == MOE_GEMM_TN) return {128, 128};
-  return {cap / E <= 32 ? 32 : 128, 128};
+static GgPlan gg_plan(int kind, int epi, bool f32, int E, int64_t cap, bool dense, int N, int K) {
+  const int64_t rows = cap / E;                     // of an average expert
+  const int cols = kind == MOE_GEMM_TN ? K : epi == EPI_SWIGLU ? 2 * N : N;
+  GgPlan q{128, 128, 1, 0};
+  if (f32)
+    q.BM = q.BN = 64;
+  else if (kind != MOE_GEMM_TN && rows <= 32)
+    q.BM = 32;
+  else if (cols > 128 && (kind == MOE_GEMM_TN ? N > 128 : rows > 128) &&
+           gg_tiles(kind, epi, E, cap, dense, N, K, 256, 256) >= 256)
+    q.BM = q.BN = 256;
+  q.tiles = gg_tiles(kind, epi, E, cap, dense, N, K, q.BM, q.BN);
+  // The reduction is cut into parts, doubled while the grid has fewer than 256
+  // workgroups and each part keeps at least 256 steps, at most 16.
+  const int64_t red = kind == MOE_GEMM_TN ? rows : K;
+  if (epi == EPI_STORE)
+    while (q.splits < 16 && q.tiles * q.splits < 256 && red / (2 * q.splits) >= 256) q.splits *= 2;
+  return q;
 }
 
 template <int KIND, int EPI>
-static moe_status gg_launch(GgParams& p, bool f32, hipStream_t s) {
-  const GgTileShape ts = gg_shape(KIND, f32, p.cap, p.E);
-  const int cols = KIND == MOE_GEMM_TN ? p.K : EPI == EPI_SWIGLU ? 2 * p.N : p.N;
-  // a SwiGLU tile holds BN / 2 gate columns and the matching up columns
-  p.n_tiles = EPI == EPI_SWIGLU ? (p.N + ts.BN / 2 - 1) / (ts.BN / 2) : (cols + ts.BN - 1) / ts.BN;
-  p.m_tiles = (p.N + ts.BM - 1) / ts.BM;
-  const int64_t tiles = KIND == MOE_GEMM_TN ? static_cast<int64_t>(p.E) * p.m_tiles * p.n_tiles
-                                            : max_row_tiles(p.cap, p.E, ts.BM, p.offsets == nullptr) * p.n_tiles;
-  if (gemm_grid(tiles) >= (1 << 24)) return MOE_ERR_UNSUPPORTED;      // 256 threads each, 2^32 in a grid
-  const dim3 grid(static_cast<unsigned>(gemm_grid(tiles)), p.splits);
+static moe_status gg_launch(GgParams& p, const GgPlan& q, bool f32, hipStream_t s) {
+  const int cols = KIND == MOE_GEMM_TN ? p.K : p.N, width = EPI == EPI_SWIGLU ? q.BN / 2 : q.BN;
+  p.n_tiles = (cols + width - 1) / width;
+  p.m_tiles = (p.N + q.BM - 1) / q.BM;
+  p.splits = q.splits;
+  if (gemm_grid(q.tiles) >= (1 << 23)) return MOE_ERR_UNSUPPORTED;      // at most 512 threads each, 2^32 in a grid
+  const dim3 grid(static_cast<unsigned>(gemm_grid(q.tiles)), q.splits);
   if (f32) {
     hipLaunchKernelGGL((k_grouped_gemm_f32<KIND, EPI>), grid, dim3(256), 0, s, p);
-  } else if (ts.BM == 32) {
-    if constexpr (KIND != MOE_GEMM_TN)
-      hipLaunchKernelGGL((k_grouped_gemm<KIND, EPI, 32, 128, 64, 1, 4, 3, 2>), grid, dim3(256), 0, s, p);
-  } else {
+  } else if (q.BM == 256) {
+    hipLaunchKernelGGL((k_grouped_gemm<KIND, EPI, 256, 256, 64, 2, 4, 2, 2>), grid, dim3(512), 0, s, p);
+  } else if (q.BM == 128) {
     hipLaunchKernelGGL((k_grouped_gemm<KIND, EPI, 128, 128, 64, 2, 2, 2, 2>), grid, dim3(256), 0, s, p);
+  } else if constexpr (KIND != MOE_GEMM_TN) {
+    hipLaunchKernelGGL((k_grouped_gemm<KIND, EPI, 32, 128, 64, 1, 4, 3, 2>), grid, dim3(256), 0, s, p);
   }
   DBOMOE_CHECK_LAUNCH();
-  if (p.splits > 1) {
+  if (q.splits > 1) {
     const int64_t elems = KIND == MOE_GEMM_TN ? static_cast<int64_t>(p.E) * p.N * p.K : p.cap * p.N;
     const int64_t blocks = (elems / 4 + 255) / 256;
     hipLaunchKernelGGL(k_join_splits, dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, p,
@@ -599,27 +831,22 @@ static moe_status gg_check(moe_dtype ab, const int32_t* offsets, int32_t E_loc, 
   if (E_loc < 1 || E_loc > 256 || cap_rows < 0 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
   if (!offsets && E_loc != 1) return MOE_ERR_INVALID_ARG;
   if (ab != MOE_F32 && ab != MOE_BF16) return MOE_ERR_UNSUPPORTED;
-  if (cap_rows > (1 << 30) || N > (1 << 24) || K > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  if (cap_rows > (1 << 30) || N > (1 << 22) || K > (1 << 22)) return MOE_ERR_UNSUPPORTED;
   const int q = ab == MOE_F32 ? 4 : 8;        // rows start on 16 bytes
   if (N % q || K % q) return MOE_ERR_MISALIGNED;
   if (offsets && !aligned16(offsets)) return MOE_ERR_MISALIGNED;
   return MOE_OK;
 }
 
-static int gg_call_splits(int kind, moe_dtype ab, int32_t E_loc, int64_t cap_rows, int32_t N, int32_t K) {
-  const GgTileShape ts = gg_shape(kind, ab == MOE_F32, cap_rows, E_loc);
-  return gg_splits(kind, E_loc, cap_rows, N, K, ts.BM, ts.BN);
-}
-
 }  // namespace dbomoe
 
 using namespace dbomoe;
 
-extern "C" size_t moe_grouped_gemm_workspace_size(moe_gemm_kind kind, moe_dtype ab, int32_t E_loc, int64_t cap_rows,
-                                                  int32_t N, int32_t K) {
+extern "C" size_t moe_grouped_gemm_workspace_size(moe_gemm_kind kind, moe_dtype ab, int32_t dense, int32_t E_loc,
+                                                  int64_t cap_rows, int32_t N, int32_t K) {
   if (kind != MOE_GEMM_NT && kind != MOE_GEMM_NN && kind != MOE_GEMM_TN) return 0;
   if (E_loc < 1 || E_loc > 256 || cap_rows < 1 || N < 1 || K < 1) return 0;
-  const int S = gg_call_splits(kind, ab, E_loc, cap_rows, N, K);
+  const int S = gg_plan(kind, EPI_STORE, ab == MOE_F32, E_loc, cap_rows, dense != 0, N, K).splits;
   if (S == 1) return 0;
   const size_t out = kind == MOE_GEMM_TN ? static_cast<size_t>(E_loc) * N * K : static_cast<size_t>(cap_rows) * N;
   return align_up(out * 4 * S, 256);
@@ -650,19 +877,19 @@ extern "C" moe_status moe_grouped_gemm(moe_gemm_kind kind, const void* a, const 
   p.K = K;
   p.c_f32 = ct == MOE_F32;
   p.accumulate = accumulate;
-  p.splits = gg_call_splits(kind, ab, E_loc, cap_rows, N, K);
-  if (p.splits > 1) {
+  const bool f32 = ab == MOE_F32;
+  const GgPlan q = gg_plan(kind, EPI_STORE, f32, E_loc, cap_rows, !offsets, N, K);
+  if (q.splits > 1) {
     if (!ws) return MOE_ERR_INVALID_ARG;
     if (!aligned256(ws)) return MOE_ERR_MISALIGNED;
-    if (ws_bytes < moe_grouped_gemm_workspace_size(kind, ab, E_loc, cap_rows, N, K)) return MOE_ERR_WORKSPACE;
+    if (ws_bytes < moe_grouped_gemm_workspace_size(kind, ab, !offsets, E_loc, cap_rows, N, K)) return MOE_ERR_WORKSPACE;
     p.part = static_cast<float*>(ws);
     p.part_stride = tn ? static_cast<int64_t>(E_loc) * N * K : cap_rows * N;
   }
-  const bool f32 = ab == MOE_F32;
   const hipStream_t s = as_stream(stream);
-  if (kind == MOE_GEMM_NT) return gg_launch<MOE_GEMM_NT, EPI_STORE>(p, f32, s);
-  if (kind == MOE_GEMM_NN) return gg_launch<MOE_GEMM_NN, EPI_STORE>(p, f32, s);
-  return gg_launch<MOE_GEMM_TN, EPI_STORE>(p, f32, s);
+  if (kind == MOE_GEMM_NT) return gg_launch<MOE_GEMM_NT, EPI_STORE>(p, q, f32, s);
+  if (kind == MOE_GEMM_NN) return gg_launch<MOE_GEMM_NN, EPI_STORE>(p, q, f32, s);
+  return gg_launch<MOE_GEMM_TN, EPI_STORE>(p, q, f32, s);
 }
 
 extern "C" moe_status moe_grouped_swiglu(const void* x_perm, const void* w13, moe_dtype act, const int32_t* offsets,
@@ -672,6 +899,8 @@ extern "C" moe_status moe_grouped_swiglu(const void* x_perm, const void* w13, mo
   if (st != MOE_OK) return st;
   if (cap_rows == 0) return MOE_OK;
   if (!x_perm || !w13 || !h) return MOE_ERR_INVALID_ARG;
+  // the up rows are addressed by 32-bit byte offsets from the gate rows
+  if ((static_cast<int64_t>(I) + 256) * H * 2 >= (int64_t{1} << 32)) return MOE_ERR_UNSUPPORTED;
   if (h == x_perm || h == w13 || h == gu || (gu && (gu == x_perm || gu == w13))) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x_perm) || !aligned16(w13) || !aligned16(h) || (gu && !aligned16(gu))) return MOE_ERR_MISALIGNED;
   GgParams p{};
@@ -684,8 +913,8 @@ extern "C" moe_status moe_grouped_swiglu(const void* x_perm, const void* w13, mo
   p.cap = cap_rows;
   p.N = I;
   p.K = H;
-  p.splits = 1;
-  return gg_launch<MOE_GEMM_NT, EPI_SWIGLU>(p, act == MOE_F32, as_stream(stream));
+  const GgPlan q = gg_plan(MOE_GEMM_NT, EPI_SWIGLU, act == MOE_F32, E_loc, cap_rows, !offsets, I, H);
+  return gg_launch<MOE_GEMM_NT, EPI_SWIGLU>(p, q, act == MOE_F32, as_stream(stream));
 }
 
 extern "C" moe_status moe_grouped_swiglu_backward(const void* dy_perm, const void* w2, const void* gu, moe_dtype act,
@@ -707,6 +936,6 @@ extern "C" moe_status moe_grouped_swiglu_backward(const void* dy_perm, const voi
   p.cap = cap_rows;
   p.N = I;
   p.K = H;
-  p.splits = 1;
-  return gg_launch<MOE_GEMM_NN, EPI_SWIGLU_BWD>(p, act == MOE_F32, as_stream(stream));
+  const GgPlan q = gg_plan(MOE_GEMM_NN, EPI_SWIGLU_BWD, act == MOE_F32, E_loc, cap_rows, !offsets, I, H);
+  return gg_launch<MOE_GEMM_NN, EPI_SWIGLU_BWD>(p, q, act == MOE_F32, as_stream(stream));
 }

@@ -294,13 +294,15 @@ moe_status moe_combine(const void* y_perm, moe_dtype act, int64_t T, int32_t H, 
  *                b [cap_rows, K], c [E_loc, N, K]: the gradient of its weights
  *   ab   MOE_BF16 or MOE_F32 (a and b); ct MOE_F32, or MOE_BF16 with ab bf16
  *   accumulate  0: c = product; 1: c = c + product, rounded once
- *   ws   moe_grouped_gemm_workspace_size(...) bytes of the same arguments (fp32
- *        partial products where the output has few tiles and the reduction is
- *        long; 0 bytes otherwise, then ws may be NULL)
+ *   ws   moe_grouped_gemm_workspace_size(...) bytes of the same arguments
+ *        (dense: 1 if offsets is NULL): fp32 partial products where the output
+ *        has few tiles and the reduction is long; 0 bytes otherwise, then ws
+ *        may be NULL
  * Sums are fp32, rounded once to ct, and do not depend on timing.  NT / NN
  * leave c's rows outside the experts' ranges untouched; TN writes zeros for an
  * expert without rows (accumulate: leaves it as it is).  N and K are multiples
- * of 8 (bf16) or 4 (fp32), else MOE_ERR_MISALIGNED.  E_loc <= 256.  c must not
+ * of 8 (bf16) or 4 (fp32), else MOE_ERR_MISALIGNED, and at most 2^22.
+ * E_loc <= 256.  c must not
  * overlap a, b or ws.
  *
  * moe_grouped_swiglu - the NT product with w13 [E_loc, 2I, H] (gate rows over
@@ -317,8 +319,8 @@ moe_status moe_combine(const void* y_perm, moe_dtype act, int64_t T, int32_t H, 
  * moe_grouped_gemm for offsets, rows, sizes and alignment.
  * ------------------------------------------------------------------------- */
 typedef enum { MOE_GEMM_NT = 0, MOE_GEMM_NN = 1, MOE_GEMM_TN = 2 } moe_gemm_kind;
-size_t moe_grouped_gemm_workspace_size(moe_gemm_kind kind, moe_dtype ab, int32_t E_loc, int64_t cap_rows,
-                                       int32_t N, int32_t K);
+size_t moe_grouped_gemm_workspace_size(moe_gemm_kind kind, moe_dtype ab, int32_t dense, int32_t E_loc,
+                                       int64_t cap_rows, int32_t N, int32_t K);
 moe_status moe_grouped_gemm(moe_gemm_kind kind, const void* a, const void* b, moe_dtype ab,
                             const int32_t* offsets, int32_t E_loc, int64_t cap_rows, int32_t N, int32_t K,
                             void* c, moe_dtype ct, int32_t accumulate, void* ws, size_t ws_bytes,

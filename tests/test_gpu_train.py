@@ -127,6 +127,76 @@ def test_grouped_gemm_weights(name, dt):
             check(c, ref, mag, max(counts), "weight gradient")
 
 
+# Enough and large enough experts for the 256 x 256 tiles: row counts around
+# one, two and several tiles, odd widths, reductions that end inside a stage.
+BIG = [0, 1, 15, 16, 17, 31, 33, 255, 256, 257, 511, 513, 700, 1030, 2049] + [(i * 97) % 331 for i in range(45)]
+
+
+def _ref_rows(kind, a, b, counts):
+    ref = torch.zeros(a.shape[0], b.shape[1] if kind == "nt" else b.shape[2], dtype=torch.float64)
+    mag = ref.clone()
+    for e, r in spans(counts):
+        w = b[e].double().T if kind == "nt" else b[e].double()
+        ref[r], mag[r] = a[r].double() @ w, a[r].double().abs() @ w.abs()
+    return ref, mag
+
+
+@pytest.mark.parametrize("N,K", [(520, 72), (1032, 200), (264, 328)])
+@pytest.mark.parametrize("kind", ["nt", "nn", "tn"])
+def test_grouped_gemm_large_tiles(kind, N, K):
+    B = _B()
+    g = torch.Generator().manual_seed(N + K)
+    M, off = sum(BIG), offsets_of(BIG).cuda()
+    for out, acc in ((BF, False), (F32, True)):
+        print(f"{kind} large N={N} K={K} {out}", flush=True)
+        a = rnd(g, M + 2, N if kind == "tn" else K, dt=BF)
+        a[M:] = math.nan
+        if kind == "tn":
+            b, c0 = rnd(g, M + 2, K, dt=BF), rnd(g, len(BIG), N, K, dt=out)
+            b[M:] = math.nan
+            ref, mag = torch.zeros(c0.shape, dtype=torch.float64), torch.zeros(c0.shape, dtype=torch.float64)
+            for e, r in spans(BIG):
+                ref[e] = a[r].double().T @ b[r].double()
+                mag[e] = a[r].double().abs().T @ b[r].double().abs()
+        else:
+            b, c0 = rnd(g, len(BIG), *((N, K) if kind == "nt" else (K, N)), dt=BF), rnd(g, M + 2, N, dt=out)
+            ref, mag = _ref_rows(kind, a[:M], b, BIG)
+        c = c0.cuda()
+        ac, bc = a.cuda(), b.cuda()
+        ws = torch.empty(B.moe_grouped_gemm_workspace_size(kind, ac, bc, off, c), dtype=torch.uint8, device="cuda")
+        B.moe_grouped_gemm(kind, ac, bc, off, c, ws, accumulate=acc)
+        n = len(ref)
+        if acc:
+            ref, mag = ref + c0[:n].double(), mag + c0[:n].double().abs()
+        check(c[:n], ref, mag, max(BIG) if kind == "tn" else K, "large")
+        if kind != "tn":
+            assert torch.equal(c[M:].cpu(), c0[M:])
+
+
+@pytest.mark.parametrize("I,H", [(520, 72), (264, 328)])
+def test_grouped_swiglu_large_tiles(I, H):
+    B = _B()
+    g = torch.Generator().manual_seed(I + H)
+    M, off = sum(BIG), offsets_of(BIG).cuda()
+    x, w13 = rnd(g, M, H, dt=BF), rnd(g, len(BIG), 2 * I, H, dt=BF, std=H ** -0.5)
+    gu, h = torch.zeros(M, 2 * I, dtype=BF, device="cuda"), torch.zeros(M, I, dtype=BF, device="cuda")
+    print(f"swiglu large I={I} H={H}", flush=True)
+    B.moe_grouped_swiglu(x.cuda(), w13.cuda(), off, h, gu=gu)
+    ref, mag = _ref_rows("nt", x, w13, BIG)
+    check(gu, ref, mag, H, "gu")
+    gate, up, mg, mu = ref[:, :I], ref[:, I:], mag[:, :I], mag[:, I:]
+    s = _sigmoid(gate)
+    check(h, gate * s * up, (H + 2) * (1.1 * up.abs() * mg + (gate * s).abs() * mu) + 16 * (gate * s * up).abs(), -1, "h")
+    dy, w2, gu64 = rnd(g, M, H, dt=BF), rnd(g, len(BIG), H, I, dt=BF, std=H ** -0.5), gu.cpu().double()
+    dgu = torch.zeros(M, 2 * I, dtype=BF, device="cuda")
+    B.moe_grouped_swiglu_backward(dy.cuda(), w2.cuda(), gu, off, dgu)
+    dh, mag = _ref_rows("nn", dy, w2, BIG)
+    gate, up = gu64[:, :I], gu64[:, I:]
+    s = _sigmoid(gate)
+    fg, fu = (up * s).abs() * (1 + gate.abs() * (1 - s)), (gate * s).abs()
+    check(dgu, _swiglu_bwd(dh, gu64, I), torch.cat([fg, fu], 1) * ((H + 2) * mag + 16 * dh.abs()).repeat(1, 2), -1, "dgu")
+
+
 def test_grouped_gemm_neighbours_values_stay_out():
     """A row of infinities or NaN spoils its own expert's results only."""
     B = _B()

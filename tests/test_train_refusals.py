@@ -26,7 +26,7 @@ def test_grouped_gemm_refusals():
     for kw in (dict(kind=3), dict(kind=-1), dict(E=0), dict(E=257), dict(cap=-1), dict(N=0), dict(K=0), dict(K=-8),
                dict(off=None), dict(acc=2), dict(a=None), dict(b=None), dict(c=None), dict(c=A), dict(c=2 * A)):
         assert call(**kw) == bad, kw
-    for kw in (dict(ab=2), dict(ct=2), dict(ab=0, ct=1), dict(cap=(1 << 30) + 1), dict(N=(1 << 24) + 8),
+    for kw in (dict(ab=2), dict(ct=2), dict(ab=0, ct=1), dict(cap=(1 << 30) + 1), dict(N=(1 << 22) + 8),
                dict(kind=0, cap=1 << 30, N=1 << 16)):
         assert call(**kw) == B.MOE_ERR_UNSUPPORTED, kw
     for kw in (dict(N=60), dict(K=12), dict(ab=0, ct=0, K=2), dict(a=A + 8), dict(b=2 * A + 2), dict(c=3 * A + 4),
@@ -35,14 +35,14 @@ def test_grouped_gemm_refusals():
     # no rows: nothing to do, for the row products
     assert call(cap=0) == B.MOE_OK and call(kind=1, cap=0) == B.MOE_OK
     # a product that is split needs its workspace
-    need = B.lib().moe_grouped_gemm_workspace_size(2, 1, 1, 8192, 64, 64)
+    need = B.lib().moe_grouped_gemm_workspace_size(2, 1, 1, 1, 8192, 64, 64)
     assert need > 0
     split = dict(kind=2, off=None, E=1, cap=8192)
     assert call(**split) == bad
     assert call(**split, ws=A, n=need - 1) == B.MOE_ERR_WORKSPACE
     assert call(**split, ws=A + 16, n=need) == B.MOE_ERR_MISALIGNED
     # sizes for which there is no product
-    for args in ((3, 1, 1, 8192, 64, 64), (2, 1, 0, 8192, 64, 64), (2, 1, 1, 0, 64, 64), (2, 1, 1, 8192, 0, 64)):
+    for args in ((3, 1, 1, 1, 8192, 64, 64), (2, 1, 0, 0, 8192, 64, 64), (2, 1, 1, 1, 0, 64, 64), (2, 1, 1, 1, 8192, 0, 64)):
         assert B.lib().moe_grouped_gemm_workspace_size(*args) == 0
 
 
