@@ -306,61 +306,95 @@ def moe_combine(y_perm, T, k, inv, topk_w, out, shared_out=None, stream=None):
 
 # ------------------------------------------------------------------ training
 # The calls below check shapes, types and devices, and run on the tensors'
-# device: `stream` defaults to that device's current stream.
+# device: `stream` defaults to that device's current stream.  A decode-sized
+# call takes the GPU less time than these checks took with torch.device and
+# torch.cuda.Stream objects, so devices are compared by number and the stream
+# is taken as a raw handle.
 
 def _need(ok, what: str):
     if not ok:
         raise ValueError(what)
 
 
-def _same_device(*ts):
-    d = ts[0].device
-    for t in ts[1:]:
-        if t is not None and t.device != d:
-            raise ValueError(f"tensors on {d} and {t.device}")
+def _device(t) -> int:
+    d = t.get_device()
+    if d < 0:
+        raise ValueError("expected a device tensor")
     return d
 
 
-def _call(fn: str, device, stream, *args):
-    f = getattr(lib(), fn)
-    if device.index == torch.cuda.current_device():
-        _check(f(*args, stream_handle(stream)), fn)
+def _ptr(d: int, t):
+    """Address of a contiguous tensor on device d; None stays None."""
+    if t is None:
+        return None
+    if t.get_device() != d:
+        raise ValueError("expected a device tensor" if not t.is_cuda else "tensors on different devices")
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(fn: str, d: int, stream, *args):
+    f = getattr(_LIB or lib(), fn)
+    if d == torch.cuda.current_device():
+        h = stream.cuda_stream if stream is not None else _raw_stream(d) if _raw_stream else stream_handle()
+        st = f(*args, h)
     else:
-        with torch.cuda.device(device):
-            _check(f(*args, stream_handle(stream)), fn)
+        with torch.cuda.device(d):
+            st = f(*args, stream_handle(stream))
+    if st != MOE_OK:
+        raise MoEError(st, fn)
+
+
+_CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.uint8: MOE_FP8_E4M3FN,
+          torch.float8_e4m3fn: MOE_FP8_E4M3FN}
+
+
+def _code(dtype) -> int:
+    c = _CODES.get(dtype)
+    if c is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return c
 
 
 def _groups(offsets, experts: int) -> int:
     """E_loc of a grouped call: offsets [E_loc + 1] int32, or None for one dense group."""
     if offsets is None:
+        if experts != 1:
+            raise ValueError("offsets None: one group")
         return 1
-    _need(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.numel() == experts + 1,
-          f"offsets: expected int32 [{experts + 1}]")
+    if offsets.dtype != torch.int32 or offsets.shape != (experts + 1,):
+        raise ValueError(f"offsets: expected int32 [{experts + 1}]")
     return experts
 
 
 def _gemm_sizes(kind: str, a, b, offsets, c):
     """(kind code, E_loc, cap_rows, N, K) of a moe_grouped_gemm call, shapes and types checked."""
-    _need(kind in GEMM_KINDS, f"kind: one of {sorted(GEMM_KINDS)}")
-    _need(a.dim() == 2 and a.dtype == b.dtype, "a: a 2-d tensor of b's type")
-    cap = a.shape[0]
-    if kind == "tn":
-        _need(b.dim() == 2 and b.shape[0] == cap and c.dim() == 3, "tn: a [rows, N], b [rows, K], c [E, N, K]")
-        E, N, K = c.shape
-        _need(a.shape[1] == N and b.shape[1] == K, "tn: a [rows, N], b [rows, K], c [E, N, K]")
+    code, sa, sb, sc = GEMM_KINDS.get(kind), a.shape, b.shape, c.shape
+    if code is None:
+        raise ValueError(f"kind: one of {sorted(GEMM_KINDS)}")
+    if a.dtype != b.dtype or len(sa) != 2:
+        raise ValueError("a: a 2-d tensor of b's type")
+    if code == MOE_GEMM_TN:
+        if len(sc) != 3 or sa != (sa[0], sc[1]) or sb != (sa[0], sc[2]):
+            raise ValueError("tn: a [rows, N], b [rows, K], c [E, N, K]")
+        E, N, K = sc
     else:
-        _need(b.dim() == 3 and c.dim() == 2 and c.shape[0] == cap, f"{kind}: a [rows, K], b of 3 axes, c [rows, N]")
-        E, N, K = b.shape[0], c.shape[1], a.shape[1]
-        _need(tuple(b.shape[1:]) == ((N, K) if kind == "nt" else (K, N)), f"{kind}: b [E, N, K] (nt) or [E, K, N] (nn)")
-    if offsets is None:
-        _need(E == 1, "offsets None: one group")
-    return GEMM_KINDS[kind], _groups(offsets, E), cap, N, K
+        if len(sb) != 3 or len(sc) != 2 or sc[0] != sa[0]:
+            raise ValueError(f"{kind}: a [rows, K], b of 3 axes, c [rows, N]")
+        E, N, K = sb[0], sc[1], sa[1]
+        if (sb[1], sb[2]) != ((N, K) if code == MOE_GEMM_NT else (K, N)):
+            raise ValueError(f"{kind}: b [E, N, K] (nt) or [E, K, N] (nn)")
+    return code, _groups(offsets, E), sa[0], N, K
 
 
 def moe_grouped_gemm_workspace_size(kind: str, a, b, offsets, c) -> int:
     """Bytes of workspace of moe_grouped_gemm on these tensors (0: none needed)."""
     code, E, cap, N, K = _gemm_sizes(kind, a, b, offsets, c)
-    return lib().moe_grouped_gemm_workspace_size(code, dtype_code(a), int(offsets is None), E, cap, N, K)
+    return lib().moe_grouped_gemm_workspace_size(code, _code(a.dtype), int(offsets is None), E, cap, N, K)
 
 
 def moe_grouped_gemm(kind: str, a, b, offsets, c, ws=None, accumulate=False, stream=None):
@@ -370,60 +404,70 @@ def moe_grouped_gemm(kind: str, a, b, offsets, c, ws=None, accumulate=False, str
     "tn": c [E, N, K] = a[rows of e]^T b[rows of e], a [rows, N], b [rows, K].
     offsets None: one group of all rows.  accumulate: c += product."""
     code, E, cap, N, K = _gemm_sizes(kind, a, b, offsets, c)
-    d = _same_device(a, b, c, offsets, ws)
-    _call("moe_grouped_gemm", d, stream, code, ptr(a), ptr(b), dtype_code(a), ptr(offsets), E, cap, N, K, ptr(c),
-          dtype_code(c), int(bool(accumulate)), ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+    d = _device(a)
+    _call("moe_grouped_gemm", d, stream, code, _ptr(d, a), _ptr(d, b), _code(a.dtype), _ptr(d, offsets), E, cap, N, K,
+          _ptr(d, c), _code(c.dtype), 1 if accumulate else 0, _ptr(d, ws), 0 if ws is None else ws.nbytes)
 
 
 def moe_grouped_swiglu(x_perm, w13, offsets, h, gu=None, stream=None):
     """h [rows, I] = silu(x g^T) * (x u^T) with w13 [E, 2I, H]; gu [rows, 2I] (optional) gets the pre-activations."""
     rows, H = x_perm.shape
     E, I = w13.shape[0], h.shape[1]
-    _need(tuple(w13.shape) == (E, 2 * I, H) and h.shape[0] == rows, "w13 [E, 2I, H], h [rows, I]")
-    _need(gu is None or tuple(gu.shape) == (rows, 2 * I), "gu [rows, 2I]")
-    _need(x_perm.dtype == w13.dtype == h.dtype and (gu is None or gu.dtype == h.dtype), "one type for every tensor")
-    _need(offsets is not None or E == 1, "offsets None: one group")
-    d = _same_device(x_perm, w13, h, gu, offsets)
-    _call("moe_grouped_swiglu", d, stream, ptr(x_perm), ptr(w13), dtype_code(x_perm), ptr(offsets),
-          _groups(offsets, E), rows, H, I, ptr(gu), ptr(h))
+    if w13.shape != (E, 2 * I, H) or h.shape != (rows, I) or (gu is not None and gu.shape != (rows, 2 * I)):
+        raise ValueError("w13 [E, 2I, H], h [rows, I], gu [rows, 2I]")
+    t = x_perm.dtype
+    if w13.dtype != t or h.dtype != t or (gu is not None and gu.dtype != t):
+        raise ValueError("one type for every tensor")
+    d = _device(x_perm)
+    _call("moe_grouped_swiglu", d, stream, _ptr(d, x_perm), _ptr(d, w13), _code(t), _ptr(d, offsets),
+          _groups(offsets, E), rows, H, I, _ptr(d, gu), _ptr(d, h))
 
 
 def moe_grouped_swiglu_backward(dy_perm, w2, gu, offsets, dgu, stream=None):
     """dgu [rows, 2I] from dy_perm [rows, H], w2 [E, H, I] and the pre-activations gu [rows, 2I] (dgu may be gu)."""
     rows, H = dy_perm.shape
     E, I = w2.shape[0], w2.shape[2]
-    _need(w2.shape[1] == H and tuple(gu.shape) == (rows, 2 * I) and gu.shape == dgu.shape,
-          "dy_perm [rows, H], w2 [E, H, I], gu and dgu [rows, 2I]")
-    _need(dy_perm.dtype == w2.dtype == gu.dtype == dgu.dtype, "one type for every tensor")
-    _need(offsets is not None or E == 1, "offsets None: one group")
-    d = _same_device(dy_perm, w2, gu, dgu, offsets)
-    _call("moe_grouped_swiglu_backward", d, stream, ptr(dy_perm), ptr(w2), ptr(gu), dtype_code(dy_perm), ptr(offsets),
-          _groups(offsets, E), rows, H, I, ptr(dgu))
+    if w2.shape != (E, H, I) or gu.shape != (rows, 2 * I) or dgu.shape != (rows, 2 * I):
+        raise ValueError("dy_perm [rows, H], w2 [E, H, I], gu and dgu [rows, 2I]")
+    t = dy_perm.dtype
+    if w2.dtype != t or gu.dtype != t or dgu.dtype != t:
+        raise ValueError("one type for every tensor")
+    d = _device(dy_perm)
+    _call("moe_grouped_swiglu_backward", d, stream, _ptr(d, dy_perm), _ptr(d, w2), _ptr(d, gu), _code(t),
+          _ptr(d, offsets), _groups(offsets, E), rows, H, I, _ptr(d, dgu))
 
 
 def moe_combine_backward(dout, y_perm, inv, topk_w, dy_perm, dtopk_w, stream=None):
     """dy_perm [rows, H] and dtopk_w [T, k] of moe_combine's out [T, H]; inv [T*k], topk_w [T, k] as it took them."""
     T, H = dout.shape
     k, cap = topk_w.shape[1], y_perm.shape[0]
-    _need(y_perm.dim() == 2 and y_perm.shape[1] == H and y_perm.shape == dy_perm.shape, "y_perm and dy_perm [rows, H]")
-    _need(dout.dtype == y_perm.dtype == dy_perm.dtype, "one type for dout, y_perm and dy_perm")
-    _need(topk_w.shape == dtopk_w.shape and topk_w.shape[0] == T and inv.numel() == T * k, "topk_w, dtopk_w, inv: T x k")
-    _need(inv.dtype == torch.int32 and topk_w.dtype == dtopk_w.dtype == torch.float32, "inv int32; weights float32")
-    d = _same_device(dout, y_perm, inv, topk_w, dy_perm, dtopk_w)
-    _call("moe_combine_backward", d, stream, ptr(dout), ptr(y_perm), dtype_code(dout), T, H, k, cap, ptr(inv),
-          ptr(topk_w), ptr(dy_perm), ptr(dtopk_w))
+    if y_perm.shape != (cap, H) or dy_perm.shape != (cap, H):
+        raise ValueError("y_perm and dy_perm [rows, H]")
+    t = dout.dtype
+    if y_perm.dtype != t or dy_perm.dtype != t:
+        raise ValueError("one type for dout, y_perm and dy_perm")
+    if topk_w.shape != (T, k) or dtopk_w.shape != (T, k) or inv.numel() != T * k:
+        raise ValueError("topk_w, dtopk_w, inv: T x k")
+    if inv.dtype != torch.int32 or topk_w.dtype != torch.float32 or dtopk_w.dtype != torch.float32:
+        raise ValueError("inv int32; weights float32")
+    d = _device(dout)
+    _call("moe_combine_backward", d, stream, _ptr(d, dout), _ptr(d, y_perm), _code(t), T, H, k, cap, _ptr(d, inv),
+          _ptr(d, topk_w), _ptr(d, dy_perm), _ptr(d, dtopk_w))
 
 
 def moe_route_backward(logits, topk_ids, dtopk_w, params: moe_route_params, dlogits, stream=None):
     """dlogits [T, E] (float32 or bfloat16) of moe_route_topk's weights, from its logits, ids and dtopk_w [T, k]."""
     T, E = logits.shape
-    _need(E == params.E and tuple(dlogits.shape) == (T, E), "logits and dlogits [T, E] with params.E experts")
-    _need(tuple(topk_ids.shape) == (T, params.k) and dtopk_w.shape == topk_ids.shape, "topk_ids and dtopk_w [T, k]")
-    _need(logits.dtype == dtopk_w.dtype == torch.float32 and topk_ids.dtype == torch.int32,
-          "logits and dtopk_w float32, topk_ids int32")
-    d = _same_device(logits, topk_ids, dtopk_w, dlogits)
-    _call("moe_route_backward", d, stream, ptr(logits), T, ptr(topk_ids), ptr(dtopk_w), ctypes.byref(params),
-          ptr(dlogits), dtype_code(dlogits))
+    k = params.k
+    if E != params.E or dlogits.shape != (T, E):
+        raise ValueError("logits and dlogits [T, E] with params.E experts")
+    if topk_ids.shape != (T, k) or dtopk_w.shape != (T, k):
+        raise ValueError("topk_ids and dtopk_w [T, k]")
+    if logits.dtype != torch.float32 or dtopk_w.dtype != torch.float32 or topk_ids.dtype != torch.int32:
+        raise ValueError("logits and dtopk_w float32, topk_ids int32")
+    d = _device(logits)
+    _call("moe_route_backward", d, stream, _ptr(d, logits), T, _ptr(d, topk_ids), _ptr(d, dtopk_w), params,
+          _ptr(d, dlogits), _code(dlogits.dtype))
 
 
 def adamw_params(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, seed=0) -> moe_adamw_params:
@@ -446,10 +490,11 @@ def moe_adamw_table(params, grads, m, v, m_scale=None, v_scale=None, master=None
     for c in cols:
         _need(c is None or len(c) == n, "lists of one length")
     entries = (moe_adamw_tensor * n)()
-    device = params[0].device
+    d = None
     for i in range(n):
         p, g, mi, vi, ms, vs, ma = (None if c is None else c[i] for c in cols)
         size = p.numel()
+        d = _device(p) if d is None else d
         _need(g.numel() == size and mi.numel() == size and vi.numel() == size and (ma is None or ma.numel() == size),
               f"tensor {i}: sizes differ")
         eight = mi.dtype != torch.float32
@@ -460,22 +505,22 @@ def moe_adamw_table(params, grads, m, v, m_scale=None, v_scale=None, master=None
         if eight:
             _need(ms.dtype == vs.dtype == torch.uint8 and ms.numel() == vs.numel() == (size + 127) // 128,
                   f"tensor {i}: scales uint8 [ceil(n / 128)]")
-        _same_device(params[0], p, g, mi, vi, ms, vs, ma)
-        entries[i] = moe_adamw_tensor(ptr(p), ptr(g), ptr(mi), ptr(vi), ptr(ms), ptr(vs), ptr(ma), size,
-                                      dtype_code(p), dtype_code(g), dtype_code(mi))
-    return AdamWTable(entries, device, cols)
+        entries[i] = moe_adamw_tensor(_ptr(d, p), _ptr(d, g), _ptr(d, mi), _ptr(d, vi), _ptr(d, ms), _ptr(d, vs),
+                                      _ptr(d, ma), size, _CODES[p.dtype], _CODES[g.dtype], _CODES[mi.dtype])
+    return AdamWTable(entries, d, cols)
 
 
 def moe_adamw_step(table: AdamWTable, hp: moe_adamw_params, step, lr_scale=None, grad_scale=None, stream=None):
     """One update of the table's tensors.  step: int32 device scalar, 1 at the first update; lr_scale and grad_scale:
     float32 device scalars or None."""
-    _need(step.dtype == torch.int32 and step.numel() == 1, "step: one int32")
+    if step.dtype != torch.int32 or step.numel() != 1:
+        raise ValueError("step: one int32")
     for s in (lr_scale, grad_scale):
-        _need(s is None or (s.dtype == torch.float32 and s.numel() == 1), "lr_scale, grad_scale: one float32")
-        _need(s is None or s.device == table.device, "lr_scale, grad_scale: on the tensors' device")
-    _need(step.device == table.device, "step: on the tensors' device")
-    _call("moe_adamw_step", table.device, stream, table.entries, len(table.entries), ctypes.byref(hp), ptr(step),
-          ptr(lr_scale), ptr(grad_scale))
+        if s is not None and (s.dtype != torch.float32 or s.numel() != 1):
+            raise ValueError("lr_scale, grad_scale: one float32")
+    d = table.device
+    _call("moe_adamw_step", d, stream, table.entries, len(table.entries), hp, _ptr(d, step), _ptr(d, lr_scale),
+          _ptr(d, grad_scale))
 
 
 class DboContext:

@@ -1,7 +1,7 @@
 // AdamW over many tensors in few launches, for gfx950.
 //   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,  g = grad * grad_scale
 //   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v / (1 - b2^t)) + eps)
-// in fp32, each operation rounded by itself.  HBM-bound: every tensor is read
+// in fp32.  HBM-bound: every tensor is read
 // once and written once.
 //
 // 8-bit states: blocks of 128 consecutive elements hold E4M3 codes and one
@@ -37,16 +37,15 @@ struct AdamTensor {
   float* master;
   int64_t n;
   uint32_t key;                       // 0x85ebca77 * the tensor's number
-  int32_t first;                      // first workgroup
 };
 
 struct AdamArgs {
+  int32_t first[kAdamTensors];        // first workgroup of each tensor; behind the last one INT32_MAX
   AdamTensor t[kAdamTensors];
-  int32_t count;
   int32_t groups;                     // groups of kAdamGroup elements per workgroup
   uint32_t seed;
-  float b1, omb1, b2, omb2, eps;
-  double lr, wd, log_b1, log_b2;
+  float b1, omb1, b2, omb2, eps, lr, lr_wd;
+  double log_b1, log_b2;
   const int32_t* step;
   const float* lr_scale;
   const float* grad_scale;
@@ -65,11 +64,17 @@ __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_ca
 // E8M0 byte -> scale; byte 0 is 2^-127, a denormal.
 __device__ __forceinline__ float e8m0(uint8_t b) { return __uint_as_float(b ? static_cast<uint32_t>(b) << 23 : 0x400000u); }
 
-// max over the 16 lanes that share a block of 128 elements
+template <int N>
+__device__ __forceinline__ float row_rotated(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + N, 0xf, 0xf, true));
+}
+
+// max over the 16 lanes that share a block of 128 elements (one DPP row)
 __device__ __forceinline__ float block_max(float v) {
-#pragma unroll
-  for (int d = 8; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, kWave));
-  return v;
+  v = fmaxf(v, row_rotated<8>(v));
+  v = fmaxf(v, row_rotated<4>(v));
+  v = fmaxf(v, row_rotated<2>(v));
+  return fmaxf(v, row_rotated<1>(v));
 }
 
 __device__ __forceinline__ int block_exponent(float top) {
@@ -78,20 +83,22 @@ __device__ __forceinline__ int block_exponent(float top) {
   return e < -127 ? -127 : e;
 }
 
-// |x| * 2^-e to an E4M3 code by stochastic rounding: floor(value / code step + r / 2^20), r of 20 bits.
-__device__ __forceinline__ uint32_t encode(float x, float inv, uint32_t r, bool keep) {
-  const float y = fabsf(x) * inv;
-  uint32_t c;
-  if (y < 0.015625f)                                      // below 2^-6 the codes are 2^-9 apart
-    c = (static_cast<uint32_t>(y * 536870912.f) + r) >> 20;
-  else
-    c = ((__float_as_uint(y) + r) >> 20) - 960u;
-  c = c > 0x7fu ? 0x7fu : c;                              // infinities and NaN
-  if (keep && y > 0.f && c == 0) c = 1;
-  return c | ((__float_as_uint(x) >> 24) & 0x80u);
+// Eight values (in units of their block's scale) to E4M3 codes by stochastic
+// rounding: floor(value / code step + r / 2^20) with r the upper 20 bits of a
+// random word, which is what v_cvt_sr_fp8_f32 computes (compared with that
+// definition over 2^24 values, denormal codes among them).
+__device__ __forceinline__ uint64_t encode8(const float* y, const uint32_t* r) {
+  int lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_sr_fp8_f32(y[0], static_cast<int>(r[0]), lo, 0);
+  lo = __builtin_amdgcn_cvt_sr_fp8_f32(y[1], static_cast<int>(r[1]), lo, 1);
+  lo = __builtin_amdgcn_cvt_sr_fp8_f32(y[2], static_cast<int>(r[2]), lo, 2);
+  lo = __builtin_amdgcn_cvt_sr_fp8_f32(y[3], static_cast<int>(r[3]), lo, 3);
+  hi = __builtin_amdgcn_cvt_sr_fp8_f32(y[4], static_cast<int>(r[4]), hi, 0);
+  hi = __builtin_amdgcn_cvt_sr_fp8_f32(y[5], static_cast<int>(r[5]), hi, 1);
+  hi = __builtin_amdgcn_cvt_sr_fp8_f32(y[6], static_cast<int>(r[6]), hi, 2);
+  hi = __builtin_amdgcn_cvt_sr_fp8_f32(y[7], static_cast<int>(r[7]), hi, 3);
+  return static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32 | static_cast<uint32_t>(lo);
 }
-
-template <int N> struct Bytes { uint8_t b[N]; };
 
 // 8 elements from index i on; those behind n read as zero.
 template <bool BF16>
@@ -154,14 +161,13 @@ __device__ __forceinline__ uint64_t load8_codes(const uint8_t* base, int64_t i, 
   return v;
 }
 
-__device__ __forceinline__ void store8_codes(uint8_t* base, int64_t i, int64_t n, const uint32_t* c) {
+__device__ __forceinline__ void store8_codes(uint8_t* base, int64_t i, int64_t n, uint64_t q) {
   if (i + 8 <= n) {
-    const uint32_t lo = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, hi = c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24;
-    *reinterpret_cast<uint64_t*>(base + i) = static_cast<uint64_t>(hi) << 32 | lo;
+    *reinterpret_cast<uint64_t*>(base + i) = q;
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (i + j < n) base[i + j] = static_cast<uint8_t>(c[j]);
+      if (i + j < n) base[i + j] = static_cast<uint8_t>(q >> (8 * j));
   }
 }
 
@@ -184,26 +190,22 @@ template <bool EIGHT, int PARAM, bool GRAD_BF16>
 __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
 #pragma clang fp contract(off)
   // this workgroup's tensor: the last whose first workgroup is not behind it
-  int lo = 0, hi = a.count - 1;
-  const int blk = blockIdx.x;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.t[mid].first <= blk)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  const AdamTensor& t = a.t[lo];
+  const int blk = blockIdx.x, lane = threadIdx.x & 63;
+  const int mine = lane < kAdamTensors ? a.first[lane] : 0x7fffffff;
+  const int q = __builtin_amdgcn_readfirstlane(__popcll(__ballot(mine <= blk)) - 1);
+  const int first = __builtin_amdgcn_readlane(mine, q);
+  const AdamTensor& t = a.t[q];
   const int64_t n = t.n;
   const int step = max(*a.step, 1);
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;
-  const double lr = a.lr * (a.lr_scale ? static_cast<double>(*a.lr_scale) : 1.0);
-  const float step_size = static_cast<float>(lr / -expm1(step * a.log_b1));
-  const float rbc2 = static_cast<float>(1.0 / sqrt(-expm1(step * a.log_b2)));
-  const float decay = static_cast<float>(1.0 - lr * a.wd);
+  const float ls = a.lr_scale ? *a.lr_scale : 1.f;
+  // 1 - beta^t; an error of some 2^-24 in these factors moves p by that part of its update only
+  const float step_size = a.lr * ls / -expm1f(static_cast<float>(step * a.log_b1));
+  const float rbc2 = 1.f / sqrtf(-expm1f(static_cast<float>(step * a.log_b2)));
+  const float decay = fmaf(-a.lr_wd, ls, 1.f);
   const uint32_t key0 = mix(mix(a.seed + 0x9e3779b9u * static_cast<uint32_t>(step)) + t.key);
 
-  const int64_t begin = static_cast<int64_t>(blk - t.first) * a.groups * kAdamGroup + threadIdx.x * 8;
+  const int64_t begin = static_cast<int64_t>(blk - first) * a.groups * kAdamGroup + threadIdx.x * 8;
   for (int it = 0; it < a.groups; ++it) {
     const int64_t i = begin + it * kAdamGroup;
     // the 16 lanes of a block of 128 stay together: they meet in block_max
@@ -230,8 +232,8 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
       const float gj = g[j] * gs;
       m[j] = m[j] * a.b1 + gj * a.omb1;
       v[j] = v[j] * a.b2 + (gj * a.omb2) * gj;
-      root[j] = sqrtf(v[j]);
-      p[j] = p[j] * decay - step_size * (m[j] / (root[j] * rbc2 + a.eps));
+      root[j] = __builtin_amdgcn_sqrtf(v[j]);               // off by at most one unit, as the reciprocal
+      p[j] = p[j] * decay - step_size * (m[j] * __builtin_amdgcn_rcpf(root[j] * rbc2 + a.eps));
     }
     uint32_t one[8], two[8];
     if constexpr (EIGHT || PARAM == PARAM_BF16) {
@@ -251,14 +253,15 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
       }
       const int em = block_exponent(block_max(tm)), ev = block_exponent(block_max(tv));
       const float im = pow2f(-em), iv = pow2f(-ev);
-      uint32_t cm[8], cv[8];
+      float ym[8], yv[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        cm[j] = encode(m[j], im, one[j] >> 12, false);
-        cv[j] = encode(root[j], iv, two[j] >> 12, true);
+        ym[j] = m[j] * im;
+        // a nonzero value below the smallest code (2^-9) becomes that code
+        yv[j] = root[j] > 0.f ? fmaxf(root[j] * iv, 0.001953125f) : 0.f;
       }
-      store8_codes(static_cast<uint8_t*>(t.m), i, n, cm);
-      store8_codes(static_cast<uint8_t*>(t.v), i, n, cv);
+      store8_codes(static_cast<uint8_t*>(t.m), i, n, encode8(ym, one));
+      store8_codes(static_cast<uint8_t*>(t.v), i, n, encode8(yv, two));
       if ((threadIdx.x & 15) == 0) {
         t.ms[i >> 7] = static_cast<uint8_t>(em + 127);
         t.vs[i >> 7] = static_cast<uint8_t>(ev + 127);
@@ -303,7 +306,7 @@ extern "C" moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n_
                                      const int32_t* step, const float* lr_scale, const float* grad_scale,
                                      void* stream) {
   if (!hp || n_tensors < 0 || (n_tensors > 0 && !tensors)) return MOE_ERR_INVALID_ARG;
-  if (!(hp->lr >= 0) || !(hp->beta1 >= 0 && hp->beta1 < 1) || !(hp->beta2 >= 0 && hp->beta2 < 1) || !(hp->eps > 0) ||
+  if (!(hp->lr >= 0) || !(hp->beta1 >= 0 && hp->beta1 < 1) || !(hp->beta2 >= 0 && hp->beta2 < 1) || !(hp->eps >= 1.2e-38) ||
       !(hp->weight_decay >= 0) || !isfinite(hp->lr) || !isfinite(hp->eps) || !isfinite(hp->weight_decay))
     return MOE_ERR_INVALID_ARG;
   if (n_tensors == 0) return MOE_OK;
@@ -335,8 +338,8 @@ extern "C" moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n_
   a.b2 = static_cast<float>(hp->beta2);
   a.omb2 = static_cast<float>(1.0 - hp->beta2);
   a.eps = static_cast<float>(hp->eps);
-  a.lr = hp->lr;
-  a.wd = hp->weight_decay;
+  a.lr = static_cast<float>(hp->lr);
+  a.lr_wd = static_cast<float>(hp->lr * hp->weight_decay);
   a.log_b1 = log(hp->beta1);
   a.log_b2 = log(hp->beta2);
   a.step = step;
@@ -349,9 +352,10 @@ extern "C" moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n_
     const bool eight = combo & 1, gbf16 = combo & 2;
     const int kind = combo >> 2;
     int64_t blocks = 0;
-    a.count = 0;
+    int count = 0;
     auto flush = [&]() -> moe_status {
-      if (a.count == 0) return MOE_OK;
+      if (count == 0) return MOE_OK;
+      for (int i = count; i < kAdamTensors; ++i) a.first[i] = 0x7fffffff;
       const unsigned nb = static_cast<unsigned>(blocks);
       if (kind == PARAM_F32)
         eight ? adamw_launch<true, PARAM_F32>(a, gbf16, nb, s) : adamw_launch<false, PARAM_F32>(a, gbf16, nb, s);
@@ -359,7 +363,7 @@ extern "C" moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n_
         eight ? adamw_launch<true, PARAM_BF16>(a, gbf16, nb, s) : adamw_launch<false, PARAM_BF16>(a, gbf16, nb, s);
       else
         eight ? adamw_launch<true, PARAM_MASTER>(a, gbf16, nb, s) : adamw_launch<false, PARAM_MASTER>(a, gbf16, nb, s);
-      a.count = 0;
+      count = 0;
       blocks = 0;
       DBOMOE_CHECK_LAUNCH();
       return MOE_OK;
@@ -370,12 +374,13 @@ extern "C" moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n_
       if (t.n == 0 || tk != kind || (t.state_dtype == MOE_FP8_E4M3FN) != eight || (t.grad_dtype == MOE_BF16) != gbf16)
         continue;
       const int64_t per = static_cast<int64_t>(a.groups) * kAdamGroup, nb = (t.n + per - 1) / per;
-      if (a.count == kAdamTensors || blocks + nb >= (1 << 24)) {
+      if (count == kAdamTensors || blocks + nb >= (1 << 24)) {
         const moe_status st = flush();
         if (st != MOE_OK) return st;
       }
-      a.t[a.count++] = AdamTensor{t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.master, t.n,
-                                  0x85ebca77u * static_cast<uint32_t>(i), static_cast<int32_t>(blocks)};
+      a.first[count] = static_cast<int32_t>(blocks);
+      a.t[count++] = AdamTensor{t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.master, t.n,
+                                0x85ebca77u * static_cast<uint32_t>(i)};
       blocks += nb;
     }
     const moe_status st = flush();

@@ -254,29 +254,13 @@ __device__ __forceinline__ void store8(void* base, int64_t i, const f32x4_t& a, 
       u32x4_t{cvt_bf16x2(a[0], a[1]), cvt_bf16x2(a[2], a[3]), cvt_bf16x2(b[0], b[1]), cvt_bf16x2(b[2], b[3])};
 }
 
-__device__ __forceinline__ void load8(const void* base, int64_t i, f32x4_t& a, f32x4_t& b) {
-  const u32x4_t v = *reinterpret_cast<const u32x4_t*>(static_cast<const bf16_t*>(base) + i);
+__device__ __forceinline__ void unpack8(const u32x4_t& v, f32x4_t& a, f32x4_t& b) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     a[2 * k] = __uint_as_float(v[k] << 16);
     a[2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
     b[2 * k] = __uint_as_float(v[2 + k] << 16);
     b[2 * k + 1] = __uint_as_float(v[2 + k] & 0xffff0000u);
-  }
-}
-
-__device__ __forceinline__ void store_c8(const GgParams& p, int64_t i, f32x4_t a, f32x4_t b) {
-  if (p.part || p.c_f32) {
-    store_c(p, i, a);
-    store_c(p, i + 4, b);
-  } else {
-    if (p.accumulate) {
-      f32x4_t c, d;
-      load8(p.C, i, c, d);
-      a += c;
-      b += d;
-    }
-    store8(p.C, i, a, b);
   }
 }
 
@@ -296,11 +280,11 @@ __device__ __forceinline__ void store_swiglu8(const GgParams& p, int64_t row, in
 }
 
 __device__ __forceinline__ void store_swiglu_bwd8(const GgParams& p, int64_t row, int col, const f32x4_t& d0,
-                                                  const f32x4_t& d1) {
+                                                  const f32x4_t& d1, const u32x4_t& gate, const u32x4_t& up) {
   const int64_t gi = row * 2 * p.N + col;
   f32x4_t g[2], u[2], dg[2], du[2];
-  load8(p.gu, gi, g[0], g[1]);
-  load8(p.gu, gi + p.N, u[0], u[1]);
+  unpack8(gate, g[0], g[1]);
+  unpack8(up, u[0], u[1]);
 #pragma unroll
   for (int k = 0; k < 2; ++k) swiglu_bwd(k ? d1 : d0, g[k], u[k], dg[k], du[k]);
   store8(p.C, gi, dg[0], dg[1]);
@@ -568,11 +552,50 @@ __device__ __forceinline__ void gg_tile(const GgParams& p, const GgTile& t, uint
   // Epilogue.  An accumulator lane holds four columns of one of 16 rows, 32
   // bytes of a bf16 row; the wave turns 16 rows at a time through LDS (16-byte
   // chunks XORed with the row) so that each lane has eight columns and eight
-  // neighbouring lanes fill a 128-byte line.
-  __syncthreads();                                   // the ring is free
-  float* turn = reinterpret_cast<float*>(lds) + wave * 16 * WN;
+  // neighbouring lanes fill a 128-byte line.  What the epilogue reads (gu, or
+  // C to add to) is loaded four groups of rows ahead.
   constexpr int CH = WN / 4;                         // 16-byte chunks of a row
   constexpr int OUT = EPI == EPI_SWIGLU ? WN / 16 : WN / 8;   // lanes per row
+  constexpr int HN = (16 * OUT + 63) / 64;           // passes of the wave over 16 rows
+  constexpr int AHEAD = TM < 4 ? TM : 4;
+  const bool reads = EPI == EPI_SWIGLU_BWD || (EPI == EPI_STORE && p.accumulate && !p.part);
+  u32x4_t old[AHEAD][HN][2];
+  struct At { int in, q; int64_t row; int col; bool ok; };
+  auto at = [&](int i, int h) {
+    At x;
+    const int r = (h * 64 + lane) / OUT;
+    x.q = lane % OUT;
+    x.in = r;
+    const int in = wm * WM + i * 16 + r;
+    x.row = KIND == MOE_GEMM_TN ? static_cast<int64_t>(t.e) * p.N + t.m_off + in : t.row0 + t.m_off + in;
+    x.col = EPI == EPI_SWIGLU ? t.nt * (BN / 2) + wn * (WN / 2) + x.q * 8 : t.nt * BN + wn * WN + x.q * 8;
+    x.ok = r < 16 && in < t.m_n && x.col < nout;
+    return x;
+  };
+  auto read_old = [&](int i) {
+#pragma unroll
+    for (int h = 0; h < HN; ++h) {
+      const At x = at(i, h);
+      if (!x.ok) continue;
+      if constexpr (EPI == EPI_SWIGLU_BWD) {
+        const bf16_t* g = static_cast<const bf16_t*>(p.gu) + x.row * 2 * p.N + x.col;
+        old[i % AHEAD][h][0] = *reinterpret_cast<const u32x4_t*>(g);
+        old[i % AHEAD][h][1] = *reinterpret_cast<const u32x4_t*>(g + p.N);
+      } else if (p.c_f32) {
+        const u32x4_t* c = reinterpret_cast<const u32x4_t*>(static_cast<const float*>(p.C) + x.row * nout + x.col);
+        old[i % AHEAD][h][0] = c[0];
+        old[i % AHEAD][h][1] = c[1];
+      } else {
+        old[i % AHEAD][h][0] = *reinterpret_cast<const u32x4_t*>(static_cast<const bf16_t*>(p.C) + x.row * nout + x.col);
+      }
+    }
+  };
+  if (reads) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) read_old(i);
+  }
+  __syncthreads();                                   // the ring is free
+  float* turn = reinterpret_cast<float*>(lds) + wave * 16 * WN;
   auto chunk = [&](int r, int c) { return reinterpret_cast<f32x4_t*>(turn + r * WN + ((c ^ (r & (CH - 1))) << 2)); };
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
@@ -582,27 +605,41 @@ __device__ __forceinline__ void gg_tile(const GgParams& p, const GgTile& t, uint
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll
-    for (int h = 0; h < (16 * OUT + 63) / 64; ++h) {
-      const int r = (h * 64 + lane) / OUT, q = lane % OUT;
-      if (16 * OUT < 64 && r >= 16) continue;
-      const int in = wm * WM + i * 16 + r, m = t.m_off + in;
-      const f32x4_t v0 = *chunk(r, 2 * q), v1 = *chunk(r, 2 * q + 1);
+    for (int h = 0; h < HN; ++h) {
+      const At x = at(i, h);
+      if (!x.ok) continue;
+      f32x4_t v0 = *chunk(x.in, 2 * x.q), v1 = *chunk(x.in, 2 * x.q + 1);
+      const u32x4_t* o = old[i % AHEAD][h];
       if constexpr (EPI == EPI_SWIGLU) {
-        const f32x4_t u0 = *chunk(r, CH / 2 + 2 * q), u1 = *chunk(r, CH / 2 + 2 * q + 1);
-        const int col = t.nt * (BN / 2) + wn * (WN / 2) + q * 8;
-        if (in < t.m_n && col < nout) store_swiglu8(p, t.row0 + m, col, v0, v1, u0, u1);
+        const f32x4_t u0 = *chunk(x.in, CH / 2 + 2 * x.q), u1 = *chunk(x.in, CH / 2 + 2 * x.q + 1);
+        store_swiglu8(p, x.row, x.col, v0, v1, u0, u1);
+      } else if constexpr (EPI == EPI_SWIGLU_BWD) {
+        store_swiglu_bwd8(p, x.row, x.col, v0, v1, o[0], o[1]);
       } else {
-        const int col = t.nt * BN + wn * WN + q * 8;
-        if (in < t.m_n && col < nout) {
-          if constexpr (EPI == EPI_SWIGLU_BWD)
-            store_swiglu_bwd8(p, t.row0 + m, col, v0, v1);
-          else if constexpr (KIND == MOE_GEMM_TN)
-            store_c8(p, (static_cast<int64_t>(t.e) * p.N + m) * p.K + col, v0, v1);
-          else
-            store_c8(p, (t.row0 + m) * p.N + col, v0, v1);
+        const int64_t at_c = x.row * nout + x.col;
+        if (p.part) {
+          float* part = p.part + static_cast<int64_t>(blockIdx.y) * p.part_stride;
+          store4<true>(part, at_c, v0);
+          store4<true>(part, at_c + 4, v1);
+        } else if (p.c_f32) {
+          if (reads) {
+            v0 += __builtin_bit_cast(f32x4_t, o[0]);
+            v1 += __builtin_bit_cast(f32x4_t, o[1]);
+          }
+          store4<true>(p.C, at_c, v0);
+          store4<true>(p.C, at_c + 4, v1);
+        } else {
+          if (reads) {
+            f32x4_t c0, c1;
+            unpack8(o[0], c0, c1);
+            v0 += c0;
+            v1 += c1;
+          }
+          store8(p.C, at_c, v0, v1);
         }
       }
     }
+    if (reads && i + AHEAD < TM) read_old(i + AHEAD);
     __builtin_amdgcn_wave_barrier();
   }
 }
@@ -745,6 +782,91 @@ __global__ __launch_bounds__(256) void k_grouped_gemm_f32(GgParams p) {
   }
 }
 
+// Few fp32 tiles: one workgroup per 32 x 32 outputs (SwiGLU: 16 gate and 16 up
+// columns), its four waves each with every fourth 16 steps of the reduction,
+// fragments loaded straight from memory eight chunks at a time, the four sums
+// joined through LDS in wave order.  Without the barriers of the tiled kernel
+// a short call is one or two memory round trips: 128 rows of 8 experts,
+// 128 x 512: 13.3 us tiled.
+template <int KIND, int EPI>
+__global__ __launch_bounds__(256) void k_grouped_gemm_f32_few(GgParams p) {
+  static_assert(KIND != MOE_GEMM_TN, "a row product");
+  constexpr int BM = 32, AHEAD = 4;
+  __shared__ f32x4_t red[4][4][64];
+  __shared__ int s_loc[8];
+  GgTile t;
+  if (!gg_locate<KIND, BM>(p, s_loc, t)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l15 = lane & 15, g4 = (lane >> 4) * 4;       // fragment: position l15, steps g4 .. g4 + 3
+  const int c0 = t.nt * (EPI == EPI_SWIGLU ? 16 : 32);
+  const float* a[2];
+  const float* b[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    a[i] = static_cast<const float*>(p.A) + (t.row0 + t.m_off + min(i * 16 + l15, t.m_n - 1)) * p.K + g4;
+    const int brows = EPI == EPI_SWIGLU ? 2 * p.N : p.N;
+    const float* B = static_cast<const float*>(p.B) + static_cast<int64_t>(t.e) * brows * p.K;
+    const int col = EPI == EPI_SWIGLU ? min(c0 + l15, p.N - 1) + i * p.N : min(c0 + i * 16 + l15, p.N - 1);
+    b[i] = KIND == MOE_GEMM_NT ? B + static_cast<int64_t>(col) * p.K + g4 : B + static_cast<int64_t>(g4) * p.N + col;
+  }
+  const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+  f32x4_t acc[2][2] = {{zero, zero}, {zero, zero}};
+  const int chunks = (p.K + 15) / 16;
+  for (int c = wave; c < chunks; c += 4 * AHEAD) {
+    f32x4_t av[AHEAD][2], bv[AHEAD][2];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int k = (c + 4 * u) * 16;
+      const bool in = k + g4 < p.K;                      // K is a multiple of 4: four steps or none
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        av[u][i] = in ? *reinterpret_cast<const f32x4_t*>(a[i] + k) : zero;
+        if constexpr (KIND == MOE_GEMM_NT) {
+          bv[u][i] = in ? *reinterpret_cast<const f32x4_t*>(b[i] + k) : zero;
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) bv[u][i][q] = in ? b[i][static_cast<int64_t>(k + q) * p.N] : 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(bv[u][j][q], av[u][i][q], acc[i][j], 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) red[wave][i * 2 + j][lane] = acc[i][j];
+  __syncthreads();
+  // wave w finishes subtile (w >> 1, w & 1)
+  auto sum = [&](int q) {
+    f32x4_t v = red[0][q][lane];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) v += red[w][q][lane];
+    return v;
+  };
+  const int i = wave >> 1, j = wave & 1, in = i * 16 + l15;
+  if (in >= t.m_n) return;
+  const int64_t row = t.row0 + t.m_off + in;
+  if constexpr (EPI == EPI_SWIGLU) {
+    const int col = c0 + g4;
+    if (j == 0 && col < p.N) store_swiglu<true>(p, row, col, sum(i * 2), sum(i * 2 + 1));
+  } else {
+    const int col = c0 + j * 16 + g4;
+    if (col >= p.N) return;
+    if constexpr (EPI == EPI_SWIGLU_BWD)
+      store_swiglu_bwd<true>(p, row, col, sum(wave));
+    else
+      store_c(p, row * p.N + col, sum(wave));
+  }
+}
+
 // Sums the partial outputs of a split reduction in split order (so the result
 // does not depend on timing) and stores C.  NT/NN: only the rows of experts.
 __global__ __launch_bounds__(256) void k_join_splits(GgParams p, int64_t quads, int row_quads) {
@@ -783,7 +905,7 @@ static GgPlan gg_plan(int kind, int epi, bool f32, int E, int64_t cap, bool dens
   const int cols = kind == MOE_GEMM_TN ? K : epi == EPI_SWIGLU ? 2 * N : N;
   GgPlan q{128, 128, 1, 0};
   if (f32)
-    q.BM = q.BN = 64;
+    q.BM = q.BN = kind != MOE_GEMM_TN && gg_tiles(kind, epi, E, cap, dense, N, K, 64, 64) < 256 ? 32 : 64;
   else if (kind != MOE_GEMM_TN && rows <= 32)
     q.BM = 32;
   else if (cols > 128 && (kind == MOE_GEMM_TN ? N > 128 : rows > 128) &&
@@ -793,7 +915,7 @@ static GgPlan gg_plan(int kind, int epi, bool f32, int E, int64_t cap, bool dens
   // The reduction is cut into parts, doubled while the grid has fewer than 256
   // workgroups and each part keeps at least 256 steps, at most 16.
   const int64_t red = kind == MOE_GEMM_TN ? rows : K;
-  if (epi == EPI_STORE)
+  if (epi == EPI_STORE && !(f32 && q.BM == 32))
     while (q.splits < 16 && q.tiles * q.splits < 256 && red / (2 * q.splits) >= 256) q.splits *= 2;
   return q;
 }
@@ -806,8 +928,11 @@ static moe_status gg_launch(GgParams& p, const GgPlan& q, bool f32, hipStream_t 
   p.splits = q.splits;
   if (gemm_grid(q.tiles) >= (1 << 23)) return MOE_ERR_UNSUPPORTED;      // at most 512 threads each, 2^32 in a grid
   const dim3 grid(static_cast<unsigned>(gemm_grid(q.tiles)), q.splits);
-  if (f32) {
+  if (f32 && q.BM == 64) {
     hipLaunchKernelGGL((k_grouped_gemm_f32<KIND, EPI>), grid, dim3(256), 0, s, p);
+  } else if (f32) {
+    if constexpr (KIND != MOE_GEMM_TN)
+      hipLaunchKernelGGL((k_grouped_gemm_f32_few<KIND, EPI>), grid, dim3(256), 0, s, p);
   } else if (q.BM == 256) {
     hipLaunchKernelGGL((k_grouped_gemm<KIND, EPI, 256, 256, 64, 2, 4, 2, 2>), grid, dim3(512), 0, s, p);
   } else if (q.BM == 128) {

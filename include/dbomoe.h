@@ -388,7 +388,8 @@ moe_status moe_route_backward(const float* logits, int64_t T, const int32_t* top
  *       a = mix((uint32)i ^ key ^ 0x9e3779b9 * (i >> 32)),  b = mix(a + 0x9e3779b9);
  *     m's code takes a >> 12, sqrt(v)'s b >> 12 (20 bits each), a bf16 param
  *     (a & 0xfff) << 4 | (b & 0xf) (16 bits).
- * Tensors of n == 0 are skipped; tensors must not overlap.
+ * Gradients must be finite: the states keep what is not.  Tensors of n == 0
+ * are skipped; tensors must not overlap.
  * ------------------------------------------------------------------------- */
 typedef struct {
   void* param;
@@ -403,7 +404,7 @@ typedef struct {
 } moe_adamw_tensor;
 
 typedef struct {
-  double lr, beta1, beta2, eps, weight_decay;   /* lr, wd >= 0; 0 <= beta < 1; eps > 0 */
+  double lr, beta1, beta2, eps, weight_decay;   /* lr, wd >= 0; 0 <= beta < 1; eps >= 1.2e-38 */
   uint32_t seed;
 } moe_adamw_params;
 
