@@ -33,7 +33,7 @@ EXPORTED = [
     "moe_quant_fp8_rows", "moe_dispatch_fp8", "moe_ffn_fp8_workspace_size", "moe_grouped_ffn_fp8",
     "moe_dispatch_send", "moe_dispatch_recv", "moe_dispatch_noalloc_max_workspace", "moe_dispatch_noalloc",
     "moe_grouped_gemm_workspace_size", "moe_grouped_gemm", "moe_grouped_swiglu", "moe_grouped_swiglu_backward",
-    "moe_combine_backward", "moe_route_backward", "moe_adamw_step",
+    "moe_combine_backward", "moe_route_backward", "moe_adamw_table_size", "moe_adamw_table_build", "moe_adamw_step",
 ]
 
 
@@ -134,8 +134,9 @@ def lib():
             "moe_grouped_swiglu_backward": (_i32, [_vp, _vp, _vp, _i32, _vp, _i32, _i64, _i32, _i32, _vp, _vp]),
             "moe_combine_backward": (_i32, [_vp, _vp, _i32, _i64, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp]),
             "moe_route_backward": (_i32, [_vp, _i64, _vp, _vp, ctypes.POINTER(moe_route_params), _vp, _i32, _vp]),
-            "moe_adamw_step": (_i32, [ctypes.POINTER(moe_adamw_tensor), _i32, ctypes.POINTER(moe_adamw_params),
-                                      _vp, _vp, _vp, _vp]),
+            "moe_adamw_table_size": (_sz, [_i32]),
+            "moe_adamw_table_build": (_i32, [ctypes.POINTER(moe_adamw_tensor), _i32, _vp, _sz]),
+            "moe_adamw_step": (_i32, [_vp, _vp, ctypes.POINTER(moe_adamw_params), _vp, _vp, _vp, _vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -475,39 +476,46 @@ def adamw_params(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, s
 
 
 class AdamWTable:
-    """The tensors of an optimizer as moe_adamw_step takes them.  Holds references: the tensors live as long as it."""
+    """The tensors of an optimizer as moe_adamw_step takes them: the table on the host and its copy on the device.
+    Holds references: the tensors live as long as it."""
 
-    def __init__(self, entries, device, keep):
-        self.entries, self.device, self.keep = entries, device, keep
+    def __init__(self, host, device_copy, device: int, keep):
+        self.host, self.device_copy, self.device, self.keep = host, device_copy, device, keep
+        self.host_ptr, self.device_ptr = host.data_ptr(), device_copy.data_ptr()
 
 
 def moe_adamw_table(params, grads, m, v, m_scale=None, v_scale=None, master=None) -> AdamWTable:
     """Lists of tensors, one entry per parameter.  params float32 or bfloat16; grads likewise; m and v float32, or
-    8-bit codes (float8_e4m3fn or uint8) with m_scale and v_scale uint8 [ceil(n / 128)]; master float32 or None."""
+    8-bit codes (float8_e4m3fn or uint8) with m_scale and v_scale uint8 [ceil(n / 128)]; master float32 or None.
+    Made once (it copies the table to the device); the tensors must stay where they are."""
     n = len(params)
     _need(n > 0, "no tensors")
     cols = [params, grads, m, v, m_scale, v_scale, master]
     for c in cols:
         _need(c is None or len(c) == n, "lists of one length")
+    none = [None] * n
     entries = (moe_adamw_tensor * n)()
+    f32, bf16, floats = torch.float32, torch.bfloat16, (torch.float32, torch.bfloat16)
     d = None
-    for i in range(n):
-        p, g, mi, vi, ms, vs, ma = (None if c is None else c[i] for c in cols)
-        size = p.numel()
+    for i, (p, g, mi, vi, ms, vs, ma) in enumerate(zip(*(none if c is None else c for c in cols))):
+        size, t, gt, mt = p.numel(), p.dtype, g.dtype, mi.dtype
         d = _device(p) if d is None else d
-        _need(g.numel() == size and mi.numel() == size and vi.numel() == size and (ma is None or ma.numel() == size),
-              f"tensor {i}: sizes differ")
-        eight = mi.dtype != torch.float32
-        _need(p.dtype in (torch.float32, torch.bfloat16) and g.dtype in (torch.float32, torch.bfloat16) and
-              mi.dtype == vi.dtype and mi.dtype in (torch.float32, torch.uint8, torch.float8_e4m3fn) and
-              (ma is None or (ma.dtype == torch.float32 and p.dtype == torch.bfloat16)), f"tensor {i}: types")
-        _need(eight == (ms is not None) == (vs is not None), f"tensor {i}: scales go with 8-bit states")
-        if eight:
-            _need(ms.dtype == vs.dtype == torch.uint8 and ms.numel() == vs.numel() == (size + 127) // 128,
-                  f"tensor {i}: scales uint8 [ceil(n / 128)]")
+        if g.numel() != size or mi.numel() != size or vi.numel() != size or (ma is not None and ma.numel() != size):
+            raise ValueError(f"tensor {i}: sizes differ")
+        if (t not in floats or gt not in floats or mt != vi.dtype or (mt != f32 and _CODES.get(mt) != MOE_FP8_E4M3FN)
+                or (ma is not None and (ma.dtype != f32 or t != bf16))):
+            raise ValueError(f"tensor {i}: types")
+        if (mt != f32) != (ms is not None) or (ms is None) != (vs is None):
+            raise ValueError(f"tensor {i}: scales go with 8-bit states")
+        if ms is not None and (ms.dtype != torch.uint8 or vs.dtype != torch.uint8 or
+                               not ms.numel() == vs.numel() == (size + 127) // 128):
+            raise ValueError(f"tensor {i}: scales uint8 [ceil(n / 128)]")
         entries[i] = moe_adamw_tensor(_ptr(d, p), _ptr(d, g), _ptr(d, mi), _ptr(d, vi), _ptr(d, ms), _ptr(d, vs),
-                                      _ptr(d, ma), size, _CODES[p.dtype], _CODES[g.dtype], _CODES[mi.dtype])
-    return AdamWTable(entries, d, cols)
+                                      _ptr(d, ma), size, _CODES[t], _CODES[gt], _CODES[mt])
+    nbytes = lib().moe_adamw_table_size(n)
+    host = torch.zeros(nbytes, dtype=torch.uint8)
+    _check(lib().moe_adamw_table_build(entries, n, host.data_ptr(), nbytes), "moe_adamw_table_build")
+    return AdamWTable(host, host.to(torch.device("cuda", d)), d, cols)
 
 
 def moe_adamw_step(table: AdamWTable, hp: moe_adamw_params, step, lr_scale=None, grad_scale=None, stream=None):
@@ -519,7 +527,7 @@ def moe_adamw_step(table: AdamWTable, hp: moe_adamw_params, step, lr_scale=None,
         if s is not None and (s.dtype != torch.float32 or s.numel() != 1):
             raise ValueError("lr_scale, grad_scale: one float32")
     d = table.device
-    _call("moe_adamw_step", d, stream, table.entries, len(table.entries), hp, _ptr(d, step), _ptr(d, lr_scale),
+    _call("moe_adamw_step", d, stream, table.host_ptr, table.device_ptr, hp, _ptr(d, step), _ptr(d, lr_scale),
           _ptr(d, grad_scale))
 
 

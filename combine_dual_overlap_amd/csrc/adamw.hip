@@ -19,13 +19,17 @@
 // result depends on nothing else.  mix() is two rounds of xor-shift and
 // multiplication, a bijection of 32-bit words.
 #include <math.h>
+#include <string.h>
+
+#include <type_traits>
 
 #include "common.h"
 
 namespace dbomoe {
 
-constexpr int kAdamTensors = 48;      // tensors per launch: the table is a kernel argument
+constexpr int kAdamTensors = 4096;    // tensors per launch at most (64 x 64: two ballots find one)
 constexpr int kAdamGroup = 2048;      // elements a workgroup takes at a time (8 a thread)
+constexpr uint32_t kAdamMagic = 0x41644d57;
 
 struct AdamTensor {
   void* p;
@@ -39,10 +43,36 @@ struct AdamTensor {
   uint32_t key;                       // 0x85ebca77 * the tensor's number
 };
 
-struct AdamArgs {
-  int32_t first[kAdamTensors];        // first workgroup of each tensor; behind the last one INT32_MAX
-  AdamTensor t[kAdamTensors];
+// The table: a header, the launches (tensors of one combination of types), the
+// first workgroup of each tensor inside its launch, the tensors.  The host copy
+// gives the launches, the device copy is what the kernels read.  (As a kernel
+// argument the tensors sat in host memory, and a step of 24 small tensors
+// waited 5 us for them.)
+struct AdamLaunch {
+  int32_t begin, count;               // tensors [begin, begin + count) of the table
+  int32_t combo;                      // bit 0: 8-bit states, bit 1: bf16 gradients, then AdamParam
   int32_t groups;                     // groups of kAdamGroup elements per workgroup
+  int32_t blocks, pad;
+};
+
+struct AdamHeader {
+  uint32_t magic;
+  int32_t launches, tensors, pad;
+};
+
+struct AdamLayout {
+  size_t launch, first, tensor, bytes;
+  explicit AdamLayout(size_t n)
+      : launch(align_up(sizeof(AdamHeader), 64)),
+        first(align_up(launch + n * sizeof(AdamLaunch), 64)),
+        tensor(align_up(first + n * sizeof(int32_t), 64)),
+        bytes(align_up(tensor + n * sizeof(AdamTensor), 256)) {}
+};
+
+struct AdamArgs {
+  const int32_t* first;
+  const AdamTensor* t;
+  int32_t count, groups;
   uint32_t seed;
   float b1, omb1, b2, omb2, eps, lr, lr_wd;
   double log_b1, log_b2;
@@ -50,7 +80,6 @@ struct AdamArgs {
   const float* lr_scale;
   const float* grad_scale;
 };
-static_assert(sizeof(AdamArgs) <= 4096, "kernel argument");
 
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
   x ^= x >> 16;
@@ -100,10 +129,10 @@ __device__ __forceinline__ uint64_t encode8(const float* y, const uint32_t* r) {
   return static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32 | static_cast<uint32_t>(lo);
 }
 
-// 8 elements from index i on; those behind n read as zero.
-template <bool BF16>
+// 8 elements from index i on; those behind n read as zero.  FULL: none is.
+template <bool BF16, bool FULL>
 __device__ __forceinline__ void load8(const void* base, int64_t i, int64_t n, float* x) {
-  if (i + 8 <= n) {
+  if (FULL || i + 8 <= n) {
     if constexpr (BF16) {
       const u32x4_t v = *reinterpret_cast<const u32x4_t*>(static_cast<const bf16_t*>(base) + i);
 #pragma unroll
@@ -129,8 +158,9 @@ __device__ __forceinline__ void load8(const void* base, int64_t i, int64_t n, fl
   }
 }
 
+template <bool FULL>
 __device__ __forceinline__ void store8_f32(float* base, int64_t i, int64_t n, const float* x) {
-  if (i + 8 <= n) {
+  if (FULL || i + 8 <= n) {
     f32x4_t* d = reinterpret_cast<f32x4_t*>(base + i);
     d[0] = f32x4_t{x[0], x[1], x[2], x[3]};
     d[1] = f32x4_t{x[4], x[5], x[6], x[7]};
@@ -141,8 +171,9 @@ __device__ __forceinline__ void store8_f32(float* base, int64_t i, int64_t n, co
   }
 }
 
+template <bool FULL>
 __device__ __forceinline__ void store8_bf16(bf16_t* base, int64_t i, int64_t n, const uint32_t* h) {
-  if (i + 8 <= n) {
+  if (FULL || i + 8 <= n) {
     *reinterpret_cast<u32x4_t*>(base + i) =
         u32x4_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
   } else {
@@ -152,8 +183,9 @@ __device__ __forceinline__ void store8_bf16(bf16_t* base, int64_t i, int64_t n, 
   }
 }
 
+template <bool FULL>
 __device__ __forceinline__ uint64_t load8_codes(const uint8_t* base, int64_t i, int64_t n) {
-  if (i + 8 <= n) return *reinterpret_cast<const uint64_t*>(base + i);
+  if (FULL || i + 8 <= n) return *reinterpret_cast<const uint64_t*>(base + i);
   uint64_t v = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -161,8 +193,9 @@ __device__ __forceinline__ uint64_t load8_codes(const uint8_t* base, int64_t i, 
   return v;
 }
 
+template <bool FULL>
 __device__ __forceinline__ void store8_codes(uint8_t* base, int64_t i, int64_t n, uint64_t q) {
-  if (i + 8 <= n) {
+  if (FULL || i + 8 <= n) {
     *reinterpret_cast<uint64_t*>(base + i) = q;
   } else {
 #pragma unroll
@@ -191,10 +224,18 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
 #pragma clang fp contract(off)
   // this workgroup's tensor: the last whose first workgroup is not behind it
   const int blk = blockIdx.x, lane = threadIdx.x & 63;
-  const int mine = lane < kAdamTensors ? a.first[lane] : 0x7fffffff;
+  int base = 0, span = a.count;
+  if (a.count > 64) {
+    span = (a.count + 63) / 64;
+    const int at = lane * span < a.count ? a.first[lane * span] : 0x7fffffff;
+    base = (__popcll(__ballot(at <= blk)) - 1) * span;
+  }
+  const int mine = lane < span && base + lane < a.count ? a.first[base + lane] : 0x7fffffff;
   const int q = __builtin_amdgcn_readfirstlane(__popcll(__ballot(mine <= blk)) - 1);
   const int first = __builtin_amdgcn_readlane(mine, q);
-  const AdamTensor& t = a.t[q];
+  // the table does not change while a step runs: scalar loads, kept across the stores
+  typedef const __attribute__((address_space(4))) AdamTensor ConstTensor;
+  const ConstTensor& t = ((ConstTensor*)(a.t))[__builtin_amdgcn_readfirstlane(base) + q];
   const int64_t n = t.n;
   const int step = max(*a.step, 1);
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;
@@ -206,27 +247,25 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
   const uint32_t key0 = mix(mix(a.seed + 0x9e3779b9u * static_cast<uint32_t>(step)) + t.key);
 
   const int64_t begin = static_cast<int64_t>(blk - first) * a.groups * kAdamGroup + threadIdx.x * 8;
-  for (int it = 0; it < a.groups; ++it) {
-    const int64_t i = begin + it * kAdamGroup;
-    // the 16 lanes of a block of 128 stay together: they meet in block_max
-    if (i - (threadIdx.x & 15) * 8 >= n) break;
+  auto group = [&](int64_t i, auto full) {
+    constexpr bool FULL = decltype(full)::value;
     float g[8], m[8], v[8], p[8], root[8];
-    load8<GRAD_BF16>(t.g, i, n, g);
+    load8<GRAD_BF16, FULL>(t.g, i, n, g);
     if constexpr (EIGHT) {
-      const uint64_t qm = load8_codes(static_cast<const uint8_t*>(t.m), i, n);
-      const uint64_t qv = load8_codes(static_cast<const uint8_t*>(t.v), i, n);
+      const uint64_t qm = load8_codes<FULL>(static_cast<const uint8_t*>(t.m), i, n);
+      const uint64_t qv = load8_codes<FULL>(static_cast<const uint8_t*>(t.v), i, n);
       decode8(qm, e8m0(t.ms[i >> 7]), m);
       decode8(qv, e8m0(t.vs[i >> 7]), v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = v[j] * v[j];
     } else {
-      load8<false>(t.m, i, n, m);
-      load8<false>(t.v, i, n, v);
+      load8<false, FULL>(t.m, i, n, m);
+      load8<false, FULL>(t.v, i, n, v);
     }
     if constexpr (PARAM == PARAM_MASTER)
-      load8<false>(t.master, i, n, p);
+      load8<false, FULL>(t.master, i, n, p);
     else
-      load8<PARAM == PARAM_BF16>(t.p, i, n, p);
+      load8<PARAM == PARAM_BF16, FULL>(t.p, i, n, p);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float gj = g[j] * gs;
@@ -260,18 +299,18 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
         // a nonzero value below the smallest code (2^-9) becomes that code
         yv[j] = root[j] > 0.f ? fmaxf(root[j] * iv, 0.001953125f) : 0.f;
       }
-      store8_codes(static_cast<uint8_t*>(t.m), i, n, encode8(ym, one));
-      store8_codes(static_cast<uint8_t*>(t.v), i, n, encode8(yv, two));
+      store8_codes<FULL>(static_cast<uint8_t*>(t.m), i, n, encode8(ym, one));
+      store8_codes<FULL>(static_cast<uint8_t*>(t.v), i, n, encode8(yv, two));
       if ((threadIdx.x & 15) == 0) {
         t.ms[i >> 7] = static_cast<uint8_t>(em + 127);
         t.vs[i >> 7] = static_cast<uint8_t>(ev + 127);
       }
     } else {
-      store8_f32(static_cast<float*>(t.m), i, n, m);
-      store8_f32(static_cast<float*>(t.v), i, n, v);
+      store8_f32<FULL>(static_cast<float*>(t.m), i, n, m);
+      store8_f32<FULL>(static_cast<float*>(t.v), i, n, v);
     }
     if constexpr (PARAM == PARAM_F32) {
-      store8_f32(static_cast<float*>(t.p), i, n, p);
+      store8_f32<FULL>(static_cast<float*>(t.p), i, n, p);
     } else {
       uint32_t h[8];
 #pragma unroll
@@ -284,9 +323,16 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
           h[j] = f32_to_bf16(p[j]);
         }
       }
-      store8_bf16(static_cast<bf16_t*>(t.p), i, n, h);
-      if constexpr (PARAM == PARAM_MASTER) store8_f32(t.master, i, n, p);
+      store8_bf16<FULL>(static_cast<bf16_t*>(t.p), i, n, h);
+      if constexpr (PARAM == PARAM_MASTER) store8_f32<FULL>(t.master, i, n, p);
     }
+  };
+  for (int it = 0; it < a.groups; ++it) {
+    const int64_t i = begin + it * kAdamGroup;
+    if (i - threadIdx.x * 8 + kAdamGroup <= n)                // the whole workgroup's elements exist
+      group(i, std::integral_constant<bool, true>{});
+    else if (i - (threadIdx.x & 15) * 8 < n)                  // the 16 lanes of a block of 128 meet in block_max
+      group(i, std::integral_constant<bool, false>{});
   }
 }
 
@@ -302,16 +348,16 @@ static void adamw_launch(const AdamArgs& a, bool gbf16, unsigned blocks, hipStre
 
 using namespace dbomoe;
 
-extern "C" moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n_tensors, const moe_adamw_params* hp,
-                                     const int32_t* step, const float* lr_scale, const float* grad_scale,
-                                     void* stream) {
-  if (!hp || n_tensors < 0 || (n_tensors > 0 && !tensors)) return MOE_ERR_INVALID_ARG;
-  if (!(hp->lr >= 0) || !(hp->beta1 >= 0 && hp->beta1 < 1) || !(hp->beta2 >= 0 && hp->beta2 < 1) || !(hp->eps >= 1.2e-38) ||
-      !(hp->weight_decay >= 0) || !isfinite(hp->lr) || !isfinite(hp->eps) || !isfinite(hp->weight_decay))
-    return MOE_ERR_INVALID_ARG;
-  if (n_tensors == 0) return MOE_OK;
-  if (!step) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(step) || !aligned16(lr_scale) || !aligned16(grad_scale)) return MOE_ERR_MISALIGNED;
+extern "C" size_t moe_adamw_table_size(int32_t n_tensors) {
+  return n_tensors < 1 ? 0 : AdamLayout(n_tensors).bytes;
+}
+
+extern "C" moe_status moe_adamw_table_build(const moe_adamw_tensor* tensors, int32_t n_tensors, void* table,
+                                            size_t bytes) {
+  if (!tensors || !table || n_tensors < 1) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(table)) return MOE_ERR_MISALIGNED;
+  const AdamLayout l(n_tensors);
+  if (bytes < l.bytes) return MOE_ERR_WORKSPACE;
   int64_t total = 0;
   for (int i = 0; i < n_tensors; ++i) {
     const moe_adamw_tensor& t = tensors[i];
@@ -330,8 +376,59 @@ extern "C" moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n_
       return MOE_ERR_MISALIGNED;
     total += (t.n + kAdamGroup - 1) / kAdamGroup;
   }
+  auto* out = static_cast<uint8_t*>(table);
+  memset(out, 0, l.bytes);
+  auto* launch = reinterpret_cast<AdamLaunch*>(out + l.launch);
+  auto* first = reinterpret_cast<int32_t*>(out + l.first);
+  auto* entry = reinterpret_cast<AdamTensor*>(out + l.tensor);
+  // four groups a workgroup where that leaves enough workgroups
+  const int groups = total >= 8192 ? 4 : 1;
+  const int64_t per = static_cast<int64_t>(groups) * kAdamGroup;
+  int launches = 0, at = 0;
+  for (int combo = 0; combo < 12; ++combo) {
+    AdamLaunch* cur = nullptr;
+    for (int i = 0; i < n_tensors; ++i) {
+      const moe_adamw_tensor& t = tensors[i];
+      const int kind = t.master ? PARAM_MASTER : t.param_dtype == MOE_BF16 ? PARAM_BF16 : PARAM_F32;
+      const int mine = (t.state_dtype == MOE_FP8_E4M3FN ? 1 : 0) | (t.grad_dtype == MOE_BF16 ? 2 : 0) | kind << 2;
+      if (t.n == 0 || mine != combo) continue;
+      const int64_t nb = (t.n + per - 1) / per;
+      // a grid holds fewer than 2^32 threads
+      if (!cur || cur->count == kAdamTensors || cur->blocks + nb >= (1 << 24)) {
+        if (nb >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
+        cur = &launch[launches++];
+        *cur = AdamLaunch{at, 0, combo, groups, 0, 0};
+      }
+      first[at] = cur->blocks;
+      entry[at] = AdamTensor{t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.master, t.n,
+                             0x85ebca77u * static_cast<uint32_t>(i)};
+      cur->blocks += static_cast<int32_t>(nb);
+      ++cur->count;
+      ++at;
+    }
+  }
+  *reinterpret_cast<AdamHeader*>(out) = AdamHeader{kAdamMagic, launches, n_tensors, 0};
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_adamw_step(const void* table_host, const void* table_dev, const moe_adamw_params* hp,
+                                     const int32_t* step, const float* lr_scale, const float* grad_scale,
+                                     void* stream) {
+  if (!hp || !table_host || !table_dev || !step) return MOE_ERR_INVALID_ARG;
+  if (!(hp->lr >= 0) || !(hp->beta1 >= 0 && hp->beta1 < 1) || !(hp->beta2 >= 0 && hp->beta2 < 1) ||
+      !(hp->eps >= 1.2e-38) || !(hp->weight_decay >= 0) || !isfinite(hp->lr) || !isfinite(hp->eps) ||
+      !isfinite(hp->weight_decay))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(table_host) || !aligned256(table_dev) || !aligned16(step) || !aligned16(lr_scale) ||
+      !aligned16(grad_scale))
+    return MOE_ERR_MISALIGNED;
+  const auto* host = static_cast<const uint8_t*>(table_host);
+  const auto* head = reinterpret_cast<const AdamHeader*>(host);
+  if (head->magic != kAdamMagic || head->tensors < 1) return MOE_ERR_INVALID_ARG;
+  const AdamLayout l(head->tensors);
+  const auto* launch = reinterpret_cast<const AdamLaunch*>(host + l.launch);
+  const auto* dev = static_cast<const uint8_t*>(table_dev);
   AdamArgs a{};
-  a.groups = total >= 8192 ? 4 : 1;
   a.seed = hp->seed;
   a.b1 = static_cast<float>(hp->beta1);
   a.omb1 = static_cast<float>(1.0 - hp->beta1);
@@ -346,45 +443,25 @@ extern "C" moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n_
   a.lr_scale = lr_scale;
   a.grad_scale = grad_scale;
   const hipStream_t s = as_stream(stream);
-  // One launch per 48 tensors of one combination of types (and 2^24
-  // workgroups: a grid holds fewer than 2^32 threads).
-  for (int combo = 0; combo < 12; ++combo) {
-    const bool eight = combo & 1, gbf16 = combo & 2;
-    const int kind = combo >> 2;
-    int64_t blocks = 0;
-    int count = 0;
-    auto flush = [&]() -> moe_status {
-      if (count == 0) return MOE_OK;
-      for (int i = count; i < kAdamTensors; ++i) a.first[i] = 0x7fffffff;
-      const unsigned nb = static_cast<unsigned>(blocks);
-      if (kind == PARAM_F32)
+  for (int i = 0; i < head->launches; ++i) {
+    const AdamLaunch& c = launch[i];
+    a.first = reinterpret_cast<const int32_t*>(dev + l.first) + c.begin;
+    a.t = reinterpret_cast<const AdamTensor*>(dev + l.tensor) + c.begin;
+    a.count = c.count;
+    a.groups = c.groups;
+    const bool eight = c.combo & 1, gbf16 = c.combo & 2;
+    const unsigned nb = static_cast<unsigned>(c.blocks);
+    switch (c.combo >> 2) {
+      case PARAM_F32:
         eight ? adamw_launch<true, PARAM_F32>(a, gbf16, nb, s) : adamw_launch<false, PARAM_F32>(a, gbf16, nb, s);
-      else if (kind == PARAM_BF16)
+        break;
+      case PARAM_BF16:
         eight ? adamw_launch<true, PARAM_BF16>(a, gbf16, nb, s) : adamw_launch<false, PARAM_BF16>(a, gbf16, nb, s);
-      else
+        break;
+      default:
         eight ? adamw_launch<true, PARAM_MASTER>(a, gbf16, nb, s) : adamw_launch<false, PARAM_MASTER>(a, gbf16, nb, s);
-      count = 0;
-      blocks = 0;
-      DBOMOE_CHECK_LAUNCH();
-      return MOE_OK;
-    };
-    for (int i = 0; i < n_tensors; ++i) {
-      const moe_adamw_tensor& t = tensors[i];
-      const int tk = t.master ? PARAM_MASTER : t.param_dtype == MOE_BF16 ? PARAM_BF16 : PARAM_F32;
-      if (t.n == 0 || tk != kind || (t.state_dtype == MOE_FP8_E4M3FN) != eight || (t.grad_dtype == MOE_BF16) != gbf16)
-        continue;
-      const int64_t per = static_cast<int64_t>(a.groups) * kAdamGroup, nb = (t.n + per - 1) / per;
-      if (count == kAdamTensors || blocks + nb >= (1 << 24)) {
-        const moe_status st = flush();
-        if (st != MOE_OK) return st;
-      }
-      a.first[count] = static_cast<int32_t>(blocks);
-      a.t[count++] = AdamTensor{t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.master, t.n,
-                                0x85ebca77u * static_cast<uint32_t>(i)};
-      blocks += nb;
     }
-    const moe_status st = flush();
-    if (st != MOE_OK) return st;
+    DBOMOE_CHECK_LAUNCH();
   }
   return MOE_OK;
 }

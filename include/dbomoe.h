@@ -361,11 +361,14 @@ moe_status moe_route_backward(const float* logits, int64_t T, const int32_t* top
                               const moe_route_params* params, void* dlogits, moe_dtype dl, void* stream);
 
 /* ---------------------------------------------------------------------------
- * moe_adamw_step - one AdamW update of n_tensors tensors.
+ * moe_adamw_step - one AdamW update of the tensors of a table.
  *   g = grad * grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
  * computed in fp32, with lr = hp.lr * lr_scale and t = *step >= 1.
- *   tensors  HOST array, read during the call; per tensor:
+ *   table    moe_adamw_table_build writes moe_adamw_table_size(n_tensors) bytes
+ *     to HOST memory from an array of tensors (no device access); the caller
+ *     copies them to device memory once and passes both copies to every step
+ *     (table_host 16-byte, table_dev 256-byte aligned).  Per tensor:
  *     param   [n] fp32 or bf16, updated
  *     grad    [n] fp32 or bf16
  *     master  [n] fp32 or NULL (bf16 param only): the parameter in fp32,
@@ -408,7 +411,9 @@ typedef struct {
   uint32_t seed;
 } moe_adamw_params;
 
-moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n_tensors, const moe_adamw_params* hp,
+size_t moe_adamw_table_size(int32_t n_tensors);
+moe_status moe_adamw_table_build(const moe_adamw_tensor* tensors, int32_t n_tensors, void* table, size_t bytes);
+moe_status moe_adamw_step(const void* table_host, const void* table_dev, const moe_adamw_params* hp,
                           const int32_t* step, const float* lr_scale, const float* grad_scale, void* stream);
 
 /* ---------------------------------------------------------------------------

@@ -95,33 +95,60 @@ def test_combine_and_route_backward_refusals():
     assert route(T=0) == B.MOE_OK
 
 
-def test_adamw_refusals():
-    B = _B()
+def _table(B, **kw):
+    """(status, table bytes) of a table of one tensor."""
+    t = (B.moe_adamw_tensor * 1)()
+    base = dict(param=A, grad=2 * A, m=3 * A, v=4 * A, m_scale=None, v_scale=None, master=None, n=100,
+                param_dtype=1, grad_dtype=1, state_dtype=0)
+    base.update(kw)
+    t[0] = B.moe_adamw_tensor(*base.values())
+    host = torch.zeros(B.lib().moe_adamw_table_size(1), dtype=torch.uint8)
+    return B.lib().moe_adamw_table_build(t, 1, host.data_ptr(), host.numel()), host
 
-    def call(hp=None, step=A, lr=None, gs=None, count=1, null=False, **kw):
-        t = (B.moe_adamw_tensor * 1)()
-        base = dict(param=A, grad=2 * A, m=3 * A, v=4 * A, m_scale=None, v_scale=None, master=None, n=100,
-                    param_dtype=1, grad_dtype=1, state_dtype=0)
-        base.update(kw)
-        t[0] = B.moe_adamw_tensor(*base.values())
+
+def test_adamw_table_refusals():
+    B = _B()
+    bad = B.MOE_ERR_INVALID_ARG
+    for kw in (dict(n=-1), dict(param=None), dict(grad=None), dict(m=None), dict(v=None), dict(m_scale=A),
+               dict(state_dtype=2), dict(state_dtype=2, m_scale=A), dict(param_dtype=0, master=5 * A), dict(grad=A),
+               dict(v=3 * A), dict(master=A)):
+        assert _table(B, **kw)[0] == bad, kw
+    for kw in (dict(param_dtype=2), dict(grad_dtype=2), dict(state_dtype=1), dict(n=(1 << 36) + 1)):
+        assert _table(B, **kw)[0] == B.MOE_ERR_UNSUPPORTED, kw
+    for kw in (dict(param=A + 8), dict(grad=2 * A + 2), dict(m=3 * A + 4), dict(v=4 * A + 4), dict(master=5 * A + 4)):
+        assert _table(B, **kw)[0] == B.MOE_ERR_MISALIGNED, kw
+    assert _table(B)[0] == _table(B, n=0)[0] == _table(B, state_dtype=2, m_scale=A + 1, v_scale=A + 3)[0] == B.MOE_OK
+    t = (B.moe_adamw_tensor * 1)()
+    build = B.lib().moe_adamw_table_build
+    host = torch.zeros(4096, dtype=torch.uint8)
+    assert B.lib().moe_adamw_table_size(0) == B.lib().moe_adamw_table_size(-3) == 0
+    assert build(None, 1, host.data_ptr(), 4096) == build(t, 0, host.data_ptr(), 4096) == build(t, 1, None, 4096) == bad
+    assert build(t, 1, host.data_ptr() + 8, 4000) == B.MOE_ERR_MISALIGNED
+    assert build(t, 1, host.data_ptr(), B.lib().moe_adamw_table_size(1) - 1) == B.MOE_ERR_WORKSPACE
+
+
+def test_adamw_step_refusals():
+    B = _B()
+    status, host = _table(B)
+    assert status == B.MOE_OK
+    empty = _table(B, n=0)[1]
+
+    def call(hp=None, table=host.data_ptr(), dev=A, step=A, lr=None, gs=None):
         hp = B.adamw_params(**(hp or {}))
-        return B.lib().moe_adamw_step(None if null else t, count, ctypes.byref(hp), step, lr, gs, None)
+        return B.lib().moe_adamw_step(table, dev, ctypes.byref(hp), step, lr, gs, None)
 
     bad = B.MOE_ERR_INVALID_ARG
     nan, inf = float("nan"), float("inf")
     for hp in (dict(lr=-1.0), dict(lr=nan), dict(lr=inf), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0),
-               dict(beta2=nan), dict(eps=0.0), dict(eps=inf), dict(weight_decay=-1.0), dict(weight_decay=inf)):
+               dict(beta2=nan), dict(eps=0.0), dict(eps=1e-40), dict(eps=inf), dict(weight_decay=-1.0),
+               dict(weight_decay=inf)):
         assert call(hp=hp) == bad, hp
-    for kw in (dict(step=None), dict(count=-1), dict(null=True), dict(n=-1), dict(param=None), dict(grad=None),
-               dict(m=None), dict(v=None), dict(m_scale=A), dict(state_dtype=2), dict(state_dtype=2, m_scale=A),
-               dict(param_dtype=0, master=5 * A), dict(grad=A), dict(v=3 * A), dict(master=A)):
+    zeros = torch.zeros(512, dtype=torch.uint8)
+    for kw in (dict(table=None), dict(dev=None), dict(step=None), dict(table=zeros.data_ptr())):
         assert call(**kw) == bad, kw
-    for kw in (dict(param_dtype=2), dict(grad_dtype=2), dict(state_dtype=1), dict(n=(1 << 36) + 1)):
-        assert call(**kw) == B.MOE_ERR_UNSUPPORTED, kw
-    for kw in (dict(param=A + 8), dict(grad=2 * A + 2), dict(m=3 * A + 4), dict(v=4 * A + 4), dict(master=5 * A + 4),
-               dict(step=A + 4), dict(lr=A + 4), dict(gs=A + 4)):
+    for kw in (dict(dev=A + 64), dict(step=A + 4), dict(lr=A + 4), dict(gs=A + 4), dict(table=host.data_ptr() + 8)):
         assert call(**kw) == B.MOE_ERR_MISALIGNED, kw
-    assert call(n=0) == B.MOE_OK and call(count=0, null=True) == B.MOE_OK
+    assert call(table=empty.data_ptr()) == B.MOE_OK          # only an empty tensor: nothing is enqueued
 
 
 def test_binding_refuses_shapes_and_types():
