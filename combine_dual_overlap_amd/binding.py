@@ -324,23 +324,28 @@ def _device(t) -> int:
     return d
 
 
-def _ptr(d: int, t):
-    """Address of a contiguous tensor on device d; None stays None."""
-    if t is None:
-        return None
-    if t.get_device() != d:
-        raise ValueError("expected a device tensor" if not t.is_cuda else "tensors on different devices")
-    if not t.is_contiguous():
-        raise ValueError("expected a contiguous tensor")
-    return t.data_ptr()
+def _ptrs(d: int, *ts) -> list:
+    """Addresses of contiguous tensors on device d; None stays None."""
+    out = []
+    for t in ts:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != d:
+            raise ValueError("tensors on different devices" if t.is_cuda else "expected a device tensor")
+        if not t.is_contiguous():
+            raise ValueError("expected a contiguous tensor")
+        out.append(t.data_ptr())
+    return out
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(fn: str, d: int, stream, *args):
     f = getattr(_LIB or lib(), fn)
-    if d == torch.cuda.current_device():
+    if d == _current_device():          # (a tensor on d: CUDA is initialised)
         h = stream.cuda_stream if stream is not None else _raw_stream(d) if _raw_stream else stream_handle()
         st = f(*args, h)
     else:
@@ -406,8 +411,9 @@ def moe_grouped_gemm(kind: str, a, b, offsets, c, ws=None, accumulate=False, str
     offsets None: one group of all rows.  accumulate: c += product."""
     code, E, cap, N, K = _gemm_sizes(kind, a, b, offsets, c)
     d = _device(a)
-    _call("moe_grouped_gemm", d, stream, code, _ptr(d, a), _ptr(d, b), _code(a.dtype), _ptr(d, offsets), E, cap, N, K,
-          _ptr(d, c), _code(c.dtype), 1 if accumulate else 0, _ptr(d, ws), 0 if ws is None else ws.nbytes)
+    pa, pb, po, pc, pw = _ptrs(d, a, b, offsets, c, ws)
+    _call("moe_grouped_gemm", d, stream, code, pa, pb, _code(a.dtype), po, E, cap, N, K, pc, _code(c.dtype),
+          1 if accumulate else 0, pw, 0 if ws is None else ws.nbytes)
 
 
 def moe_grouped_swiglu(x_perm, w13, offsets, h, gu=None, stream=None):
@@ -420,8 +426,8 @@ def moe_grouped_swiglu(x_perm, w13, offsets, h, gu=None, stream=None):
     if w13.dtype != t or h.dtype != t or (gu is not None and gu.dtype != t):
         raise ValueError("one type for every tensor")
     d = _device(x_perm)
-    _call("moe_grouped_swiglu", d, stream, _ptr(d, x_perm), _ptr(d, w13), _code(t), _ptr(d, offsets),
-          _groups(offsets, E), rows, H, I, _ptr(d, gu), _ptr(d, h))
+    px, pw, po, pg, ph = _ptrs(d, x_perm, w13, offsets, gu, h)
+    _call("moe_grouped_swiglu", d, stream, px, pw, _code(t), po, _groups(offsets, E), rows, H, I, pg, ph)
 
 
 def moe_grouped_swiglu_backward(dy_perm, w2, gu, offsets, dgu, stream=None):
@@ -434,8 +440,8 @@ def moe_grouped_swiglu_backward(dy_perm, w2, gu, offsets, dgu, stream=None):
     if w2.dtype != t or gu.dtype != t or dgu.dtype != t:
         raise ValueError("one type for every tensor")
     d = _device(dy_perm)
-    _call("moe_grouped_swiglu_backward", d, stream, _ptr(d, dy_perm), _ptr(d, w2), _ptr(d, gu), _code(t),
-          _ptr(d, offsets), _groups(offsets, E), rows, H, I, _ptr(d, dgu))
+    py, pw, pg, po, pd = _ptrs(d, dy_perm, w2, gu, offsets, dgu)
+    _call("moe_grouped_swiglu_backward", d, stream, py, pw, pg, _code(t), po, _groups(offsets, E), rows, H, I, pd)
 
 
 def moe_combine_backward(dout, y_perm, inv, topk_w, dy_perm, dtopk_w, stream=None):
@@ -452,8 +458,8 @@ def moe_combine_backward(dout, y_perm, inv, topk_w, dy_perm, dtopk_w, stream=Non
     if inv.dtype != torch.int32 or topk_w.dtype != torch.float32 or dtopk_w.dtype != torch.float32:
         raise ValueError("inv int32; weights float32")
     d = _device(dout)
-    _call("moe_combine_backward", d, stream, _ptr(d, dout), _ptr(d, y_perm), _code(t), T, H, k, cap, _ptr(d, inv),
-          _ptr(d, topk_w), _ptr(d, dy_perm), _ptr(d, dtopk_w))
+    po, py, pi, pw, pd, pg = _ptrs(d, dout, y_perm, inv, topk_w, dy_perm, dtopk_w)
+    _call("moe_combine_backward", d, stream, po, py, _code(t), T, H, k, cap, pi, pw, pd, pg)
 
 
 def moe_route_backward(logits, topk_ids, dtopk_w, params: moe_route_params, dlogits, stream=None):
@@ -467,8 +473,8 @@ def moe_route_backward(logits, topk_ids, dtopk_w, params: moe_route_params, dlog
     if logits.dtype != torch.float32 or dtopk_w.dtype != torch.float32 or topk_ids.dtype != torch.int32:
         raise ValueError("logits and dtopk_w float32, topk_ids int32")
     d = _device(logits)
-    _call("moe_route_backward", d, stream, _ptr(d, logits), T, _ptr(d, topk_ids), _ptr(d, dtopk_w), params,
-          _ptr(d, dlogits), _code(dlogits.dtype))
+    pl, pi, pw, pd = _ptrs(d, logits, topk_ids, dtopk_w, dlogits)
+    _call("moe_route_backward", d, stream, pl, T, pi, pw, params, pd, _code(dlogits.dtype))
 
 
 def adamw_params(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, seed=0) -> moe_adamw_params:
@@ -510,8 +516,7 @@ def moe_adamw_table(params, grads, m, v, m_scale=None, v_scale=None, master=None
         if ms is not None and (ms.dtype != torch.uint8 or vs.dtype != torch.uint8 or
                                not ms.numel() == vs.numel() == (size + 127) // 128):
             raise ValueError(f"tensor {i}: scales uint8 [ceil(n / 128)]")
-        entries[i] = moe_adamw_tensor(_ptr(d, p), _ptr(d, g), _ptr(d, mi), _ptr(d, vi), _ptr(d, ms), _ptr(d, vs),
-                                      _ptr(d, ma), size, _CODES[t], _CODES[gt], _CODES[mt])
+        entries[i] = moe_adamw_tensor(*_ptrs(d, p, g, mi, vi, ms, vs, ma), size, _CODES[t], _CODES[gt], _CODES[mt])
     nbytes = lib().moe_adamw_table_size(n)
     host = torch.zeros(nbytes, dtype=torch.uint8)
     _check(lib().moe_adamw_table_build(entries, n, host.data_ptr(), nbytes), "moe_adamw_table_build")
@@ -527,8 +532,7 @@ def moe_adamw_step(table: AdamWTable, hp: moe_adamw_params, step, lr_scale=None,
         if s is not None and (s.dtype != torch.float32 or s.numel() != 1):
             raise ValueError("lr_scale, grad_scale: one float32")
     d = table.device
-    _call("moe_adamw_step", d, stream, table.host_ptr, table.device_ptr, hp, _ptr(d, step), _ptr(d, lr_scale),
-          _ptr(d, grad_scale))
+    _call("moe_adamw_step", d, stream, table.host_ptr, table.device_ptr, hp, *_ptrs(d, step, lr_scale, grad_scale))
 
 
 class DboContext:

@@ -317,7 +317,8 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
 // 4 x 16 block and each gets the four reduction steps of one column).
 // Swizzles, so that the addresses of one read spread over the banks: RCONT
 // XORs the 16-byte chunk with the row; the other XORs the 32-byte chunk with
-// (step & 3) + 4 * (step >> 3 & 1), the eight steps that half a wave reads.
+// (step & 3) + 4 * (step >> 3 & 1), the eight steps that half a wave reads
+// (64 positions: two steps share a 256-byte row of banks, see key32).
 // USED: positions that hold anything (RCONT only: the others are not loaded).
 template <bool RCONT, int BT, int BK, int NW, int USED = BT>
 struct Operand {
@@ -326,10 +327,14 @@ struct Operand {
   static constexpr int NQ = (ROWS + RPD * NW - 1) / (RPD * NW);   // DMAs per wave and stage
   static constexpr int BYTES = BT * BK * 2;
   static_assert(NQ * NW * RPD <= (RCONT ? BT : BK), "DMA split");
-  static_assert(RCONT || COLS >= 128, "transposing reads: 8 chunks of 32 bytes");
+  static_assert(RCONT || COLS >= 64, "transposing reads: at least 4 chunks of 32 bytes");
 
+  // the XOR that row r (a reduction step) puts on its 32-byte chunks
+  static __device__ __forceinline__ int key32(int r) {
+    return COLS == 64 ? (r >> 1 & 1) | ((r >> 3 & 1) << 1) : (r & 3) | ((r >> 3 & 1) << 2);
+  }
   // RCONT: the XOR that row r puts on its 16-byte chunks
-  static __device__ __forceinline__ int swz(int r) { return BK == 32 ? (r >> 2) & 3 : r & 7; }
+  static __device__ __forceinline__ int swz(int r) { return r & (BK == 128 ? 15 : 7); }
 
   const bf16_t* base;       // uniform
   uint32_t off[NQ];         // this lane's chunks: byte offsets from the stage's base
@@ -350,8 +355,7 @@ struct Operand {
       if constexpr (RCONT) {
         off[i] = (static_cast<uint32_t>(row(R)) * static_cast<uint32_t>(ld) + (pos ^ swz(R)) * 8) * 2;
       } else {
-        const int key = (R & 3) | ((R >> 3 & 1) << 2);
-        int col = t0 + (((pos >> 1) ^ key) << 4) + (pos & 1) * 8;
+        int col = t0 + (((pos >> 1) ^ key32(R)) << 4) + (pos & 1) * 8;
         col = min(col, limit - 8);
         off[i] = (static_cast<uint32_t>(R) * static_cast<uint32_t>(ld) + col) * 2;
       }
@@ -388,9 +392,9 @@ struct Operand {
       return *reinterpret_cast<const bf16x8_t*>(&T[r * BK + (((kk * 4 + (lane >> 4)) ^ swz(r)) << 3)]);
     } else {
       const int g = lane >> 4, L = lane & 15;
-      const int key = (L >> 2) | ((g & 1) << 2);
       const int r = kk * 32 + g * 8 + (L >> 2);
-      const bf16_t* a = T + r * COLS + (((pos >> 4) ^ key) << 4) + (L & 3) * 4;
+      // (the step four further on has the same key; the key does not depend on kk)
+      const bf16_t* a = T + r * COLS + (((pos >> 4) ^ key32(g * 8 + (L >> 2))) << 4) + (L & 3) * 4;
       typedef __attribute__((address_space(3))) s16x4_t* lds4;
       const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(a));
       const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(a + 4 * COLS));
@@ -401,10 +405,12 @@ struct Operand {
 
 // Tile BM x BN, BK reduction steps per stage, WAVES_M x WAVES_N waves, a ring
 // of NBUF stages (stage s in buffer s % NBUF).  TM: 16-position subtiles of
-// the first axis per wave that hold anything.
-template <int KIND, int EPI, int BM, int BN, int BK, int WAVES_M, int WAVES_N, int NBUF, int TM>
+// the first axis per wave that hold anything.  WAVES_K = 2: twice the waves;
+// each half takes half of every stage's steps, and the halves' sums are joined
+// through LDS (subtile i by half i & 1).
+template <int KIND, int EPI, int BM, int BN, int BK, int WAVES_M, int WAVES_N, int WAVES_K, int NBUF, int TM>
 __device__ __forceinline__ void gg_tile(const GgParams& p, const GgTile& t, uint8_t* lds) {
-  constexpr int NW = WAVES_M * WAVES_N;
+  constexpr int NW = WAVES_M * WAVES_N * WAVES_K;
   constexpr int WM = TM * 16, WN = BN / WAVES_N, TN = WN / 16;
   using OpA = Operand<KIND != MOE_GEMM_TN, BM, BK, NW, TM * 16 * WAVES_M>;
   using OpB = Operand<KIND == MOE_GEMM_NT, BN, BK, NW>;
@@ -412,7 +418,7 @@ __device__ __forceinline__ void gg_tile(const GgParams& p, const GgTile& t, uint
   static_assert((NBUF - 1) * NDMA < 64, "vmcnt");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / WAVES_N, wn = wave % WAVES_N;
+  const int wk = wave / (WAVES_M * WAVES_N), wm = wave / WAVES_N % WAVES_M, wn = wave % WAVES_N;
   const int nout = KIND == MOE_GEMM_TN ? p.K : p.N;              // positions on the second output axis
   const int red = KIND == MOE_GEMM_TN ? t.rows : p.K;            // reduction length
   const int KT_all = (red + BK - 1) / BK;
@@ -420,8 +426,7 @@ __device__ __forceinline__ void gg_tile(const GgParams& p, const GgTile& t, uint
   const int per_split = (KT_all + p.splits - 1) / p.splits;
   const int kt0 = min(t.split * per_split, KT_all);
   const int end = min(red, (kt0 + per_split) * BK);              // reduction steps behind it are zeros
-  int KT = min(per_split, KT_all - kt0);
-  if (BK == 32) KT += KT & 1;                                    // the main loop takes two such stages at a time
+  const int KT = min(per_split, KT_all - kt0);
 
   OpA a;
   OpB b;
@@ -477,13 +482,14 @@ __device__ __forceinline__ void gg_tile(const GgParams& p, const GgTile& t, uint
   // read ahead into a second set: LDS reads are spread between the MFMAs and
   // 192 registers hold a 128 x 64 wave tile.  In a stage's last step half of
   // the MFMAs run before the barrier that hands the stage's buffer back.
-  constexpr int KK = BK / 32;
+  constexpr int KK = BK / 32 / WAVES_K;              // steps of a stage that this wave takes
+  static_assert(KK % 2 == 0, "the second operand's sets in turn");
   bf16x8_t af[TM], bfr[2][TN];
   auto at_a = [&](int kt) { return lds + (kt % NBUF) * STAGE; };
-  auto read_a = [&](int kt, int kk, int i) { af[i] = OpA::frag(at_a(kt), wm * WM + i * 16, kk); };
+  auto read_a = [&](int kt, int kk, int i) { af[i] = OpA::frag(at_a(kt), wm * WM + i * 16, wk * KK + kk); };
   auto read_b = [&](int kt, int kk, int set) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) bfr[set][j] = OpB::frag(at_a(kt) + OpA::BYTES, b_pos(j), kk);
+    for (int j = 0; j < TN; ++j) bfr[set][j] = OpB::frag(at_a(kt) + OpA::BYTES, b_pos(j), wk * KK + kk);
   };
   auto mfmas = [&](int i, int set) {
 #pragma unroll
@@ -491,13 +497,12 @@ __device__ __forceinline__ void gg_tile(const GgParams& p, const GgTile& t, uint
       acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bfr[set][j], af[i], acc[i][j], 0, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
-  // Stage kt, whose first step's fragments of the second operand are in set
-  // `first`.  (The last stage reads a stage that does not exist: bytes of the
-  // ring that nothing uses.)
-  auto stage = [&](int kt, auto first) {
+  // (The last stage reads a stage that does not exist: bytes of the ring that
+  // nothing uses.)
+  auto stage = [&](int kt) {
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
-      const int set = (decltype(first)::value + kk) & 1;
+      const int set = kk & 1;
       if (kk + 1 < KK) {
         read_b(kt, kk + 1, set ^ 1);
         __builtin_amdgcn_sched_barrier(0);
@@ -535,18 +540,8 @@ __device__ __forceinline__ void gg_tile(const GgParams& p, const GgTile& t, uint
     read_b(0, 0, 0);
 #pragma unroll
     for (int i = 0; i < TM; ++i) read_a(0, 0, i);
-    using Set0 = std::integral_constant<int, 0>;
-    using Set1 = std::integral_constant<int, 1>;
-    if constexpr (KK % 2 == 0) {
 #pragma unroll 1
-      for (int kt = 0; kt < KT; ++kt) stage(kt, Set0{});
-    } else {
-#pragma unroll 1
-      for (int kt = 0; kt < KT; kt += 2) {
-        stage(kt, Set0{});
-        stage(kt + 1, Set1{});
-      }
-    }
+    for (int kt = 0; kt < KT; ++kt) stage(kt);
   }
 
   // Epilogue.  An accumulator lane holds four columns of one of 16 rows, 32
@@ -590,15 +585,34 @@ __device__ __forceinline__ void gg_tile(const GgParams& p, const GgTile& t, uint
       }
     }
   };
+  auto mine = [&](int i) { return WAVES_K == 1 || (i & 1) == wk; };
   if (reads) {
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) read_old(i);
+    for (int i = 0; i < AHEAD; ++i)
+      if (mine(i)) read_old(i);
   }
   __syncthreads();                                   // the ring is free
-  float* turn = reinterpret_cast<float*>(lds) + wave * 16 * WN;
+  constexpr int JOIN = WAVES_K == 1 ? 0 : NW * TM * TN * 1024;
+  static_assert(JOIN + NW * 16 * WN * 4 <= NBUF * STAGE, "epilogue scratch");
+  if constexpr (WAVES_K == 2) {
+    f32x4_t* slot = reinterpret_cast<f32x4_t*>(lds);
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+      if (!mine(i))
+#pragma unroll
+        for (int j = 0; j < TN; ++j) slot[((wave * TM + i) * TN + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+      if (mine(i))
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] += slot[(((wave ^ (NW / 2)) * TM + i) * TN + j) * 64 + lane];
+  }
+  float* turn = reinterpret_cast<float*>(lds + JOIN) + wave * 16 * WN;
   auto chunk = [&](int r, int c) { return reinterpret_cast<f32x4_t*>(turn + r * WN + ((c ^ (r & (CH - 1))) << 2)); };
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
+    if (!mine(i)) continue;
 #pragma unroll
     for (int j = 0; j < TN; ++j) *chunk(lane & 15, j * 4 + (lane >> 4)) = acc[i][j];
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -639,33 +653,34 @@ __device__ __forceinline__ void gg_tile(const GgParams& p, const GgTile& t, uint
         }
       }
     }
-    if (reads && i + AHEAD < TM) read_old(i + AHEAD);
+    if (reads && i + AHEAD < TM) read_old(i + AHEAD);   // (two halves: AHEAD is all of them)
     __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <int KIND, int EPI, int BM, int BN, int BK, int WAVES_M, int WAVES_N, int NBUF, int TM>
+template <int KIND, int EPI, int BM, int BN, int BK, int WAVES_M, int WAVES_N, int WAVES_K, int NBUF, int TM>
 __device__ __forceinline__ void gg_tile_of(int tm, const GgParams& p, const GgTile& t, uint8_t* lds) {
   if constexpr (TM == 1) {
-    gg_tile<KIND, EPI, BM, BN, BK, WAVES_M, WAVES_N, NBUF, 1>(p, t, lds);
+    gg_tile<KIND, EPI, BM, BN, BK, WAVES_M, WAVES_N, WAVES_K, NBUF, 1>(p, t, lds);
   } else {
     if (tm == TM)
-      gg_tile<KIND, EPI, BM, BN, BK, WAVES_M, WAVES_N, NBUF, TM>(p, t, lds);
+      gg_tile<KIND, EPI, BM, BN, BK, WAVES_M, WAVES_N, WAVES_K, NBUF, TM>(p, t, lds);
     else
-      gg_tile_of<KIND, EPI, BM, BN, BK, WAVES_M, WAVES_N, NBUF, TM - 1>(tm, p, t, lds);
+      gg_tile_of<KIND, EPI, BM, BN, BK, WAVES_M, WAVES_N, WAVES_K, NBUF, TM - 1>(tm, p, t, lds);
   }
 }
 
-template <int KIND, int EPI, int BM, int BN, int BK, int WAVES_M, int WAVES_N, int NBUF, int MINW>
-__global__ __launch_bounds__(WAVES_M * WAVES_N * 64, MINW) void k_grouped_gemm(GgParams p) {
+template <int KIND, int EPI, int BM, int BN, int BK, int WAVES_M, int WAVES_N, int WAVES_K, int NBUF>
+__global__ __launch_bounds__(WAVES_M * WAVES_N * WAVES_K * 64, 2) void k_grouped_gemm(GgParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[NBUF * (BM + BN) * BK * 2];
   GgTile t;
   if (!gg_locate<KIND, BM>(p, reinterpret_cast<int*>(lds), t)) return;
   constexpr int TM = BM / WAVES_M / 16;
   if constexpr (KIND == MOE_GEMM_TN)
-    gg_tile<KIND, EPI, BM, BN, BK, WAVES_M, WAVES_N, NBUF, TM>(p, t, lds);
+    gg_tile<KIND, EPI, BM, BN, BK, WAVES_M, WAVES_N, WAVES_K, NBUF, TM>(p, t, lds);
   else
-    gg_tile_of<KIND, EPI, BM, BN, BK, WAVES_M, WAVES_N, NBUF, TM>((t.m_n + 16 * WAVES_M - 1) / (16 * WAVES_M), p, t, lds);
+    gg_tile_of<KIND, EPI, BM, BN, BK, WAVES_M, WAVES_N, WAVES_K, NBUF, TM>((t.m_n + 16 * WAVES_M - 1) / (16 * WAVES_M),
+                                                                          p, t, lds);
 }
 
 // ---- fp32 -------------------------------------------------------------------
@@ -911,12 +926,15 @@ static GgPlan gg_plan(int kind, int epi, bool f32, int E, int64_t cap, bool dens
   else if (cols > 128 && (kind == MOE_GEMM_TN ? N > 128 : rows > 128) &&
            gg_tiles(kind, epi, E, cap, dense, N, K, 256, 256) >= 256)
     q.BM = q.BN = 256;
+  else if (gg_tiles(kind, epi, E, cap, dense, N, K, 64, 128) <= 128)
+    q.BM = 64;
   q.tiles = gg_tiles(kind, epi, E, cap, dense, N, K, q.BM, q.BN);
   // The reduction is cut into parts, doubled while the grid has fewer than 256
-  // workgroups and each part keeps at least 256 steps, at most 16.
-  const int64_t red = kind == MOE_GEMM_TN ? rows : K;
+  // workgroups (64-row tiles, one a compute unit: as long as it stays within
+  // 256) and each part keeps at least 256 steps, at most 16.
+  const int64_t red = kind == MOE_GEMM_TN ? rows : K, limit = q.BM == 64 && !f32 ? 129 : 256;
   if (epi == EPI_STORE && !(f32 && q.BM == 32))
-    while (q.splits < 16 && q.tiles * q.splits < 256 && red / (2 * q.splits) >= 256) q.splits *= 2;
+    while (q.splits < 16 && q.tiles * q.splits < limit && red / (2 * q.splits) >= 256) q.splits *= 2;
   return q;
 }
 
@@ -934,11 +952,13 @@ static moe_status gg_launch(GgParams& p, const GgPlan& q, bool f32, hipStream_t 
     if constexpr (KIND != MOE_GEMM_TN)
       hipLaunchKernelGGL((k_grouped_gemm_f32_few<KIND, EPI>), grid, dim3(256), 0, s, p);
   } else if (q.BM == 256) {
-    hipLaunchKernelGGL((k_grouped_gemm<KIND, EPI, 256, 256, 64, 2, 4, 2, 2>), grid, dim3(512), 0, s, p);
+    hipLaunchKernelGGL((k_grouped_gemm<KIND, EPI, 256, 256, 64, 2, 4, 1, 2>), grid, dim3(512), 0, s, p);
   } else if (q.BM == 128) {
-    hipLaunchKernelGGL((k_grouped_gemm<KIND, EPI, 128, 128, 64, 2, 2, 2, 2>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((k_grouped_gemm<KIND, EPI, 128, 128, 64, 2, 2, 1, 2>), grid, dim3(256), 0, s, p);
+  } else if (q.BM == 64) {
+    hipLaunchKernelGGL((k_grouped_gemm<KIND, EPI, 64, 128, 128, 2, 2, 2, 3>), grid, dim3(512), 0, s, p);
   } else if constexpr (KIND != MOE_GEMM_TN) {
-    hipLaunchKernelGGL((k_grouped_gemm<KIND, EPI, 32, 128, 64, 1, 4, 3, 2>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((k_grouped_gemm<KIND, EPI, 32, 128, 64, 1, 4, 1, 3>), grid, dim3(256), 0, s, p);
   }
   DBOMOE_CHECK_LAUNCH();
   if (q.splits > 1) {

@@ -129,6 +129,7 @@ def test_grouped_gemm_weights(name, dt):
 
 # Enough and large enough experts for the 256 x 256 tiles: row counts around
 # one, two and several tiles, odd widths, reductions that end inside a stage.
+MID = [(i * 29) % 131 for i in range(60)]                  # 128 x 128 tiles
 BIG = [0, 1, 15, 16, 17, 31, 33, 255, 256, 257, 511, 513, 700, 1030, 2049] + [(i * 97) % 331 for i in range(45)]
 
 
@@ -141,11 +142,13 @@ def _ref_rows(kind, a, b, counts):
     return ref, mag
 
 
-@pytest.mark.parametrize("N,K", [(520, 72), (1032, 200), (264, 328)])
+@pytest.mark.parametrize("N,K,counts", [(520, 72, BIG), (1032, 200, BIG), (264, 328, BIG), (648, 200, MID), (88, 136, MID)],
+                         ids=lambda v: "x" if isinstance(v, list) else str(v))
 @pytest.mark.parametrize("kind", ["nt", "nn", "tn"])
-def test_grouped_gemm_large_tiles(kind, N, K):
+def test_grouped_gemm_large_tiles(kind, N, K, counts):
     B = _B()
     g = torch.Generator().manual_seed(N + K)
+    BIG = counts
     M, off = sum(BIG), offsets_of(BIG).cuda()
     for out, acc in ((BF, False), (F32, True)):
         print(f"{kind} large N={N} K={K} {out}", flush=True)
@@ -173,10 +176,12 @@ def test_grouped_gemm_large_tiles(kind, N, K):
             assert torch.equal(c[M:].cpu(), c0[M:])
 
 
-@pytest.mark.parametrize("I,H", [(520, 72), (264, 328)])
-def test_grouped_swiglu_large_tiles(I, H):
+@pytest.mark.parametrize("I,H,counts", [(520, 72, BIG), (264, 328, BIG), (648, 200, MID)],
+                         ids=lambda v: "x" if isinstance(v, list) else str(v))
+def test_grouped_swiglu_large_tiles(I, H, counts):
     B = _B()
     g = torch.Generator().manual_seed(I + H)
+    BIG = counts
     M, off = sum(BIG), offsets_of(BIG).cuda()
     x, w13 = rnd(g, M, H, dt=BF), rnd(g, len(BIG), 2 * I, H, dt=BF, std=H ** -0.5)
     gu, h = torch.zeros(M, 2 * I, dtype=BF, device="cuda"), torch.zeros(M, I, dtype=BF, device="cuda")
