@@ -403,6 +403,10 @@ def moe_grouped_gemm_workspace_size(kind: str, a, b, offsets, c) -> int:
     return lib().moe_grouped_gemm_workspace_size(code, _code(a.dtype), int(offsets is None), E, cap, N, K)
 
 
+# No call's workspace is larger: a split product has fewer than 512 tiles of at most 128 x 128 fp32 partial sums.
+GEMM_MAX_WORKSPACE = 512 * 128 * 128 * 4
+
+
 def moe_grouped_gemm(kind: str, a, b, offsets, c, ws=None, accumulate=False, stream=None):
     """Matrix products grouped by expert; rows [offsets[e], offsets[e+1]) belong to expert e.
 

@@ -26,7 +26,9 @@ class TrainLayer:
     forward(x) -> out [T, H]; backward(dout) -> dx [T, H], adding to the
     gradients in `grads` (zero_grad() starts them anew); step() updates the
     weights and zeroes the gradients.  Outputs live in the layer's buffers
-    until the next call.
+    until the next call; x must stay as it is until backward().  Calls run on the
+    current stream of the layer's device; calls of one layer on several streams
+    need the caller's ordering.
     """
 
     def __init__(self, inp: dict, device: str = "cuda", T_max: int = None, grad_dtype=torch.float32,
@@ -41,10 +43,12 @@ class TrainLayer:
             raise ValueError("trainable weights are float32 or bfloat16, in the activations' type")
         if states not in ("f32", "fp8"):
             raise ValueError("states: f32 or fp8")
+        self.logit_bias, self.forced_ids = _dev(inp.get("logit_bias"), d), _dev(inp.get("forced_ids"), d)
+        if self.logit_bias is not None and (self.logit_bias.dtype != torch.float32 or self.logit_bias.numel() != cfg.E):
+            raise ValueError(f"logit_bias: float32 [{cfg.E}]")
         if cfg.E % (8 if act == torch.bfloat16 else 4):
             raise ValueError("the number of experts must be a multiple of 8 (float32: 4)")
         self.act, self.T_max = act, T_max or inp["x"].shape[0]
-        self.logit_bias, self.forced_ids = _dev(inp.get("logit_bias"), d), _dev(inp.get("forced_ids"), d)
         sh13, sh2, shI = concat_shared(inp.get("shared_w13") or [], inp.get("shared_w2") or [])
         own = lambda t: None if t is None else t.contiguous().to(d, copy=True)   # trained in place
         self.weights = {"w_router": own(inp["w_router"])[None], "w13": own(inp["w13"]), "w2": own(inp["w2"])}
@@ -67,7 +71,7 @@ class TrainLayer:
             self.buf.update(sh_gu=new(T, 2 * shI), sh_h=new(T, shI), sh_out=new(T, H), sh_dgu=new(T, 2 * shI))
         self.ws_route = new(max(B.moe_route_workspace_size(T, H, E), 256), dt=torch.uint8)
         self.ws_dispatch = new(max(B.moe_dispatch_workspace_size(T, k, E_loc), 256), dt=torch.uint8)
-        self.ws_gemm = new(256, dt=torch.uint8)
+        self.ws_gemm = new(B.GEMM_MAX_WORKSPACE, dt=torch.uint8)      # whatever the number of tokens
 
         self.grads = {name: torch.zeros(w.shape, dtype=grad_dtype, device=d) for name, w in self.weights.items()}
         self.fresh = True                     # no gradient has been added since zero_grad()
@@ -87,9 +91,6 @@ class TrainLayer:
         self.T = 0
 
     def _gemm(self, kind, a, b, offsets, c, accumulate=False):
-        need = B.moe_grouped_gemm_workspace_size(kind, a, b, offsets, c)
-        if need > self.ws_gemm.numel():
-            self.ws_gemm = torch.empty(need, dtype=torch.uint8, device=self.device)
         B.moe_grouped_gemm(kind, a, b, offsets, c, self.ws_gemm, accumulate=accumulate)
         return c
 
@@ -111,6 +112,10 @@ class TrainLayer:
         logits, ids, w, perm, inv, x_perm, gu, h, y_perm, out = self._rows(
             "logits", "ids", "w", "perm", "inv", "x_perm", "gu", "h", "y_perm", "out")
         forced = self.forced_ids if forced_ids is None else forced_ids
+        if forced is not None and (forced.dtype != torch.int32 or forced.dim() != 2 or forced.shape[0] < self.T or
+                                   forced.shape[1] != cfg.k):
+            self.T = 0
+            raise ValueError(f"forced_ids: int32 [{x.shape[0]}, {cfg.k}]")
         B.moe_route_topk(x, W["w_router"], self.route, ids, w, self.ws_route, logits_out=logits,
                          logit_bias=self.logit_bias, forced_ids=forced)
         B.moe_dispatch(x, ids, cfg.E, cfg.expert_begin, cfg.expert_end, self.buf["counts"], self.offsets, perm, inv,

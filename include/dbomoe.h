@@ -296,8 +296,9 @@ moe_status moe_combine(const void* y_perm, moe_dtype act, int64_t T, int32_t H, 
  *   accumulate  0: c = product; 1: c = c + product, rounded once
  *   ws   moe_grouped_gemm_workspace_size(...) bytes of the same arguments
  *        (dense: 1 if offsets is NULL): fp32 partial products where the output
- *        has few tiles and the reduction is long; 0 bytes otherwise, then ws
- *        may be NULL
+ *        has few tiles and the reduction is long (never more than 32 MiB); 0
+ *        bytes otherwise, then ws may be NULL.  Calls that may overlap need a
+ *        workspace each
  * Sums are fp32, rounded once to ct, and do not depend on timing.  NT / NN
  * leave c's rows outside the experts' ranges untouched; TN writes zeros for an
  * expert without rows (accumulate: leaves it as it is).  N and K are multiples

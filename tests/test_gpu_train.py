@@ -272,6 +272,60 @@ def test_grouped_gemm_split_reduction(kind, cap, N, K):
         check(outs[0], ref, mag, max(cap, K) + 32, "split")
 
 
+def test_grouped_gemm_graph_replays_and_streams():
+    """A split and an unsplit product captured in one graph and replayed with new inputs and new offsets between
+    eager calls; then the same two products on two streams at once."""
+    B = _B()
+    g = torch.Generator().manual_seed(12)
+    counts = [[100, 0, 333, 67], [0, 250, 1, 249], [500, 0, 0, 0]]
+    a, b = rnd(g, 500, 136, dt=BF).cuda(), rnd(g, 500, 264, dt=BF).cuda()
+    w = rnd(g, 4, 264, 136, dt=BF).cuda()
+    x2, y2 = rnd(g, 4096, 72, dt=BF).cuda(), rnd(g, 4096, 136, dt=BF).cuda()
+    off = offsets_of(counts[0]).cuda()
+    c, d, e = torch.zeros(4, 136, 264, device="cuda"), torch.zeros(500, 264, dtype=BF, device="cuda"), \
+        torch.zeros(1, 72, 136, device="cuda")
+    need = B.moe_grouped_gemm_workspace_size("tn", x2, y2, None, e)
+    assert need > 0
+    ws, ws2 = (torch.zeros(need, dtype=torch.uint8, device="cuda") for _ in range(2))
+
+    def run(c, d, e, ws):
+        B.moe_grouped_gemm("tn", a, b, off, c)
+        B.moe_grouped_gemm("nt", a, w, off, d)
+        B.moe_grouped_gemm("tn", x2, y2, None, e, ws)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run(c, d, e, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(c, d, e, ws)
+    for k in (1, 2, 0, 1):
+        off.copy_(offsets_of(counts[k]))
+        for t in (a, b, x2, y2):
+            t.copy_(rnd(g, *t.shape, dt=BF))
+        want = [torch.zeros_like(t) for t in (c, d, e)]
+        run(*want, ws2)
+        torch.cuda.synchronize()
+        for t in (c, d, e):
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        for t, u in zip((c, d, e), want):
+            assert torch.equal(t, u)
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        got = [[torch.zeros_like(t) for t in (c, d, e)] for _ in range(2)]
+        torch.cuda.synchronize()
+        for s, outs, wk in ((s1, got[0], ws), (s2, got[1], ws2)):
+            with torch.cuda.stream(s):
+                for _ in range(5):
+                    run(*outs, wk)
+        torch.cuda.synchronize()
+        for outs in got:
+            for t, u in zip(outs, want):
+                assert torch.equal(t, u)
+
+
 def _sigmoid(g):
     return 1.0 / (1.0 + torch.exp(-g))
 
@@ -765,6 +819,56 @@ def test_train_layer_step_changes_the_forward(states, master):
     assert not torch.equal(before, after)
     with pytest.raises(RuntimeError):
         layer.step()
+
+
+def test_train_layer_refuses_short_forced_ids():
+    from combine_dual_overlap_amd import TrainLayer
+    _B()
+    cfg, inp = _layer_inputs(2, "bf16", forced=True)
+    layer = TrainLayer(inp, T_max=2 * cfg.T)
+    x = inp["x"].repeat(2, 1).cuda()
+    with pytest.raises(ValueError):
+        layer.forward(x)                                      # ids of half of these tokens
+    with pytest.raises(RuntimeError):
+        layer.backward(x)
+    with pytest.raises(ValueError):
+        layer.forward(torch.cat([x, x]))                      # more than T_max
+    with pytest.raises(ValueError):
+        layer.forward(x[:, :128].contiguous())
+
+
+def test_train_layer_step_in_a_graph():
+    """Forward, backward and step captured once and replayed three times equal three eager steps."""
+    from combine_dual_overlap_amd import TrainLayer
+    _B()
+    cfg, inp = _layer_inputs(2, "bf16", forced=False)
+    g = torch.Generator().manual_seed(8)
+    kw = dict(states="fp8", master=False, lr=2.0 ** -8)
+    x, dout = inp["x"].cuda(), rnd(g, *inp["x"].shape, dt=BF).cuda()
+    a, b, warm = TrainLayer(inp, **kw), TrainLayer(inp, **kw), TrainLayer(inp, **kw)
+
+    def one(layer):
+        layer.forward(x)
+        layer.backward(dout)
+        layer.step()
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        one(warm)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one(b)
+    for _ in range(3):
+        x.copy_(rnd(g, *x.shape, dt=BF))
+        one(a)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a.buf["out"], b.buf["out"])
+        for n in a.weights:
+            assert torch.equal(a.weights[n], b.weights[n]), n
+        for p, q in zip(a.m + a.v + a.m_scale + a.v_scale, b.m + b.v + b.m_scale + b.v_scale):
+            assert torch.equal(p.view(torch.uint8), q.view(torch.uint8))
 
 
 def test_train_layer_fewer_tokens_and_another_stream():

@@ -196,6 +196,20 @@ def test_binding_refuses_shapes_and_types():
             B.moe_adamw_table(**{**ok, **kw})
 
 
+def test_grouped_gemm_workspace_bound():
+    """No call needs more than the bound that callers allocate once."""
+    B = _B()
+    import random
+    r = random.Random(1)
+    largest = 0
+    for _ in range(20000):
+        lg = lambda hi: int(2 ** r.uniform(0, hi))
+        dense = r.random() < 0.4
+        args = (r.randrange(3), r.choice([0, 1]), int(dense), 1 if dense else r.randint(1, 256), lg(20), 8 * lg(13), 8 * lg(13))
+        largest = max(largest, B.lib().moe_grouped_gemm_workspace_size(*args))
+    assert 8 << 20 < largest <= B.GEMM_MAX_WORKSPACE
+
+
 def test_train_layer_refuses_what_it_cannot_train():
     import workloads as W
     from combine_dual_overlap_amd import TrainLayer
