@@ -129,20 +129,29 @@ __device__ __forceinline__ uint64_t encode8(const float* y, const uint32_t* r) {
   return static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32 | static_cast<uint32_t>(lo);
 }
 
+// STREAM: accesses that the caches need not keep.  With 8-bit states (a state
+// byte is next used one step later) they took 42 M parameters from 91.7 to
+// 86.7 us; with fp32 states the same hint cost 15 %.
+template <bool STREAM, typename T>
+__device__ __forceinline__ T read_as(const void* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(static_cast<const T*>(p));
+  return *static_cast<const T*>(p);
+}
+
 // 8 elements from index i on; those behind n read as zero.  FULL: none is.
-template <bool BF16, bool FULL>
+template <bool BF16, bool FULL, bool STREAM>
 __device__ __forceinline__ void load8(const void* base, int64_t i, int64_t n, float* x) {
   if (FULL || i + 8 <= n) {
     if constexpr (BF16) {
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(static_cast<const bf16_t*>(base) + i);
+      const u32x4_t v = read_as<STREAM, u32x4_t>(static_cast<const bf16_t*>(base) + i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         x[2 * j] = __uint_as_float(v[j] << 16);
         x[2 * j + 1] = __uint_as_float(v[j] & 0xffff0000u);
       }
     } else {
-      const f32x4_t* s = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(base) + i);
-      const f32x4_t a = s[0], b = s[1];
+      const float* s = static_cast<const float*>(base) + i;
+      const f32x4_t a = read_as<STREAM, f32x4_t>(s), b = read_as<STREAM, f32x4_t>(s + 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         x[j] = a[j];
@@ -185,7 +194,7 @@ __device__ __forceinline__ void store8_bf16(bf16_t* base, int64_t i, int64_t n, 
 
 template <bool FULL>
 __device__ __forceinline__ uint64_t load8_codes(const uint8_t* base, int64_t i, int64_t n) {
-  if (FULL || i + 8 <= n) return *reinterpret_cast<const uint64_t*>(base + i);
+  if (FULL || i + 8 <= n) return read_as<true, uint64_t>(base + i);
   uint64_t v = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -196,7 +205,7 @@ __device__ __forceinline__ uint64_t load8_codes(const uint8_t* base, int64_t i, 
 template <bool FULL>
 __device__ __forceinline__ void store8_codes(uint8_t* base, int64_t i, int64_t n, uint64_t q) {
   if (FULL || i + 8 <= n) {
-    *reinterpret_cast<uint64_t*>(base + i) = q;
+    __builtin_nontemporal_store(q, reinterpret_cast<uint64_t*>(base + i));
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -250,7 +259,7 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
   auto group = [&](int64_t i, auto full) {
     constexpr bool FULL = decltype(full)::value;
     float g[8], m[8], v[8], p[8], root[8];
-    load8<GRAD_BF16, FULL>(t.g, i, n, g);
+    load8<GRAD_BF16, FULL, EIGHT>(t.g, i, n, g);
     if constexpr (EIGHT) {
       const uint64_t qm = load8_codes<FULL>(static_cast<const uint8_t*>(t.m), i, n);
       const uint64_t qv = load8_codes<FULL>(static_cast<const uint8_t*>(t.v), i, n);
@@ -259,13 +268,13 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = v[j] * v[j];
     } else {
-      load8<false, FULL>(t.m, i, n, m);
-      load8<false, FULL>(t.v, i, n, v);
+      load8<false, FULL, EIGHT>(t.m, i, n, m);
+      load8<false, FULL, EIGHT>(t.v, i, n, v);
     }
     if constexpr (PARAM == PARAM_MASTER)
-      load8<false, FULL>(t.master, i, n, p);
+      load8<false, FULL, EIGHT>(t.master, i, n, p);
     else
-      load8<PARAM == PARAM_BF16, FULL>(t.p, i, n, p);
+      load8<PARAM == PARAM_BF16, FULL, EIGHT>(t.p, i, n, p);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float gj = g[j] * gs;

@@ -248,10 +248,21 @@ __device__ __forceinline__ void store_swiglu_bwd(const GgParams& p, int64_t row,
   store4<F32>(p.C, gi + p.N, du);
 }
 
-// Eight columns of a bf16 row.
+// Eight columns of a row.  STREAM (weight gradients, which the optimizer reads
+// much later): a store that the caches need not keep; the skewed layer's gate/up
+// gradient 557 -> 528 us.  (The same for gate/up outputs cost 2 %.)
+template <bool STREAM, typename T>
+__device__ __forceinline__ void write_as(void* p, const T& v) {
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(v, static_cast<T*>(p));
+  else
+    *static_cast<T*>(p) = v;
+}
+
+template <bool STREAM = false>
 __device__ __forceinline__ void store8(void* base, int64_t i, const f32x4_t& a, const f32x4_t& b) {
-  *reinterpret_cast<u32x4_t*>(static_cast<bf16_t*>(base) + i) =
-      u32x4_t{cvt_bf16x2(a[0], a[1]), cvt_bf16x2(a[2], a[3]), cvt_bf16x2(b[0], b[1]), cvt_bf16x2(b[2], b[3])};
+  write_as<STREAM>(static_cast<bf16_t*>(base) + i, u32x4_t{cvt_bf16x2(a[0], a[1]), cvt_bf16x2(a[2], a[3]),
+                                                           cvt_bf16x2(b[0], b[1]), cvt_bf16x2(b[2], b[3])});
 }
 
 __device__ __forceinline__ void unpack8(const u32x4_t& v, f32x4_t& a, f32x4_t& b) {
@@ -640,8 +651,8 @@ __device__ __forceinline__ void gg_tile(const GgParams& p, const GgTile& t, uint
             v0 += __builtin_bit_cast(f32x4_t, o[0]);
             v1 += __builtin_bit_cast(f32x4_t, o[1]);
           }
-          store4<true>(p.C, at_c, v0);
-          store4<true>(p.C, at_c + 4, v1);
+          write_as<KIND == MOE_GEMM_TN>(static_cast<float*>(p.C) + at_c, v0);
+          write_as<KIND == MOE_GEMM_TN>(static_cast<float*>(p.C) + at_c + 4, v1);
         } else {
           if (reads) {
             f32x4_t c0, c1;
@@ -649,7 +660,7 @@ __device__ __forceinline__ void gg_tile(const GgParams& p, const GgTile& t, uint
             v0 += c0;
             v1 += c1;
           }
-          store8(p.C, at_c, v0, v1);
+          store8<KIND == MOE_GEMM_TN>(p.C, at_c, v0, v1);
         }
       }
     }

@@ -416,7 +416,7 @@ def test_swiglu_backward_formula_against_differences():
 # ------------------------------------------------------------------ combine, router
 
 @pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("T,H,k", [(1, 8, 1), (3, 1000, 2), (129, 520, 7), (17, 2048, 16), (5, 16384, 3)])
+@pytest.mark.parametrize("T,H,k", [(1, 8, 1), (3, 1000, 2), (129, 520, 7), (17, 2048, 16), (5, 16384, 3), (1100, 2048, 8)])
 def test_combine_backward(T, H, k, dt):
     B = _B()
     g = torch.Generator().manual_seed(T + H)
