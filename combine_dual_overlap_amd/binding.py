@@ -500,7 +500,7 @@ def moe_adamw_table(params, grads, m, v, m_scale=None, v_scale=None, master=None
     Made once (it copies the table to the device); the tensors must stay where they are."""
     n = len(params)
     _need(n > 0, "no tensors")
-    cols = [params, grads, m, v, m_scale, v_scale, master]
+    cols = [None if c is None else list(c) for c in (params, grads, m, v, m_scale, v_scale, master)]
     for c in cols:
         _need(c is None or len(c) == n, "lists of one length")
     none = [None] * n

@@ -21,6 +21,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
@@ -80,6 +81,13 @@ struct AdamArgs {
   const float* lr_scale;
   const float* grad_scale;
 };
+
+// One array of a tensor, in bytes.
+struct AdamRange {
+  uintptr_t begin, end;
+};
+static_assert(4 * sizeof(AdamRange) <= sizeof(AdamLaunch) + sizeof(int32_t) + sizeof(AdamTensor),
+              "the table's bytes hold four ranges of each tensor while they are compared");
 
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
   x ^= x >> 16;
@@ -384,6 +392,33 @@ extern "C" moe_status moe_adamw_table_build(const moe_adamw_tensor* tensors, int
     if (!aligned16(t.param) || !aligned16(t.grad) || !aligned16(t.m) || !aligned16(t.v) || !aligned16(t.master))
       return MOE_ERR_MISALIGNED;
     total += (t.n + kAdamGroup - 1) / kAdamGroup;
+  }
+  // Two workgroups must not update one element: the updated arrays are sorted,
+  // in the table's own bytes, and compared with their neighbours and the gradients.
+  auto* ranges = static_cast<AdamRange*>(table);
+  size_t nr = 0;
+  for (int i = 0; i < n_tensors; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    auto add = [&](const void* p, int64_t size) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+      if (p && t.n > 0) ranges[nr++] = AdamRange{a, a + static_cast<uintptr_t>(t.n * size)};
+    };
+    const int64_t state = t.state_dtype == MOE_F32 ? 4 : 1;
+    add(t.param, dtype_size(t.param_dtype));
+    add(t.m, state);
+    add(t.v, state);
+    add(t.master, 4);
+  }
+  std::sort(ranges, ranges + nr, [](const AdamRange& a, const AdamRange& b) { return a.begin < b.begin; });
+  for (size_t i = 1; i < nr; ++i)
+    if (ranges[i].begin < ranges[i - 1].end) return MOE_ERR_INVALID_ARG;
+  for (int i = 0; i < n_tensors; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(t.grad);
+    const uintptr_t z = a + static_cast<uintptr_t>(t.n * static_cast<int64_t>(dtype_size(t.grad_dtype)));
+    const AdamRange* r = std::upper_bound(ranges, ranges + nr, a, [](uintptr_t v, const AdamRange& x) { return v < x.end; });
+    if (r != ranges + nr && r->begin < z) return MOE_ERR_INVALID_ARG;
   }
   auto* out = static_cast<uint8_t*>(table);
   memset(out, 0, l.bytes);

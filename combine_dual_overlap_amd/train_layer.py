@@ -25,7 +25,8 @@ class TrainLayer:
 
     forward(x) -> out [T, H]; backward(dout) -> dx [T, H], adding to the
     gradients in `grads` (zero_grad() starts them anew); step() updates the
-    weights and zeroes the gradients.  Outputs live in the layer's buffers
+    weights and zeroes the gradients; the next backward() needs a new forward().
+    Outputs live in the layer's buffers
     until the next call; x must stay as it is until backward().  Calls run on the
     current stream of the layer's device; calls of one layer on several streams
     need the caller's ordering.
@@ -101,21 +102,26 @@ class TrainLayer:
         return [self.buf[s][:T if s in per_token else n] for s in names]
 
     def forward(self, x, forced_ids=None):
-        with torch.cuda.device(self.device):
-            return self._forward(x, forced_ids)
-
-    def _forward(self, x, forced_ids):
-        cfg, W = self.cfg, self.weights
+        cfg = self.cfg
+        self.T = 0                            # backward() refuses after a forward pass that failed
         if x.dtype != self.act or x.dim() != 2 or x.shape[1] != cfg.H or not 0 < x.shape[0] <= self.T_max:
             raise ValueError(f"x: [T, {cfg.H}] of {self.act}, 1 <= T <= {self.T_max}")
+        forced = self.forced_ids if forced_ids is None else forced_ids
+        if forced is not None and (forced.dtype != torch.int32 or forced.dim() != 2 or forced.shape[0] < x.shape[0] or
+                                   forced.shape[1] != cfg.k):
+            raise ValueError(f"forced_ids: int32 [{x.shape[0]}, {cfg.k}]")
         self.T, self.x = x.shape[0], x
+        try:
+            with torch.cuda.device(self.device):
+                return self._forward(x, forced)
+        except Exception:
+            self.T = 0
+            raise
+
+    def _forward(self, x, forced):
+        cfg, W = self.cfg, self.weights
         logits, ids, w, perm, inv, x_perm, gu, h, y_perm, out = self._rows(
             "logits", "ids", "w", "perm", "inv", "x_perm", "gu", "h", "y_perm", "out")
-        forced = self.forced_ids if forced_ids is None else forced_ids
-        if forced is not None and (forced.dtype != torch.int32 or forced.dim() != 2 or forced.shape[0] < self.T or
-                                   forced.shape[1] != cfg.k):
-            self.T = 0
-            raise ValueError(f"forced_ids: int32 [{x.shape[0]}, {cfg.k}]")
         B.moe_route_topk(x, W["w_router"], self.route, ids, w, self.ws_route, logits_out=logits,
                          logit_bias=self.logit_bias, forced_ids=forced)
         B.moe_dispatch(x, ids, cfg.E, cfg.expert_begin, cfg.expert_end, self.buf["counts"], self.offsets, perm, inv,
@@ -132,7 +138,7 @@ class TrainLayer:
 
     def backward(self, dout):
         if self.T == 0:
-            raise RuntimeError("backward() follows forward()")
+            raise RuntimeError("backward() follows forward(), with the weights it used")
         if dout.shape != (self.T, self.cfg.H) or dout.dtype != self.act:
             raise ValueError(f"dout: [{self.T}, {self.cfg.H}] of {self.act}")
         with torch.cuda.device(self.device):
@@ -172,3 +178,4 @@ class TrainLayer:
         self.steps.add_(1)
         B.moe_adamw_step(self.table, self.hyper, self.steps, lr_scale=lr_scale, grad_scale=grad_scale)
         self.zero_grad()
+        self.T = 0                            # the weights are no longer those of the last forward pass

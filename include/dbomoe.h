@@ -337,7 +337,8 @@ moe_status moe_grouped_swiglu_backward(const void* dy_perm, const void* w2, cons
  * moe_combine_backward - gradients of moe_combine.
  *   dout [T, H] act; y_perm [cap_rows, H] act and inv, topk_w as moe_combine took them
  *   dy_perm  [cap_rows, H] act out: dy_perm[inv[t*k+j]] = topk_w[t, j] * dout[t]
- *            (rows no pair points at are untouched)
+ *            (rows no pair points at are untouched; no two pairs may name one
+ *            row, as none do in moe_dispatch's inv)
  *   dtopk_w  [T, k] fp32 out: <dout[t], y_perm[inv[t*k+j]]>, 0 where inv is
  *            outside [0, cap_rows)
  * The gradient of shared_out is dout itself; the gradient of moe_dispatch's x
@@ -393,7 +394,8 @@ moe_status moe_route_backward(const float* logits, int64_t T, const int32_t* top
  *     m's code takes a >> 12, sqrt(v)'s b >> 12 (20 bits each), a bf16 param
  *     (a & 0xfff) << 4 | (b & 0xf) (16 bits).
  * Gradients must be finite: the states keep what is not.  Tensors of n == 0
- * are skipped; tensors must not overlap.
+ * are skipped.  Arrays must not overlap: moe_adamw_table_build refuses
+ * params, masters and states that do, among themselves or with a gradient.
  * ------------------------------------------------------------------------- */
 typedef struct {
   void* param;

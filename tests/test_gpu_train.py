@@ -897,3 +897,35 @@ def test_train_layer_fewer_tokens_and_another_stream():
         for n in a.grads:
             assert torch.equal(a.grads[n], b.grads[n]), n
         a.zero_grad()
+
+
+def test_train_layer_refuses_a_backward_without_its_forward():
+    """After a step (the weights have moved) and after a forward pass that failed."""
+    from combine_dual_overlap_amd import TrainLayer
+    _B()
+    cfg, inp = _layer_inputs(2, "bf16", forced=False)
+    layer = TrainLayer(inp)
+    x = inp["x"].cuda()
+    layer.forward(x)
+    layer.backward(x)
+    layer.step()
+    with pytest.raises(RuntimeError):
+        layer.backward(x)
+    layer.forward(x)
+    with pytest.raises(ValueError):
+        layer.forward(x.t().contiguous().t())                 # rows are not contiguous
+    with pytest.raises(RuntimeError):
+        layer.backward(x)
+
+
+def test_adamw_table_holds_its_tensors():
+    """The caller may drop its lists."""
+    B = _B()
+    p, g, m, v = ([torch.ones(256, device="cuda")] for _ in range(4))
+    table = B.moe_adamw_table(p, g, m, v)
+    kept = p[0]
+    for t in (p, g, m, v):
+        t.clear()
+    assert [c[0].numel() for c in table.keep[:4]] == [256] * 4 and table.keep[0][0] is kept
+    with pytest.raises(RuntimeError):
+        B.moe_adamw_table([kept], [kept], [torch.zeros(256, device="cuda")], [torch.zeros(256, device="cuda")])

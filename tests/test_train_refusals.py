@@ -127,6 +127,32 @@ def test_adamw_table_refusals():
     assert build(t, 1, host.data_ptr(), B.lib().moe_adamw_table_size(1) - 1) == B.MOE_ERR_WORKSPACE
 
 
+def test_adamw_table_refuses_overlapping_arrays():
+    """An array that is updated twice, or read as a gradient while it is updated, in any order of the tensors."""
+    B = _B()
+
+    def tensor(i, **kw):
+        base = dict(param=(8 * i + 1) * A, grad=(8 * i + 2) * A, m=(8 * i + 3) * A, v=(8 * i + 4) * A, m_scale=None,
+                    v_scale=None, master=(8 * i + 5) * A, n=A // 4, param_dtype=1, grad_dtype=0, state_dtype=0)
+        base.update(kw)
+        return B.moe_adamw_tensor(*base.values())
+
+    def build(*tensors):
+        t = (B.moe_adamw_tensor * len(tensors))(*tensors)
+        host = torch.zeros(B.lib().moe_adamw_table_size(len(tensors)), dtype=torch.uint8)
+        return B.lib().moe_adamw_table_build(t, len(tensors), host.data_ptr(), host.numel())
+
+    # A bytes hold n fp32 elements: m, v, grad and master touch, which is fine
+    assert build(*[tensor(i) for i in range(60)]) == B.MOE_OK
+    assert build(tensor(0), tensor(1, grad=2 * A)) == B.MOE_OK             # two tensors may read one gradient
+    assert build(tensor(0), tensor(1, grad=6 * A)) == B.MOE_OK             # right behind the first one's master
+    for kw in (dict(param=A), dict(param=A + 1024), dict(m=3 * A), dict(v=4 * A - 64), dict(master=5 * A), dict(m=A),
+               dict(m=2 * A), dict(grad=3 * A), dict(grad=3 * A - 64), dict(grad=6 * A - 64), dict(grad=A + A // 2 - 64)):
+        assert build(tensor(0), tensor(1, **kw)) == B.MOE_ERR_INVALID_ARG, kw
+        assert build(tensor(1, **kw), tensor(2), tensor(0)) == B.MOE_ERR_INVALID_ARG, kw
+        assert build(tensor(0), tensor(1, n=0, **kw)) == B.MOE_OK, kw      # nothing overlaps with nothing
+
+
 def test_adamw_step_refusals():
     B = _B()
     status, host = _table(B)
