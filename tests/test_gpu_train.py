@@ -929,3 +929,55 @@ def test_adamw_table_holds_its_tensors():
     assert [c[0].numel() for c in table.keep[:4]] == [256] * 4 and table.keep[0][0] is kept
     with pytest.raises(RuntimeError):
         B.moe_adamw_table([kept], [kept], [torch.zeros(256, device="cuda")], [torch.zeros(256, device="cuda")])
+
+
+def test_adamw_large_tensor_equals_its_prefix():
+    """Where a workgroup takes four groups of elements instead of one the results are the same, bit for bit: an
+    element's random numbers depend on its place in the tensor only."""
+    B = _B()
+    n, cut = 17 * 1000 * 1000 + 5, 128 * 330
+    g = torch.Generator(device="cuda").manual_seed(3)
+    p = torch.randn(n, generator=g, device="cuda").to(BF)
+    gr = torch.randn(n, generator=g, device="cuda").to(BF)
+    codes = lambda k: torch.zeros(k, dtype=torch.uint8, device="cuda")
+
+    def steps(p, gr):
+        k = p.numel()
+        st = [codes(k), codes(k), codes((k + 127) // 128), codes((k + 127) // 128)]
+        table = B.moe_adamw_table([p], [gr], [st[0]], [st[1]], [st[2]], [st[3]])
+        step = torch.zeros(1, dtype=torch.int32, device="cuda")
+        for _ in range(2):
+            step.add_(1)
+            B.moe_adamw_step(table, B.adamw_params(lr=0.01, weight_decay=0.0), step)
+        return st
+
+    small = p[:cut].clone()
+    old_tail = p[-1000:].clone()
+    a, b = steps(p, gr), steps(small, gr[:cut].clone())
+    assert torch.equal(p[:cut], small) and all(torch.equal(x[:y.numel()], y) for x, y in zip(a, b))
+    # The last elements have moved against their gradients by 2 lr, but for: bf16's stochastic rounding, less than
+    # 2^-10 twice for weights below 1/4; the second step's m and sqrt(v) from codes off by an eighth at most (where
+    # |g| > 0.1 no code is denormal): m by 0.09 / 0.19 / 8 = 6 %, sqrt(v) by sqrt(1 + (1.125^2 - 1) / 2) - 1 = 6.5 %.
+    d = (p[-1000:].float() - old_tail.float()) * torch.sign(gr[-1000:].float())
+    near = (old_tail.abs().float() < 0.22) & (gr[-1000:].abs().float() > 0.1)
+    assert (d[near] < -0.02 + 0.01 * 0.13 + 2.0 ** -9).all() and int(near.sum()) > 100
+    big = gr[-1000:].abs().float() > 0.1
+    assert (a[0][-1000:] != 0)[big].all() and (a[1][-1000:] != 0).all()
+
+
+def test_adamw_more_tensors_than_a_launch_holds():
+    """4100 tensors of three elements equal the same elements in one tensor (fp32 throughout: nothing is random)."""
+    B = _B()
+    n = 4100
+    g = torch.Generator().manual_seed(5)
+    flat = [rnd(g, n, 4).cuda() for _ in range(2)] + [torch.zeros(n, 4, device="cuda") for _ in range(2)]
+    one = [t.clone().reshape(-1) for t in flat]
+    rows = [[r[:3] for r in t] for t in flat]
+    hp = B.adamw_params(lr=0.01)
+    step = torch.ones(1, dtype=torch.int32, device="cuda")
+    B.moe_adamw_step(B.moe_adamw_table(*rows), hp, step)
+    before = flat[0][:, 3].clone()
+    B.moe_adamw_step(B.moe_adamw_table(*([t] for t in one)), hp, step)
+    for t, u in zip(flat, one):
+        assert torch.equal(t[:, :3], u.view(n, 4)[:, :3])
+    assert torch.equal(flat[0][:, 3], before) and (flat[2][:, 3] == 0).all()
