@@ -259,14 +259,23 @@ __device__ __forceinline__ void store_swiglu_bwd(const GgParams& p, int64_t row,
 }
 
 // Eight columns of a row.  STREAM (weight gradients, which the optimizer reads
-// much later): a store that the caches need not keep; the skewed layer's gate/up
-// gradient 557 -> 528 us.  (The same for gate/up outputs cost 2 %.)
+// much later, and the SwiGLU backward's dgu): a store that the caches need not
+// keep; the skewed layer's gate/up gradient 557 -> 528 us, dgu of 32768 rows 2 to
+// 4 %.  (The same for gate/up outputs cost 2 %.)
 template <bool STREAM, typename T>
 __device__ __forceinline__ void write_as(void* p, const T& v) {
   if constexpr (STREAM)
     __builtin_nontemporal_store(v, static_cast<T*>(p));
   else
     *static_cast<T*>(p) = v;
+}
+
+// Likewise for what an epilogue reads once: gu, and the bf16 C that TN adds to
+// (64 rows an expert 475 -> 443 us; fp32 C gained nothing).
+template <bool STREAM>
+__device__ __forceinline__ u32x4_t read_as(const u32x4_t* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(p);
+  return *p;
 }
 
 template <bool STREAM = false>
@@ -308,8 +317,8 @@ __device__ __forceinline__ void store_swiglu_bwd8(const GgParams& p, int64_t row
   unpack8(up, u[0], u[1]);
 #pragma unroll
   for (int k = 0; k < 2; ++k) swiglu_bwd(k ? d1 : d0, g[k], u[k], dg[k], du[k]);
-  store8(p.C, gi, dg[0], dg[1]);
-  store8(p.C, gi + p.N, du[0], du[1]);
+  store8<true>(p.C, gi, dg[0], dg[1]);
+  store8<true>(p.C, gi + p.N, du[0], du[1]);
 }
 
 // ---- bf16 -------------------------------------------------------------------
@@ -595,14 +604,15 @@ __device__ __forceinline__ void gg_tile(const GgParams& p, const GgTile& t, uint
       if (!x.ok) continue;
       if constexpr (EPI == EPI_SWIGLU_BWD) {
         const bf16_t* g = static_cast<const bf16_t*>(p.gu) + x.row * 2 * p.N + x.col;
-        old[i % AHEAD][h][0] = *reinterpret_cast<const u32x4_t*>(g);
-        old[i % AHEAD][h][1] = *reinterpret_cast<const u32x4_t*>(g + p.N);
+        old[i % AHEAD][h][0] = read_as<true>(reinterpret_cast<const u32x4_t*>(g));
+        old[i % AHEAD][h][1] = read_as<true>(reinterpret_cast<const u32x4_t*>(g + p.N));
       } else if (p.c_f32) {
         const u32x4_t* c = reinterpret_cast<const u32x4_t*>(static_cast<const float*>(p.C) + x.row * nout + x.col);
         old[i % AHEAD][h][0] = c[0];
         old[i % AHEAD][h][1] = c[1];
       } else {
-        old[i % AHEAD][h][0] = *reinterpret_cast<const u32x4_t*>(static_cast<const bf16_t*>(p.C) + x.row * nout + x.col);
+        old[i % AHEAD][h][0] = read_as<KIND == MOE_GEMM_TN>(
+            reinterpret_cast<const u32x4_t*>(static_cast<const bf16_t*>(p.C) + x.row * nout + x.col));
       }
     }
   };
@@ -924,8 +934,9 @@ __global__ __launch_bounds__(256) void k_join_splits(GgParams p, int64_t quads, 
 
 // ---- host -------------------------------------------------------------------
 
-// Tile and reduction parts of a call, from its sizes alone (the workspace
-// query makes the same choice).  Measured on both sides of each border, 64
+// Tile and reduction parts of a call, from its sizes alone.  (The workspace
+// query makes the same choice; adds, the one argument it does not have, decides
+// between two shapes that are never split.)  Measured on both sides of each border, 64
 // experts, us with uniform / Zipf-distributed (1.2) rows:
 //   32 x 128 against 128 x 128, by rows of an average expert (2048 x 1408): the
 //   SwiGLU backward with 24 rows 76 / 77 against 82 / 87, with 32 rows 83 / 87
@@ -934,6 +945,14 @@ __global__ __launch_bounds__(256) void k_join_splits(GgParams p, int64_t quads, 
 //   256 x 256 against 128 x 128: NT with 96 rows 93 against 90 (uniform), with 128
 //   rows 98 / 121 against 108 / 109, with 192 rows 108 / 124 against 129 / 132; TN
 //   with 32 to 256 rows 107 to 174 against 124 to 187 (uniform).
+//   Where the epilogue reads as much as it writes and the reduction is short, two
+//   workgroups of 128 x 128 on a compute unit overlap one's epilogue with the
+//   other's MFMAs.  SwiGLU backward, 512 rows an expert x 1408, against 256 x 256:
+//   H = 512 153 / 135 against 172 / 157, 1024 197 / 188 against 209 / 204, 2048
+//   302 / 303 against 307 / 305, 4096 520 / 528 against 501 / 521; 768 wide (128
+//   experts), H = 2048 334 / 332 against 326 / 325.  TN that adds to C, 2816 x
+//   2048 fp32 (uniform): 64 rows 541 against 614, 256 rows 662 against 720, 512
+//   rows 841 against 864, 1024 rows 1183 against 1136.
 //   64 x 128 (the reduction split inside the workgroup) up to 128 tiles, against
 //   128 x 128: TN 8192 rows 128 x 2048 19 against 23, NN 661 rows of 8 experts
 //   760 x 104 7.0 against 10.0; with more tiles its traffic from L2 (12 TB/s)
@@ -950,7 +969,7 @@ static int64_t gg_tiles(int kind, int epi, int E, int64_t cap, bool dense, int N
   return max_row_tiles(cap, E, BM, dense) * nt;
 }
 
-static GgPlan gg_plan(int kind, int epi, bool f32, int E, int64_t cap, bool dense, int N, int K) {
+static GgPlan gg_plan(int kind, int epi, bool f32, int E, int64_t cap, bool dense, int N, int K, bool adds = false) {
   const int64_t rows = cap / E;                     // of an average expert
   const int cols = kind == MOE_GEMM_TN ? K : epi == EPI_SWIGLU ? 2 * N : N;
   GgPlan q{128, 128, 1, 0};
@@ -959,6 +978,7 @@ static GgPlan gg_plan(int kind, int epi, bool f32, int E, int64_t cap, bool dens
   else if (kind != MOE_GEMM_TN && rows <= 32)
     q.BM = 32;
   else if (cols > 128 && (kind == MOE_GEMM_TN ? N > 128 : rows > 128) &&
+           !(epi == EPI_SWIGLU_BWD && K < 2048) && !(kind == MOE_GEMM_TN && adds && rows <= 512) &&
            gg_tiles(kind, epi, E, cap, dense, N, K, 256, 256) >= 256)
     q.BM = q.BN = 256;
   else if (gg_tiles(kind, epi, E, cap, dense, N, K, 64, 128) <= 128)
@@ -1058,7 +1078,7 @@ extern "C" moe_status moe_grouped_gemm(moe_gemm_kind kind, const void* a, const 
   p.c_f32 = ct == MOE_F32;
   p.accumulate = accumulate;
   const bool f32 = ab == MOE_F32;
-  const GgPlan q = gg_plan(kind, EPI_STORE, f32, E_loc, cap_rows, !offsets, N, K);
+  const GgPlan q = gg_plan(kind, EPI_STORE, f32, E_loc, cap_rows, !offsets, N, K, accumulate != 0);
   if (q.splits > 1) {
     if (!ws) return MOE_ERR_INVALID_ARG;
     if (!aligned256(ws)) return MOE_ERR_MISALIGNED;

@@ -131,6 +131,7 @@ def test_grouped_gemm_weights(name, dt):
 # one, two and several tiles, odd widths, reductions that end inside a stage.
 MID = [(i * 29) % 131 for i in range(60)]                  # 128 x 128 tiles
 BIG = [0, 1, 15, 16, 17, 31, 33, 255, 256, 257, 511, 513, 700, 1030, 2049] + [(i * 97) % 331 for i in range(45)]
+TALL = [0, 1, 1999, 640, 513] + [450 + (i * 97) % 331 for i in range(17)]     # 256 x 256 also where TN adds to C
 
 
 def _ref_rows(kind, a, b, counts):
@@ -142,7 +143,7 @@ def _ref_rows(kind, a, b, counts):
     return ref, mag
 
 
-@pytest.mark.parametrize("N,K,counts", [(520, 72, BIG), (1032, 200, BIG), (264, 328, BIG), (648, 200, MID), (88, 136, MID)],
+@pytest.mark.parametrize("N,K,counts", [(520, 72, BIG), (1032, 200, BIG), (264, 328, BIG), (648, 200, MID), (88, 136, MID), (520, 1032, TALL)],
                          ids=lambda v: "x" if isinstance(v, list) else str(v))
 @pytest.mark.parametrize("kind", ["nt", "nn", "tn"])
 def test_grouped_gemm_large_tiles(kind, N, K, counts):
@@ -176,7 +177,7 @@ def test_grouped_gemm_large_tiles(kind, N, K, counts):
             assert torch.equal(c[M:].cpu(), c0[M:])
 
 
-@pytest.mark.parametrize("I,H,counts", [(520, 72, BIG), (264, 328, BIG), (648, 200, MID)],
+@pytest.mark.parametrize("I,H,counts", [(520, 72, BIG), (264, 328, BIG), (648, 200, MID), (520, 2056, BIG)],
                          ids=lambda v: "x" if isinstance(v, list) else str(v))
 def test_grouped_swiglu_large_tiles(I, H, counts):
     B = _B()
