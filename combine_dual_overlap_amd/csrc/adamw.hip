@@ -76,6 +76,7 @@ struct AdamArgs {
   int32_t count, groups;
   uint32_t seed;
   float b1, omb1, b2, omb2, eps, lr, lr_wd;
+  float root_b2, root_omb2;           // sqrt(b2), sqrt(1 - b2), both times 2^120
   double log_b1, log_b2;
   const int32_t* step;
   const float* lr_scale;
@@ -100,6 +101,21 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 // E8M0 byte -> scale; byte 0 is 2^-127, a denormal.
 __device__ __forceinline__ float e8m0(uint8_t b) { return __uint_as_float(b ? static_cast<uint32_t>(b) << 23 : 0x400000u); }
+
+// The square root instruction: off by at most one unit, and it takes a denormal
+// for zero, so that a small argument is scaled out of that range (exactly).
+__device__ __forceinline__ float root_f32(float v) {
+  const bool small = v < 0x1p-100f;
+  return __builtin_amdgcn_sqrtf(small ? v * 0x1p64f : v) * (small ? 0x1p-32f : 1.f);
+}
+
+// sqrt(b2 r^2 + (1 - b2) g^2) where that is below 2^-60: its square leaves
+// fp32's normal range, or fp32.  A nonzero one does not become 0.
+__device__ __forceinline__ float small_root(float r, float g, float root_b2, float root_omb2) {
+  const float x = r * root_b2, y = g * root_omb2;           // times 2^120: below 2^60
+  const float w = x * x + y * y;
+  return w > 0.f ? fmaxf(__builtin_amdgcn_sqrtf(w) * 0x1p-120f, 0x1p-149f) : 0.f;
+}
 
 template <int N>
 __device__ __forceinline__ float row_rotated(float v) {
@@ -272,9 +288,9 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
       const uint64_t qm = load8_codes<FULL>(static_cast<const uint8_t*>(t.m), i, n);
       const uint64_t qv = load8_codes<FULL>(static_cast<const uint8_t*>(t.v), i, n);
       decode8(qm, e8m0(t.ms[i >> 7]), m);
-      decode8(qv, e8m0(t.vs[i >> 7]), v);
+      decode8(qv, e8m0(t.vs[i >> 7]), root);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = v[j] * v[j];
+      for (int j = 0; j < 8; ++j) v[j] = root[j] * root[j];
     } else {
       load8<false, FULL, EIGHT>(t.m, i, n, m);
       load8<false, FULL, EIGHT>(t.v, i, n, v);
@@ -285,12 +301,32 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
       load8<PARAM == PARAM_BF16, FULL, EIGHT>(t.p, i, n, p);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float gj = g[j] * gs;
-      m[j] = m[j] * a.b1 + gj * a.omb1;
-      v[j] = v[j] * a.b2 + (gj * a.omb2) * gj;
-      root[j] = __builtin_amdgcn_sqrtf(v[j]);               // off by at most one unit, as the reciprocal
-      p[j] = p[j] * decay - step_size * (m[j] * __builtin_amdgcn_rcpf(root[j] * rbc2 + a.eps));
+      g[j] = g[j] * gs;
+      m[j] = m[j] * a.b1 + g[j] * a.omb1;
+      v[j] = v[j] * a.b2 + (g[j] * a.omb2) * g[j];
     }
+    if constexpr (EIGHT) {
+      float low = v[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) low = fminf(low, v[j]);
+      float r[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        r[j] = root[j];
+        root[j] = __builtin_amdgcn_sqrtf(v[j]);
+      }
+      if (low < 0x1p-120f) {                                // seldom: a branch costs less than the work
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (v[j] < 0x1p-120f) root[j] = small_root(r[j], g[j], a.root_b2, a.root_omb2);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) root[j] = root_f32(v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)                             // (the reciprocal's argument is at least eps, a normal number)
+      p[j] = p[j] * decay - step_size * (m[j] * __builtin_amdgcn_rcpf(root[j] * rbc2 + a.eps));
     uint32_t one[8], two[8];
     if constexpr (EIGHT || PARAM == PARAM_BF16) {
       const uint32_t key = key0 ^ (static_cast<uint32_t>(i >> 32) * 0x9e3779b9u);
@@ -479,6 +515,8 @@ extern "C" moe_status moe_adamw_step(const void* table_host, const void* table_d
   a.b2 = static_cast<float>(hp->beta2);
   a.omb2 = static_cast<float>(1.0 - hp->beta2);
   a.eps = static_cast<float>(hp->eps);
+  a.root_b2 = static_cast<float>(ldexp(sqrt(hp->beta2), 120));
+  a.root_omb2 = static_cast<float>(ldexp(sqrt(1.0 - hp->beta2), 120));
   a.lr = static_cast<float>(hp->lr);
   a.lr_wd = static_cast<float>(hp->lr * hp->weight_decay);
   a.log_b1 = log(hp->beta1);

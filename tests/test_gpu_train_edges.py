@@ -1,0 +1,112 @@
+"""Corners of the training operators on the GPU: second moments below fp32's normal range, gradients that are not
+finite, experts without rows, refused and captured training steps, fp32 tiles and split reductions.
+
+Tolerances count roundings as the other tests of these operators do: `check` is theirs.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_train import (BF, E4M3, F32, TALL, _B, _decode, _layer_inputs, _ref_rows, _sigmoid, _swiglu_bwd, check,
+                            offsets_of, rnd, spans)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ AdamW far from 1
+
+def _update(p0, m1, v1, t, b1, b2, eps):
+    """The parameter after a step of lr 1 without decay, from the new moments, in 64 bits."""
+    return p0 - m1 / (1 - b1 ** t) / (np.sqrt(v1 / (1 - b2 ** t)) + eps)
+
+
+@pytest.mark.parametrize("beta2", [0.95, 0.999])
+@pytest.mark.parametrize("master", [False, True], ids=["f32", "master"])
+def test_adamw_second_moment_below_the_normal_range(master, beta2):
+    """fp32 states whose v is denormal: the update still divides by its root, not by eps alone."""
+    B = _B()
+    n, eps = 4099, 1e-30
+    g = torch.Generator().manual_seed(21)
+    gr = (10.0 ** (torch.rand(n, generator=g, dtype=torch.float64) * 8 - 22) * torch.sign(rnd(g, n))).float().cuda()
+    gr[5] = 0.0
+    ma = torch.zeros(n, device="cuda")
+    p = torch.zeros(n, dtype=BF, device="cuda") if master else ma
+    m, v = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    table = B.moe_adamw_table([p], [gr], [m], [v], master=[ma] if master else None)
+    hp = B.adamw_params(lr=1.0, beta2=beta2, eps=eps, weight_decay=0.0)
+    step = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gd = gr.double().cpu().numpy()
+    u = 2.0 ** -24
+    for t in (1, 2, 3):
+        p0, m0, v0 = (x.double().cpu().numpy() for x in (ma, m, v))
+        step.add_(1)
+        B.moe_adamw_step(table, hp, step)
+        m1, v1 = 0.9 * m0 + 0.1 * gd, beta2 * v0 + (1 - beta2) * gd * gd
+        # m: 4 roundings; v: 4 roundings, and three of them may be of denormals, half of 2^-149 each.  The update lies
+        # between those of the smallest and the largest root, with 12 roundings of its own.
+        em, ev = 4 * u * (0.9 * np.abs(m0) + 0.1 * np.abs(gd)) + 1e-44, 4 * u * v1 + 1.5 * 2.0 ** -149
+        ends = [_update(0, m1 + i * em, np.maximum(v1 + j * ev, 0), t, 0.9, beta2, eps) for i in (-1, 1) for j in (-1, 1)]
+        lo, hi = p0 + np.minimum.reduce(ends), p0 + np.maximum.reduce(ends)
+        slack = 3 * u * np.abs(p0) + 12 * u * np.maximum.reduce(np.abs(ends))
+        got = ma.double().cpu().numpy()
+        bad = (got < lo - slack) | (got > hi + slack)
+        assert not bad.any(), (t, int(bad.sum()), gd[bad][:3], got[bad][:3], lo[bad][:3], hi[bad][:3])
+        assert (np.abs(v.double().cpu().numpy() - v1) <= ev).all()
+        assert got[5] == 0.0
+
+
+@pytest.mark.parametrize("param", [F32, BF], ids=["f32", "bf16"])
+def test_adamw_8bit_states_at_every_magnitude(param):
+    """Blocks from 1 down to denormal gradients, and blocks that span the whole range: a nonzero second moment keeps a
+    nonzero code, codes bracket the formula's values and the update divides by the root."""
+    B = _B()
+    blocks, eps, b2 = 46, 1.2e-38, 0.95
+    n = 128 * blocks + 37
+    g = torch.Generator().manual_seed(22)
+    mag = 10.0 ** -(torch.arange(n) // 128).double().clamp(max=40)
+    wide = 10.0 ** -(torch.rand(n, generator=g, dtype=torch.float64) * 41)
+    mag = torch.where((torch.arange(n) // 128) % 4 == 3, wide, mag)
+    gr = torch.zeros(n, device="cuda")
+    p = torch.zeros(n, dtype=param, device="cuda")
+    m, v = (torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ms, vs = (torch.zeros((n + 127) // 128, dtype=torch.uint8, device="cuda") for _ in range(2))
+    table = B.moe_adamw_table([p], [gr], [m], [v], [ms], [vs])
+    hp = B.adamw_params(lr=1.0, beta2=b2, eps=eps, weight_decay=0.0)
+    step = torch.zeros(1, dtype=torch.int32, device="cuda")
+    u = 2.0 ** -24
+    for t in (1, 2, 3):
+        if t < 3:
+            gr.copy_(((0.5 + torch.rand(n, generator=g)) * torch.sign(rnd(g, n)) * mag).float())
+        else:
+            gr.zero_()                                        # the states only decay
+        gd, p0 = gr.double().cpu().numpy(), p.double().cpu().numpy()
+        m0, v0 = (_decode(c.cpu().numpy(), s.cpu().numpy()) for c, s in ((m, ms), (v, vs)))
+        step.add_(1)
+        B.moe_adamw_step(table, hp, step)
+        m1, r1 = 0.9 * m0 + 0.1 * gd, np.sqrt(b2 * v0 ** 2 + (1 - b2) * gd ** 2)
+        for x, codes, scale, root in ((m1, m, ms, False), (r1, v, vs, True)):
+            c, s = codes.cpu().numpy(), scale.cpu().numpy()
+            top = np.array([np.abs(x[j:j + 128]).max() for j in range(0, n, 128)])
+            want = np.maximum(np.ceil(np.log2(np.maximum(top, 1e-300) / 448)), -127)
+            near = (np.abs(top / (448 * 2.0 ** want) - 1) < 1e-5) | (np.abs(top / (224 * 2.0 ** want) - 1) < 1e-5)
+            assert ((s.astype(int) - 127 == want) | near).all(), (t, root)
+            sc = np.repeat(2.0 ** (s.astype(np.float64) - 127), 128)[:n]
+            # m: 4 roundings of its terms, fp32's lowest step; the root: 8 roundings, and that step (of 2^-149)
+            err = 8 * u * (0.9 * np.abs(m0) + 0.1 * np.abs(gd) if not root else r1) + 2.0 ** -148
+            val = np.abs(_decode(c, s))
+            lo = E4M3[np.searchsorted(E4M3, np.maximum(np.abs(x) - err, 0) / sc, side="right") - 1] * sc
+            hi = E4M3[np.minimum(np.searchsorted(E4M3, (np.abs(x) + err) / sc, side="left"), 126)] * sc
+            if root:
+                hi = np.where(x > 0, np.maximum(hi, 2.0 ** -9 * sc), hi)
+                assert ((c != 0) == (x > 0)).all(), (t, int(((c != 0) != (x > 0)).sum()), x[(c != 0) != (x > 0)][:4])
+            assert ((val >= lo) & (val <= hi)).all(), (t, root)
+        den = r1 / np.sqrt(1 - b2 ** t) + eps
+        up = m1 / (1 - 0.9 ** t) / den
+        err = (4 * u * (0.9 * np.abs(m0) + 0.1 * np.abs(gd)) + 2.0 ** -148) / (1 - 0.9 ** t) / den
+        err += np.abs(up) * (16 * u + 2.0 ** -148 / den) + 3 * u * np.abs(p0)
+        if param == BF:                                       # a stochastic rounding: less than one bf16 step
+            err += 2.0 ** -7 * (np.abs(p0 - up) + err) + 2.0 ** -133
+        bad = np.abs(p.double().cpu().numpy() - (p0 - up)) > err
+        assert not bad.any(), (t, int(bad.sum()), gd[bad][:3])
