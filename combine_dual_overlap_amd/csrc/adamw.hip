@@ -13,7 +13,8 @@
 // up to 12 % away), so rounding to nearest would hold it where it is.  A
 // nonzero sqrt(v) never becomes code 0, or the next step would divide by eps
 // alone.  bf16 parameters without an fp32 master are rounded stochastically
-// for the same reason.
+// for the same reason.  What is not finite becomes a NaN code and has no part in
+// its block's scale.
 //
 // Random numbers: two 32-bit hashes of (seed, step, tensor, element), so the
 // result depends on nothing else.  mix() is two rounds of xor-shift and
@@ -337,11 +338,27 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
       }
     }
     if constexpr (EIGHT) {
-      float tm = 0.f, tv = 0.f;
+      // maxima of bit patterns: infinities and NaN are above every number
+      uint32_t bm = 0, bv = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        tm = fmaxf(tm, fabsf(m[j]));
-        tv = fmaxf(tv, root[j]);
+        bm = max(bm, __float_as_uint(m[j]) & 0x7fffffffu);
+        bv = max(bv, __float_as_uint(root[j]) & 0x7fffffffu);
+      }
+      float tm = __uint_as_float(bm), tv = __uint_as_float(bv);
+      if (max(bm, bv) >= 0x7f800000u) {
+        tm = tv = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (fabsf(m[j]) < INFINITY)
+            tm = fmaxf(tm, fabsf(m[j]));
+          else
+            m[j] = NAN;
+          if (root[j] < INFINITY)
+            tv = fmaxf(tv, root[j]);
+          else
+            root[j] = NAN;
+        }
       }
       const int em = block_exponent(block_max(tm)), ev = block_exponent(block_max(tv));
       const float im = pow2f(-em), iv = pow2f(-ev);
@@ -349,8 +366,9 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         ym[j] = m[j] * im;
-        // a nonzero value below the smallest code (2^-9) becomes that code
-        yv[j] = root[j] > 0.f ? fmaxf(root[j] * iv, 0.001953125f) : 0.f;
+        // a nonzero value below the smallest code (2^-9) becomes that code; NaN stays
+        yv[j] = root[j] * iv;
+        if (root[j] > 0.f && yv[j] < 0.001953125f) yv[j] = 0.001953125f;
       }
       store8_codes<FULL>(static_cast<uint8_t*>(t.m), i, n, encode8(ym, one));
       store8_codes<FULL>(static_cast<uint8_t*>(t.v), i, n, encode8(yv, two));

@@ -393,7 +393,9 @@ moe_status moe_route_backward(const float* logits, int64_t T, const int32_t* top
  *       a = mix((uint32)i ^ key ^ 0x9e3779b9 * (i >> 32)),  b = mix(a + 0x9e3779b9);
  *     m's code takes a >> 12, sqrt(v)'s b >> 12 (20 bits each), a bf16 param
  *     (a & 0xfff) << 4 | (b & 0xf) (16 bits).
- * Gradients must be finite: the states keep what is not.  Tensors of n == 0
+ * Gradients must be finite and g^2 within fp32's range (|g| < 1.8e19): the
+ * states keep what is not, an infinity or NaN in fp32, a NaN code in 8 bits
+ * (the other elements of its block are not touched by it).  Tensors of n == 0
  * are skipped.  Arrays must not overlap: moe_adamw_table_build refuses
  * params, masters and states that do, among themselves or with a gradient.
  * ------------------------------------------------------------------------- */

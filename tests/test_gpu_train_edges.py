@@ -110,3 +110,45 @@ def test_adamw_8bit_states_at_every_magnitude(param):
             err += 2.0 ** -7 * (np.abs(p0 - up) + err) + 2.0 ** -133
         bad = np.abs(p.double().cpu().numpy() - (p0 - up)) > err
         assert not bad.any(), (t, int(bad.sum()), gd[bad][:3])
+
+
+@pytest.mark.parametrize("param", [F32, BF], ids=["f32", "bf16"])
+def test_adamw_8bit_states_keep_what_is_not_finite(param):
+    """An infinity or NaN stays in its own element, as NaN codes; the block's other elements are what they are beside
+    a gradient of zero."""
+    B = _B()
+    n = 128 * 40 + 50
+    bad = {3: math.inf, 130: math.nan, 131: -math.inf, 300: math.inf, 2047: math.nan, n - 1: -math.inf}
+    bad.update({i: math.nan for i in range(512, 640)})        # a block with nothing else
+    at = torch.tensor(sorted(bad))
+    keep = torch.ones(n, dtype=torch.bool)
+    keep[at] = False
+    g = torch.Generator().manual_seed(23)
+    p0 = rnd(g, n, dt=param)
+
+    def make():
+        codes = lambda k: torch.zeros(k, dtype=torch.uint8, device="cuda")
+        s = dict(p=p0.cuda(), g=torch.zeros(n, device="cuda"), m=codes(n), v=codes(n), ms=codes((n + 127) // 128),
+                 vs=codes((n + 127) // 128))
+        s["table"] = B.moe_adamw_table([s["p"]], [s["g"]], [s["m"]], [s["v"]], [s["ms"]], [s["vs"]])
+        return s
+
+    a, b = make(), make()
+    hp, step = B.adamw_params(lr=0.01), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for t in (1, 2, 3):
+        grad = rnd(g, n)
+        clean = grad * keep                                   # zeros in b, so that its states there stay zero
+        if t == 1:
+            for i, x in bad.items():
+                grad[i] = x
+        a["g"].copy_(grad)
+        b["g"].copy_(clean)
+        step.add_(1)
+        for s in (a, b):
+            B.moe_adamw_step(s["table"], hp, step)
+        for name in ("p", "m", "v"):
+            assert torch.equal(a[name].cpu()[keep], b[name].cpu()[keep]), (t, name)
+        assert torch.equal(a["ms"], b["ms"]) and torch.equal(a["vs"], b["vs"]), t
+        assert torch.isnan(a["p"].cpu()[at]).all(), t
+        for name in ("m", "v"):
+            assert torch.isnan(a[name].view(torch.float8_e4m3fn).float().cpu()[at]).all(), (t, name)
