@@ -152,3 +152,43 @@ def test_adamw_8bit_states_keep_what_is_not_finite(param):
         assert torch.isnan(a["p"].cpu()[at]).all(), t
         for name in ("m", "v"):
             assert torch.isnan(a[name].view(torch.float8_e4m3fn).float().cpu()[at]).all(), (t, name)
+
+
+# ------------------------------------------------------------------ grouped products
+
+# tiles of 64 rows with and without a split reduction, of 128, of 256 (only where C is fp32 and experts are tall), and
+# the fp32 kernel's with and without a split
+@pytest.mark.parametrize("dt,N,K,counts,split", [(BF, 72, 136, [40, 0, 70, 33], False), (BF, 72, 136, [4700, 0, 0, 300], True),
+                                                 (BF, 1032, 520, [0, 300, 17, 0, 1], False), (BF, 520, 1032, TALL, False),
+                                                 (F32, 68, 36, [40, 0, 70, 33], False), (F32, 64, 64, [0, 4000, 0, 96], True)],
+                         ids=["64", "64split", "128", "256", "f32", "f32split"])
+def test_weight_gradients_leave_experts_without_rows(dt, N, K, counts, split):
+    """Adding to C: an expert without rows keeps its bits, negative zeros and NaN patterns among them."""
+    B = _B()
+    g = torch.Generator().manual_seed(31)
+    M = sum(counts)
+    a, b = rnd(g, M, N, dt=dt), rnd(g, M, K, dt=dt)
+    off = offsets_of(counts).cuda()
+    for out in (F32, BF) if dt == BF else (F32,):
+        c0 = rnd(g, len(counts), N, K, dt=out)
+        bits = torch.int32 if out == F32 else torch.int16
+        idle = [e for e, n in enumerate(counts) if n == 0]
+        for e in idle:
+            c0[e].view(-1)[0::3] = -0.0
+            c0[e].view(bits).view(-1)[1::5] = 0x7fa5 << (16 if out == F32 else 0)     # a signalling NaN
+        c = c0.cuda()
+        ac, bc = a.cuda(), b.cuda()
+        need = B.moe_grouped_gemm_workspace_size("tn", ac, bc, off, c)
+        assert (need > 0) == split
+        print(f"idle experts {dt} N={N} K={K} {out} ws={need}", flush=True)
+        B.moe_grouped_gemm("tn", ac, bc, off, c, torch.empty(need, dtype=torch.uint8, device="cuda"), accumulate=True)
+        for e in idle:
+            assert torch.equal(c[e].cpu().view(bits), c0[e].view(bits)), e
+        for e, r in spans(counts):
+            if counts[e]:
+                x, y, z = a[r].double().T, b[r].double(), c0[e].double()
+                check(c[e], x @ y + z, x.abs() @ y.abs() + z.abs(), max(counts) + 32, "beside idle experts")
+        # without adding: zeros
+        B.moe_grouped_gemm("tn", ac, bc, off, c, torch.empty(need, dtype=torch.uint8, device="cuda"))
+        for e in idle:
+            assert (c[e].cpu().view(bits) == 0).all(), e
