@@ -176,6 +176,10 @@ class TrainLayer:
         if self.fresh:
             raise RuntimeError("step() follows backward()")
         self.steps.add_(1)
-        B.moe_adamw_step(self.table, self.hyper, self.steps, lr_scale=lr_scale, grad_scale=grad_scale)
+        try:
+            B.moe_adamw_step(self.table, self.hyper, self.steps, lr_scale=lr_scale, grad_scale=grad_scale)
+        except Exception:
+            self.steps.sub_(1)                # refused: no update has been made
+            raise
         self.zero_grad()
         self.T = 0                            # the weights are no longer those of the last forward pass

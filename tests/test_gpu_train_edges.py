@@ -192,3 +192,30 @@ def test_weight_gradients_leave_experts_without_rows(dt, N, K, counts, split):
         B.moe_grouped_gemm("tn", ac, bc, off, c, torch.empty(need, dtype=torch.uint8, device="cuda"))
         for e in idle:
             assert (c[e].cpu().view(bits) == 0).all(), e
+
+
+# ------------------------------------------------------------------ the layer
+
+def test_train_layer_step_that_is_refused_changes_nothing():
+    """A step refused for its scalars leaves the step count, so that the next one corrects its moments as the first."""
+    from combine_dual_overlap_amd import TrainLayer
+    B = _B()
+    cfg, inp = _layer_inputs(2, "bf16", forced=False)
+    x = inp["x"].cuda()
+    dout = rnd(torch.Generator().manual_seed(8), *x.shape, dt=BF).cuda()
+    a, b = TrainLayer(inp), TrainLayer(inp)
+    for layer in (a, b):
+        layer.forward(x)
+        layer.backward(dout)
+    two = torch.ones(8, device="cuda")
+    for kw, err in ((dict(lr_scale=torch.ones(1, dtype=torch.float64, device="cuda")), ValueError),
+                    (dict(grad_scale=torch.ones(2, device="cuda")), ValueError), (dict(lr_scale=torch.ones(1)), ValueError),
+                    (dict(lr_scale=two[1:2]), B.MoEError)):
+        with pytest.raises(err):
+            a.step(**kw)
+        assert a.steps.item() == 0
+    a.step()
+    b.step()
+    assert a.steps.item() == 1
+    for n in a.weights:
+        assert torch.equal(a.weights[n], b.weights[n]), n
