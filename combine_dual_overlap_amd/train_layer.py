@@ -23,13 +23,19 @@ class TrainLayer:
     they are rounded stochastically).  The remaining keywords are those of
     binding.adamw_params.
 
-    forward(x) -> out [T, H]; backward(dout) -> dx [T, H], adding to the
-    gradients in `grads` (zero_grad() starts them anew); step() updates the
-    weights and zeroes the gradients; the next backward() needs a new forward().
-    Outputs live in the layer's buffers
-    until the next call; x must stay as it is until backward().  Calls run on the
-    current stream of the layer's device; calls of one layer on several streams
-    need the caller's ordering.
+    forward(x) -> out [T, H]; backward(dout) -> dx [T, H], of the last forward(),
+    adding to the gradients in `grads`; zero_grad() zeroes them; step() updates
+    the weights and zeroes the gradients; the next backward() needs a new
+    forward().  (The first backward() after either writes the gradients without
+    reading them: what else was put there in between is replaced.)  Outputs live
+    in the layer's buffers until the next call; x must stay as it is until
+    backward().  Calls run on the current stream of the layer's device; calls of
+    one layer on several streams need the caller's ordering.
+
+    forward(), backward() and step() can be captured, each by itself or together;
+    a replay is a call, in order with the others, and uses the same buffers.  From
+    the first capture on every backward() adds, and step() no longer checks that a
+    backward() came before it: the host does not see replays.
     """
 
     def __init__(self, inp: dict, device: str = "cuda", T_max: int = None, grad_dtype=torch.float32,
@@ -75,7 +81,8 @@ class TrainLayer:
         self.ws_gemm = new(B.GEMM_MAX_WORKSPACE, dt=torch.uint8)      # whatever the number of tokens
 
         self.grads = {name: torch.zeros(w.shape, dtype=grad_dtype, device=d) for name, w in self.weights.items()}
-        self.fresh = True                     # no gradient has been added since zero_grad()
+        self.fresh = True                     # the gradients are zero
+        self.captured = False                 # calls were captured: `fresh` says nothing any more
         ws = list(self.weights.values())
         self.master = [w.float() for w in ws] if act == torch.bfloat16 and master else None
         if states == "fp8":
@@ -145,7 +152,7 @@ class TrainLayer:
             return self._backward(dout)
 
     def _backward(self, dout):
-        W, G, more = self.weights, self.grads, not self.fresh
+        W, G, more = self.weights, self.grads, self._captured() or not self.fresh
         logits, ids, w, inv, x_perm, gu, h, y_perm, dy, dw, dgu, dx_perm, dlogits, dx_dense, dx = self._rows(
             "logits", "ids", "w", "inv", "x_perm", "gu", "h", "y_perm", "dy_perm", "dw", "dgu", "dx_perm", "dlogits",
             "dx_dense", "dx")
@@ -168,12 +175,20 @@ class TrainLayer:
         self.fresh = False
         return dx
 
+    def _captured(self):
+        self.captured = self.captured or torch.cuda.is_current_stream_capturing()
+        return self.captured
+
     def zero_grad(self):
+        with torch.cuda.device(self.device):
+            self._captured()
+            for g in self.grads.values():
+                g.zero_()
         self.fresh = True
 
     def step(self, lr_scale=None, grad_scale=None):
         """One AdamW update from the gradients added since zero_grad(); lr_scale, grad_scale: device scalars."""
-        if self.fresh:
+        if self.fresh and not self.captured:
             raise RuntimeError("step() follows backward()")
         self.steps.add_(1)
         try:

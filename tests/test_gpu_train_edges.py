@@ -219,3 +219,71 @@ def test_train_layer_step_that_is_refused_changes_nothing():
     assert a.steps.item() == 1
     for n in a.weights:
         assert torch.equal(a.weights[n], b.weights[n]), n
+
+
+def test_train_layer_zeroes_its_gradients():
+    """What a reader of the gradients sees after zero_grad() and after step()."""
+    from combine_dual_overlap_amd import TrainLayer
+    _B()
+    cfg, inp = _layer_inputs(2, "bf16", forced=False)
+    layer = TrainLayer(inp)
+    x = inp["x"].cuda()
+    grads = dict(layer.grads)
+    for end in (layer.zero_grad, layer.step):
+        layer.forward(x)
+        layer.backward(x)
+        assert all((t != 0).any() for t in grads.values())
+        end()
+        assert all((t == 0).all() for t in grads.values())
+
+
+def test_train_layer_captured_micro_steps():
+    """One forward and backward captured while no gradient had been added, then replayed: every replay adds, also after
+    zero_grad(), between eager calls and around eager steps; each state equals the same eager calls'."""
+    from combine_dual_overlap_amd import TrainLayer
+    _B()
+    cfg, inp = _layer_inputs(2, "bf16", forced=False)
+    g = torch.Generator().manual_seed(8)
+    kw = dict(lr=2.0 ** -8)
+    a, b, warm = TrainLayer(inp, **kw), TrainLayer(inp, **kw), TrainLayer(inp, **kw)
+    x, dout = inp["x"].cuda(), rnd(g, *inp["x"].shape, dt=BF).cuda()
+
+    def one(layer):
+        layer.forward(x)
+        layer.backward(dout)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        one(warm)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one(b)
+    replay = lambda: graph.replay()
+    eager = lambda: one(b)
+    for calls in ((replay, replay, replay), (replay,), (eager, replay), (replay, eager, replay), (eager,)):
+        for call in calls:
+            x.copy_(rnd(g, *x.shape, dt=BF))
+            one(a)
+            call()
+            torch.cuda.synchronize()
+            for n in a.grads:
+                assert torch.equal(a.grads[n], b.grads[n]), (n, len(calls))
+        a.step()
+        b.step()
+        for n in a.weights:
+            assert torch.equal(a.weights[n], b.weights[n]), n
+    # what zero_grad() drops is gone for the replays too
+    one(a)
+    graph.replay()
+    a.zero_grad()
+    b.zero_grad()
+    one(a)
+    graph.replay()
+    torch.cuda.synchronize()
+    for n in a.grads:
+        assert torch.equal(a.grads[n], b.grads[n]), n
+    a.step()
+    b.step()                                                  # follows a replayed backward
+    for n in a.weights:
+        assert torch.equal(a.weights[n], b.weights[n]), n
