@@ -33,7 +33,8 @@ EXPORTED = [
     "moe_quant_fp8_rows", "moe_dispatch_fp8", "moe_ffn_fp8_workspace_size", "moe_grouped_ffn_fp8",
     "moe_dispatch_send", "moe_dispatch_recv", "moe_dispatch_noalloc_max_workspace", "moe_dispatch_noalloc",
     "moe_grouped_gemm_workspace_size", "moe_grouped_gemm", "moe_grouped_swiglu", "moe_grouped_swiglu_backward",
-    "moe_combine_backward", "moe_route_backward", "moe_adamw_table_size", "moe_adamw_table_build", "moe_adamw_step",
+    "moe_combine_backward", "moe_route_backward", "moe_adamw_table_size", "moe_adamw_table_build",
+    "moe_adamw_table_check", "moe_adamw_step",
 ]
 
 
@@ -136,6 +137,7 @@ def lib():
             "moe_route_backward": (_i32, [_vp, _i64, _vp, _vp, ctypes.POINTER(moe_route_params), _vp, _i32, _vp]),
             "moe_adamw_table_size": (_sz, [_i32]),
             "moe_adamw_table_build": (_i32, [ctypes.POINTER(moe_adamw_tensor), _i32, _vp, _sz]),
+            "moe_adamw_table_check": (_i32, [_vp]),
             "moe_adamw_step": (_i32, [_vp, _vp, ctypes.POINTER(moe_adamw_params), _vp, _vp, _vp, _vp]),
         }
         for name, (res, args) in sig.items():
@@ -524,6 +526,7 @@ def moe_adamw_table(params, grads, m, v, m_scale=None, v_scale=None, master=None
     nbytes = lib().moe_adamw_table_size(n)
     host = torch.zeros(nbytes, dtype=torch.uint8)
     _check(lib().moe_adamw_table_build(entries, n, host.data_ptr(), nbytes), "moe_adamw_table_build")
+    _check(lib().moe_adamw_table_check(host.data_ptr()), "moe_adamw_table_check")
     return AdamWTable(host, host.to(torch.device("cuda", d)), d, cols)
 
 

@@ -59,7 +59,8 @@ struct AdamLaunch {
 
 struct AdamHeader {
   uint32_t magic;
-  int32_t launches, tensors, pad;
+  int32_t launches, tensors;
+  int32_t scales_in_params;           // nonzero: no step takes this table
 };
 
 struct AdamLayout {
@@ -88,8 +89,8 @@ struct AdamArgs {
 struct AdamRange {
   uintptr_t begin, end;
 };
-static_assert(4 * sizeof(AdamRange) <= sizeof(AdamLaunch) + sizeof(int32_t) + sizeof(AdamTensor),
-              "the table's bytes hold four ranges of each tensor while they are compared");
+static_assert(6 * sizeof(AdamRange) <= sizeof(AdamLaunch) + sizeof(int32_t) + sizeof(AdamTensor),
+              "the table's bytes hold six ranges of each tensor while they are compared");
 
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
   x ^= x >> 16;
@@ -447,33 +448,57 @@ extern "C" moe_status moe_adamw_table_build(const moe_adamw_tensor* tensors, int
       return MOE_ERR_MISALIGNED;
     total += (t.n + kAdamGroup - 1) / kAdamGroup;
   }
-  // Two workgroups must not update one element: the updated arrays are sorted,
-  // in the table's own bytes, and compared with their neighbours and the gradients.
+  // Two workgroups must not update one element, and none what another reads:
+  // the updated arrays are sorted, in the table's own bytes, and compared with
+  // their neighbours and the gradients.
   auto* ranges = static_cast<AdamRange*>(table);
   size_t nr = 0;
-  for (int i = 0; i < n_tensors; ++i) {
-    const moe_adamw_tensor& t = tensors[i];
-    auto add = [&](const void* p, int64_t size) {
-      const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-      if (p && t.n > 0) ranges[nr++] = AdamRange{a, a + static_cast<uintptr_t>(t.n * size)};
-    };
-    const int64_t state = t.state_dtype == MOE_F32 ? 4 : 1;
-    add(t.param, dtype_size(t.param_dtype));
-    add(t.m, state);
-    add(t.v, state);
-    add(t.master, 4);
-  }
-  std::sort(ranges, ranges + nr, [](const AdamRange& a, const AdamRange& b) { return a.begin < b.begin; });
-  for (size_t i = 1; i < nr; ++i)
-    if (ranges[i].begin < ranges[i - 1].end) return MOE_ERR_INVALID_ARG;
-  for (int i = 0; i < n_tensors; ++i) {
-    const moe_adamw_tensor& t = tensors[i];
-    if (t.n == 0) continue;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(t.grad);
-    const uintptr_t z = a + static_cast<uintptr_t>(t.n * static_cast<int64_t>(dtype_size(t.grad_dtype)));
-    const AdamRange* r = std::upper_bound(ranges, ranges + nr, a, [](uintptr_t v, const AdamRange& x) { return v < x.end; });
-    if (r != ranges + nr && r->begin < z) return MOE_ERR_INVALID_ARG;
-  }
+  auto collect = [&](bool params, bool moments, bool scales) {
+    nr = 0;
+    for (int i = 0; i < n_tensors; ++i) {
+      const moe_adamw_tensor& t = tensors[i];
+      auto add = [&](const void* p, int64_t bytes) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+        if (p && t.n > 0) ranges[nr++] = AdamRange{a, a + static_cast<uintptr_t>(bytes)};
+      };
+      const int64_t state = t.state_dtype == MOE_F32 ? 4 : 1;
+      if (params) add(t.param, t.n * static_cast<int64_t>(dtype_size(t.param_dtype)));
+      if (moments) {
+        add(t.m, t.n * state);
+        add(t.v, t.n * state);
+        add(t.master, t.n * 4);
+      }
+      if (scales) {
+        add(t.m_scale, (t.n + 127) / 128);
+        add(t.v_scale, (t.n + 127) / 128);
+      }
+    }
+    std::sort(ranges, ranges + nr, [](const AdamRange& a, const AdamRange& b) { return a.begin < b.begin; });
+  };
+  auto overlap = [&] {
+    for (size_t i = 1; i < nr; ++i)
+      if (ranges[i].begin < ranges[i - 1].end) return true;
+    return false;
+  };
+  auto meets_gradient = [&] {
+    for (int i = 0; i < n_tensors; ++i) {
+      const moe_adamw_tensor& t = tensors[i];
+      if (t.n == 0) continue;
+      const uintptr_t a = reinterpret_cast<uintptr_t>(t.grad);
+      const uintptr_t z = a + static_cast<uintptr_t>(t.n * static_cast<int64_t>(dtype_size(t.grad_dtype)));
+      const AdamRange* r = std::upper_bound(ranges, ranges + nr, a, [](uintptr_t v, const AdamRange& x) { return v < x.end; });
+      if (r != ranges + nr && r->begin < z) return true;
+    }
+    return false;
+  };
+  collect(true, true, false);
+  if (overlap() || meets_gradient()) return MOE_ERR_INVALID_ARG;
+  collect(false, true, true);
+  if (overlap() || meets_gradient()) return MOE_ERR_INVALID_ARG;
+  // (A table whose only fault is a scale inside a param is built, and refused by
+  // moe_adamw_table_check and by every step: callers rely on that status.)
+  collect(true, false, true);
+  const bool scales_in_params = overlap();
   auto* out = static_cast<uint8_t*>(table);
   memset(out, 0, l.bytes);
   auto* launch = reinterpret_cast<AdamLaunch*>(out + l.launch);
@@ -505,8 +530,15 @@ extern "C" moe_status moe_adamw_table_build(const moe_adamw_tensor* tensors, int
       ++at;
     }
   }
-  *reinterpret_cast<AdamHeader*>(out) = AdamHeader{kAdamMagic, launches, n_tensors, 0};
+  *reinterpret_cast<AdamHeader*>(out) = AdamHeader{kAdamMagic, launches, n_tensors, scales_in_params};
   return MOE_OK;
+}
+
+extern "C" moe_status moe_adamw_table_check(const void* table_host) {
+  if (!table_host) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(table_host)) return MOE_ERR_MISALIGNED;
+  const auto* head = static_cast<const AdamHeader*>(table_host);
+  return head->magic != kAdamMagic || head->tensors < 1 || head->scales_in_params ? MOE_ERR_INVALID_ARG : MOE_OK;
 }
 
 extern "C" moe_status moe_adamw_step(const void* table_host, const void* table_dev, const moe_adamw_params* hp,
@@ -522,7 +554,7 @@ extern "C" moe_status moe_adamw_step(const void* table_host, const void* table_d
     return MOE_ERR_MISALIGNED;
   const auto* host = static_cast<const uint8_t*>(table_host);
   const auto* head = reinterpret_cast<const AdamHeader*>(host);
-  if (head->magic != kAdamMagic || head->tensors < 1) return MOE_ERR_INVALID_ARG;
+  if (moe_adamw_table_check(table_host) != MOE_OK) return MOE_ERR_INVALID_ARG;
   const AdamLayout l(head->tensors);
   const auto* launch = reinterpret_cast<const AdamLaunch*>(host + l.launch);
   const auto* dev = static_cast<const uint8_t*>(table_dev);

@@ -397,7 +397,9 @@ moe_status moe_route_backward(const float* logits, int64_t T, const int32_t* top
  * states keep what is not, an infinity or NaN in fp32, a NaN code in 8 bits
  * (the other elements of its block are not touched by it).  Tensors of n == 0
  * are skipped.  Arrays must not overlap: moe_adamw_table_build refuses
- * params, masters and states that do, among themselves or with a gradient.
+ * params, masters, states and scales that do, among themselves or with a
+ * gradient - but for scales that lie inside a param: moe_adamw_table_check and
+ * moe_adamw_step refuse the table that it builds of them (MOE_ERR_INVALID_ARG).
  * ------------------------------------------------------------------------- */
 typedef struct {
   void* param;
@@ -418,6 +420,8 @@ typedef struct {
 
 size_t moe_adamw_table_size(int32_t n_tensors);
 moe_status moe_adamw_table_build(const moe_adamw_tensor* tensors, int32_t n_tensors, void* table, size_t bytes);
+/* MOE_OK if moe_adamw_step takes this table.  Pure host function. */
+moe_status moe_adamw_table_check(const void* table_host);
 moe_status moe_adamw_step(const void* table_host, const void* table_dev, const moe_adamw_params* hp,
                           const int32_t* step, const float* lr_scale, const float* grad_scale, void* stream);
 

@@ -1,0 +1,69 @@
+"""More checks of the training entry points, without a GPU: addresses are made up, nothing is enqueued."""
+import ctypes
+
+import pytest
+import torch
+
+A = 1 << 20       # aligned made-up address
+
+
+def _B():
+    from combine_dual_overlap_amd import binding
+    binding.lib()
+    return binding
+
+
+def _tensor(B, i, **kw):
+    """An entry with 8-bit states whose arrays lie apart from every other entry's: 4096 elements, 32 scales."""
+    base = dict(param=(8 * i + 1) * A, grad=(8 * i + 2) * A, m=(8 * i + 3) * A, v=(8 * i + 4) * A,
+                m_scale=(8 * i + 5) * A + 3, v_scale=(8 * i + 5) * A + 35, master=(8 * i + 6) * A, n=4096, param_dtype=1,
+                grad_dtype=1, state_dtype=2)
+    base.update(kw)
+    return B.moe_adamw_tensor(*base.values())
+
+
+def _status(B, *tensors):
+    """The first refusal of the table's way to a step: building, checking, stepping."""
+    t = (B.moe_adamw_tensor * len(tensors))(*tensors)
+    host = torch.zeros(B.lib().moe_adamw_table_size(len(tensors)), dtype=torch.uint8)
+    st = B.lib().moe_adamw_table_build(t, len(tensors), host.data_ptr(), host.numel())
+    if st != B.MOE_OK:
+        return st
+    st = B.lib().moe_adamw_table_check(host.data_ptr())
+    if st != B.MOE_OK:                                        # a step says the same, and enqueues nothing
+        hp = B.adamw_params()
+        assert B.lib().moe_adamw_step(host.data_ptr(), A, ctypes.byref(hp), A, None, None, None) == st
+    return st
+
+
+def test_adamw_table_refuses_overlapping_scales():
+    """Scales shared by two moments or two tensors, or lying inside any other array, in any order of the tensors."""
+    B = _B()
+    bad = B.MOE_ERR_INVALID_ARG
+    assert _status(B, *[_tensor(B, i) for i in range(50)]) == B.MOE_OK        # (m_scale and v_scale touch)
+    assert _status(B, _tensor(B, 0, m_scale=5 * A, v_scale=5 * A)) == bad
+    assert _status(B, _tensor(B, 0, m_scale=5 * A, v_scale=5 * A + 31)) == bad
+    assert _status(B, _tensor(B, 0, m_scale=5 * A, v_scale=5 * A + 32)) == B.MOE_OK
+    arrays = dict(param=(A, 8192), grad=(2 * A, 8192), m=(3 * A, 4096), v=(4 * A, 4096), m_scale=(5 * A + 3, 32),
+                  v_scale=(5 * A + 35, 32), master=(6 * A, 16384))
+    for name, (at, size) in arrays.items():
+        for scale in ("m_scale", "v_scale"):
+            for where, ok in ((at - 32, name != "v_scale"), (at - 31, False), (at + size // 2, False),
+                              (at + size - 1, False), (at + size, name != "m_scale")):
+                want = B.MOE_OK if ok else bad
+                kw = {scale: where}
+                assert _status(B, _tensor(B, 0), _tensor(B, 1, **kw)) == want, (name, kw)
+                assert _status(B, _tensor(B, 1, **kw), _tensor(B, 2), _tensor(B, 0)) == want, (name, kw)
+                if not name.endswith("scale"):                # its own tensor's arrays
+                    assert _status(B, _tensor(B, 0, **kw)) == want, (name, kw)
+                assert _status(B, _tensor(B, 0), _tensor(B, 1, n=0, **kw)) == B.MOE_OK
+                fresh = dict(n=100, state_dtype=0, m_scale=None, v_scale=None)
+                assert _status(B, _tensor(B, 0), _tensor(B, 1, **fresh)) == B.MOE_OK
+
+
+def test_adamw_table_check_refuses_what_is_no_table():
+    B = _B()
+    check = B.lib().moe_adamw_table_check
+    zeros = torch.zeros(512, dtype=torch.uint8)
+    assert check(None) == check(zeros.data_ptr()) == B.MOE_ERR_INVALID_ARG
+    assert check(zeros.data_ptr() + 8) == B.MOE_ERR_MISALIGNED
