@@ -57,15 +57,23 @@ class TrainLayer:
             raise ValueError("the number of experts must be a multiple of 8 (float32: 4)")
         self.act, self.T_max = act, T_max or inp["x"].shape[0]
         sh13, sh2, shI = concat_shared(inp.get("shared_w13") or [], inp.get("shared_w2") or [])
-        own = lambda t: None if t is None else t.contiguous().to(d, copy=True)   # trained in place
-        self.weights = {"w_router": own(inp["w_router"])[None], "w13": own(inp["w13"]), "w2": own(inp["w2"])}
+        H, I, E_loc = cfg.H, cfg.I, cfg.expert_end - cfg.expert_begin
+
+        def own(name, t, *shape):             # trained in place
+            if t.dtype != act or t.shape != shape:
+                raise ValueError(f"{name}: {act} {list(shape)}")
+            return t.contiguous().to(d, copy=True)
+
+        self.weights = {"w_router": own("w_router", inp["w_router"], cfg.E, H)[None],
+                        "w13": own("w13", inp["w13"], E_loc, 2 * I, H), "w2": own("w2", inp["w2"], E_loc, H, I)}
         if shI:
-            self.weights["shared_w13"], self.weights["shared_w2"] = own(sh13)[None], own(sh2)[None]
+            self.weights["shared_w13"] = own("shared_w13", sh13, 2 * shI, H)[None]
+            self.weights["shared_w2"] = own("shared_w2", sh2, H, shI)[None]
         self.route = B.route_params(cfg.E, cfg.k, cfg.score, cfg.renormalize, cfg.n_groups, cfg.topk_groups,
                                     cfg.group_topn, cfg.routed_scale)
 
-        H, I, k, E, T = cfg.H, cfg.I, cfg.k, cfg.E, self.T_max
-        n, E_loc = T * k, cfg.expert_end - cfg.expert_begin
+        k, E, T = cfg.k, cfg.E, self.T_max
+        n = T * k
         new = lambda *shape, dt=act: torch.empty(shape, dtype=dt, device=d)
         i32, f32 = torch.int32, torch.float32
         self.buf = dict(logits=new(T, E, dt=f32), ids=new(T, k, dt=i32), w=new(T, k, dt=f32), counts=new(E_loc, dt=i32),

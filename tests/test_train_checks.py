@@ -67,3 +67,30 @@ def test_adamw_table_check_refuses_what_is_no_table():
     zeros = torch.zeros(512, dtype=torch.uint8)
     assert check(None) == check(zeros.data_ptr()) == B.MOE_ERR_INVALID_ARG
     assert check(zeros.data_ptr() + 8) == B.MOE_ERR_MISALIGNED
+
+
+def _refused(match, device="cpu", **kw):
+    """TrainLayer refuses the small fp32 (cid 1) or bf16 (cid 2) layer with these inputs changed, before it needs a GPU."""
+    import workloads as W
+    from combine_dual_overlap_amd import TrainLayer
+    inp = W.make_inputs(W.get_config(kw.pop("cid", 2), small=True))
+    inp.update({n: f(inp[n]) for n, f in kw.items()})
+    with pytest.raises(ValueError, match=match):
+        TrainLayer(inp, device=device)
+
+
+def test_train_layer_refuses_weights_of_another_type_or_shape():
+    """The kernels read every weight as the activations' type: a smaller one would be read behind its end."""
+    half, full = (lambda t: t.to(torch.bfloat16)), (lambda t: t.float())
+    for name in ("w_router", "w2"):
+        _refused(name, cid=1, **{name: half})
+        _refused(name, cid=2, **{name: full})
+        _refused(name, **{name: lambda t: t.double()})
+        for cut in (lambda t: t[:-1], lambda t: t[..., :-8], lambda t: t[None], lambda t: t.transpose(-1, -2)):
+            _refused(name, **{name: cut})
+    for cut in (lambda t: t[:-1], lambda t: t[..., :-8], lambda t: t[:, :-8]):
+        _refused("w13", w13=cut)
+    _refused("shared_w13", shared_w13=lambda ts: [t.float() for t in ts])
+    _refused("shared_w2", shared_w2=lambda ts: [t.float() for t in ts])
+    _refused("shared_w13", shared_w13=lambda ts: [t[..., :-8] for t in ts])
+    _refused("shared_w2", shared_w2=lambda ts: [t[:-8] for t in ts])
