@@ -119,12 +119,13 @@ class TrainLayer:
     def forward(self, x, forced_ids=None):
         cfg = self.cfg
         self.T = 0                            # backward() refuses after a forward pass that failed
-        if x.dtype != self.act or x.dim() != 2 or x.shape[1] != cfg.H or not 0 < x.shape[0] <= self.T_max:
-            raise ValueError(f"x: [T, {cfg.H}] of {self.act}, 1 <= T <= {self.T_max}")
+        if (x.dtype != self.act or x.dim() != 2 or x.shape[1] != cfg.H or not 0 < x.shape[0] <= self.T_max or
+                x.device != self.device):
+            raise ValueError(f"x: [T, {cfg.H}] of {self.act} on {self.device}, 1 <= T <= {self.T_max}")
         forced = self.forced_ids if forced_ids is None else forced_ids
         if forced is not None and (forced.dtype != torch.int32 or forced.dim() != 2 or forced.shape[0] < x.shape[0] or
-                                   forced.shape[1] != cfg.k):
-            raise ValueError(f"forced_ids: int32 [{x.shape[0]}, {cfg.k}]")
+                                   forced.shape[1] != cfg.k or forced.device != self.device):
+            raise ValueError(f"forced_ids: int32 [{x.shape[0]}, {cfg.k}] on {self.device}")
         self.T, self.x = x.shape[0], x
         try:
             with torch.cuda.device(self.device):

@@ -94,3 +94,20 @@ def test_train_layer_refuses_weights_of_another_type_or_shape():
     _refused("shared_w2", shared_w2=lambda ts: [t.float() for t in ts])
     _refused("shared_w13", shared_w13=lambda ts: [t[..., :-8] for t in ts])
     _refused("shared_w2", shared_w2=lambda ts: [t[:-8] for t in ts])
+
+
+def test_train_layer_refuses_tokens_on_another_device():
+    """x and forced_ids are read by kernels of the layer's device (no GPU here: a layer without buffers, tensors
+    without memory)."""
+    from types import SimpleNamespace
+    from combine_dual_overlap_amd import TrainLayer
+    layer = object.__new__(TrainLayer)
+    layer.cfg, layer.act, layer.T_max = SimpleNamespace(H=128, k=2), torch.bfloat16, 4
+    layer.device, layer.forced_ids = torch.device("cuda", 0), None
+    x = torch.empty(4, 128, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="x: .*cuda:0"):
+        layer.forward(x)
+    layer.device = torch.device("meta")
+    with pytest.raises(ValueError, match="forced_ids: .*meta"):
+        layer.forward(x, forced_ids=torch.zeros(4, 2, dtype=torch.int32))
+    assert layer.T == 0
