@@ -1047,15 +1047,20 @@ static moe_status gg_launch(GgParams& p, const GgPlan& q, bool f32, hipStream_t 
 }
 
 // Checks that every grouped product shares.  E_loc, sizes and types only.
-static moe_status gg_check(moe_dtype ab, const int32_t* offsets, int32_t E_loc, int64_t cap_rows, int32_t N, int32_t K) {
+static moe_status gg_check_sizes(moe_dtype ab, bool dense, int32_t E_loc, int64_t cap_rows, int32_t N, int32_t K) {
   if (E_loc < 1 || E_loc > 256 || cap_rows < 0 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
-  if (!offsets && E_loc != 1) return MOE_ERR_INVALID_ARG;
+  if (dense && E_loc != 1) return MOE_ERR_INVALID_ARG;
   if (ab != MOE_F32 && ab != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (cap_rows > (1 << 30) || N > (1 << 22) || K > (1 << 22)) return MOE_ERR_UNSUPPORTED;
   const int q = ab == MOE_F32 ? 4 : 8;        // rows start on 16 bytes
   if (N % q || K % q) return MOE_ERR_MISALIGNED;
-  if (offsets && !aligned16(offsets)) return MOE_ERR_MISALIGNED;
   return MOE_OK;
+}
+
+static moe_status gg_check(moe_dtype ab, const int32_t* offsets, int32_t E_loc, int64_t cap_rows, int32_t N, int32_t K) {
+  const moe_status st = gg_check_sizes(ab, !offsets, E_loc, cap_rows, N, K);
+  if (st != MOE_OK) return st;
+  return offsets && !aligned16(offsets) ? MOE_ERR_MISALIGNED : MOE_OK;
 }
 
 }  // namespace dbomoe
@@ -1065,7 +1070,7 @@ using namespace dbomoe;
 extern "C" size_t moe_grouped_gemm_workspace_size(moe_gemm_kind kind, moe_dtype ab, int32_t dense, int32_t E_loc,
                                                   int64_t cap_rows, int32_t N, int32_t K) {
   if (kind != MOE_GEMM_NT && kind != MOE_GEMM_NN && kind != MOE_GEMM_TN) return 0;
-  if (E_loc < 1 || E_loc > 256 || cap_rows < 1 || N < 1 || K < 1) return 0;
+  if (cap_rows < 1 || gg_check_sizes(ab, dense != 0, E_loc, cap_rows, N, K) != MOE_OK) return 0;
   const int S = gg_plan(kind, EPI_STORE, ab == MOE_F32, E_loc, cap_rows, dense != 0, N, K).splits;
   if (S == 1) return 0;
   const size_t out = kind == MOE_GEMM_TN ? static_cast<size_t>(E_loc) * N * K : static_cast<size_t>(cap_rows) * N;

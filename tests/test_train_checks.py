@@ -111,3 +111,17 @@ def test_train_layer_refuses_tokens_on_another_device():
     with pytest.raises(ValueError, match="forced_ids: .*meta"):
         layer.forward(x, forced_ids=torch.zeros(4, 2, dtype=torch.int32))
     assert layer.T == 0
+
+
+def test_workspace_query_of_sizes_without_a_product():
+    """Sizes and types that moe_grouped_gemm refuses need no workspace, also where their tile counts leave 32 bits."""
+    B = _B()
+    top = (1 << 31) - 8
+    ask = B.lib().moe_grouped_gemm_workspace_size
+    assert ask(2, 1, 1, 1, 8192, 64, 64) > 0
+    for kind in (0, 1, 2):
+        for args in ((1, 1, 1, 64, top, 4096), (1, 1, 1, 64, 64, top), (1, 1, 1, 64, (1 << 22) + 8, 4096),
+                     (1, 1, 1, 64, 64, (1 << 22) + 8), (1, 1, 1, (1 << 30) + 1, 64, 4096), (1, 1, 1, 1 << 62, 64, 64),
+                     (0, 0, 256, 8192, top, top), (2, 1, 1, 8192, 64, 64), (-1, 1, 1, 8192, 64, 64),
+                     (1, 1, 2, 8192, 64, 64), (1, 1, 1, 8192, 60, 64), (0, 1, 1, 8192, 64, 62)):
+            assert ask(kind, *args) == 0, (kind, args)
