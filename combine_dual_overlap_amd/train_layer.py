@@ -48,6 +48,8 @@ class TrainLayer:
         act = inp["x"].dtype
         if act not in (torch.float32, torch.bfloat16) or inp["w13"].dtype != act:
             raise ValueError("trainable weights are float32 or bfloat16, in the activations' type")
+        if grad_dtype not in (torch.float32, act):
+            raise ValueError("grad_dtype: float32, or bfloat16 with bfloat16 weights")
         if states not in ("f32", "fp8"):
             raise ValueError("states: f32 or fp8")
         self.logit_bias, self.forced_ids = _dev(inp.get("logit_bias"), d), _dev(inp.get("forced_ids"), d)

@@ -125,3 +125,12 @@ def test_workspace_query_of_sizes_without_a_product():
                      (0, 0, 256, 8192, top, top), (2, 1, 1, 8192, 64, 64), (-1, 1, 1, 8192, 64, 64),
                      (1, 1, 2, 8192, 64, 64), (1, 1, 1, 8192, 60, 64), (0, 1, 1, 8192, 64, 62)):
             assert ask(kind, *args) == 0, (kind, args)
+
+
+def test_train_layer_refuses_gradient_types_that_backward_cannot_write():
+    """fp32 activations have fp32 gradients; others were refused by the first backward() only, or by the optimizer."""
+    import workloads as W
+    from combine_dual_overlap_amd import TrainLayer
+    for cid, dt in ((1, torch.bfloat16), (1, torch.float16), (2, torch.float16), (2, torch.float64)):
+        with pytest.raises(ValueError, match="grad_dtype"):
+            TrainLayer(W.make_inputs(W.get_config(cid, small=True)), device="cpu", grad_dtype=dt)
