@@ -194,6 +194,109 @@ def test_weight_gradients_leave_experts_without_rows(dt, N, K, counts, split):
             assert (c[e].cpu().view(bits) == 0).all(), e
 
 
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+def test_weight_gradients_of_no_rows_at_all(dt):
+    """Row operands of length zero: zeros, or C as it was where the product is added."""
+    B = _B()
+    for E, off in ((1, None), (3, torch.zeros(4, dtype=torch.int32, device="cuda"))):
+        a, b = torch.empty(0, 72, dtype=dt, device="cuda"), torch.empty(0, 136, dtype=dt, device="cuda")
+        c = torch.full((E, 72, 136), -0.0, device="cuda")
+        B.moe_grouped_gemm("tn", a, b, off, c, accumulate=True)
+        assert (c.view(torch.int32) == -2 ** 31).all()
+        B.moe_grouped_gemm("tn", a, b, off, c)
+        assert (c.view(torch.int32) == 0).all()
+
+
+# ------------------------------------------------------------------ fp32 tiles, split reductions
+
+# rows around the 64-row tile and its second half, several tiles an expert (of equal height), one row, none
+TILES = [1, 33, 0, 63, 64, 65, 129, 200, 31, 32]
+
+
+@pytest.mark.parametrize("kind", ["nt", "nn"])
+def test_grouped_gemm_f32_of_many_tiles(kind):
+    """Enough 64 x 64 tiles that fp32 products take them."""
+    B = _B()
+    g = torch.Generator().manual_seed(41)
+    M, off = sum(TILES), offsets_of(TILES).cuda()
+    for N, K in ((1028, 100), (1092, 12)):
+        for acc in (False, True):
+            print(f"{kind} f32 N={N} K={K} acc={acc}", flush=True)
+            a, c0 = rnd(g, M + 3, K), rnd(g, M + 3, N)
+            a[M:] = math.nan
+            b = rnd(g, len(TILES), *((N, K) if kind == "nt" else (K, N)))
+            c = c0.cuda()
+            B.moe_grouped_gemm(kind, a.cuda(), b.cuda(), off, c, accumulate=acc)
+            ref, mag = _ref_rows(kind, a[:M], b, TILES)
+            if acc:
+                ref, mag = ref + c0[:M].double(), mag + c0[:M].double().abs()
+            check(c[:M], ref, mag, K, "f32 tiles")
+            assert torch.equal(c[M:].cpu(), c0[M:])
+
+
+def test_grouped_swiglu_f32_of_many_tiles():
+    B = _B()
+    g = torch.Generator().manual_seed(42)
+    M, off = sum(TILES), offsets_of(TILES).cuda()
+    for I, H in ((1028, 100), (1092, 12)):
+        print(f"swiglu f32 I={I} H={H}", flush=True)
+        x, w13 = rnd(g, M, H), rnd(g, len(TILES), 2 * I, H, std=H ** -0.5)
+        gu, h = torch.zeros(M + 2, 2 * I, device="cuda"), torch.zeros(M + 2, I, device="cuda")
+        xs = torch.cat([x, torch.full((2, H), math.nan)]).cuda()
+        B.moe_grouped_swiglu(xs, w13.cuda(), off, h, gu=gu)
+        ref, mag = _ref_rows("nt", x, w13, TILES)
+        check(gu[:M], ref, mag, H, "gu")
+        gate, up, mg, mu = ref[:, :I], ref[:, I:], mag[:, :I], mag[:, I:]
+        s = _sigmoid(gate)
+        check(h[:M], gate * s * up, (H + 2) * (1.1 * up.abs() * mg + (gate * s).abs() * mu) + 16 * (gate * s * up).abs(), -1, "h")
+        assert (gu[M:] == 0).all() and (h[M:] == 0).all()
+        dy, w2, gu64 = rnd(g, M, H), rnd(g, len(TILES), H, I, std=H ** -0.5), gu[:M].cpu().double()
+        dgu = torch.zeros(M + 2, 2 * I, device="cuda")
+        B.moe_grouped_swiglu_backward(torch.cat([dy, torch.full((2, H), math.nan)]).cuda(), w2.cuda(), gu, off, dgu)
+        dh, mag = _ref_rows("nn", dy, w2, TILES)
+        gate, up = gu64[:, :I], gu64[:, I:]
+        s = _sigmoid(gate)
+        fg, fu = (up * s).abs() * (1 + gate.abs() * (1 - s)), (gate * s).abs()
+        check(dgu[:M], _swiglu_bwd(dh, gu64, I), torch.cat([fg, fu], 1) * ((H + 2) * mag + 16 * dh.abs()).repeat(1, 2), -1, "dgu")
+        assert (dgu[M:] == 0).all()
+
+
+@pytest.mark.parametrize("acc", [False, True], ids=["write", "add"])
+@pytest.mark.parametrize("kind,cap,N,K,dt,out", [("tn", 5000, 72, 136, BF, BF), ("nt", 33, 72, 4104, BF, BF),
+                                                 ("nn", 33, 72, 4104, BF, BF), ("tn", 4096, 64, 64, F32, F32),
+                                                 ("tn", 4099, 68, 132, F32, F32)])
+def test_split_reductions_to_each_type(kind, cap, N, K, dt, out, acc):
+    """Parts of the fp32 kernel, and joins that write bf16: rounded once, rows and experts as in the unsplit call."""
+    B = _B()
+    g = torch.Generator().manual_seed(43)
+    for counts in (None, [cap // 3, 0, cap // 5, 1]):
+        E = 1 if counts is None else 4
+        if kind == "tn":
+            a, b, c0 = rnd(g, cap, N, dt=dt), rnd(g, cap, K, dt=dt), rnd(g, E, N, K, dt=out)
+        else:
+            a, c0 = rnd(g, cap, K, dt=dt), rnd(g, cap, N, dt=out)
+            b = rnd(g, E, *((N, K) if kind == "nt" else (K, N)), dt=dt)
+        off = None if counts is None else offsets_of(counts).cuda()
+        c, ac, bc = c0.cuda(), a.cuda(), b.cuda()
+        need = B.moe_grouped_gemm_workspace_size(kind, ac, bc, off, c)
+        print(f"split {kind} cap={cap} N={N} K={K} {dt} {out} acc={acc} E={E} ws={need}", flush=True)
+        assert need > 0 or counts is not None
+        ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")               # NaN patterns
+        B.moe_grouped_gemm(kind, ac, bc, off, c, ws, accumulate=acc)
+        z0 = c0.double() if acc else torch.zeros_like(c0, dtype=torch.float64)
+        ref, mag = z0.clone(), z0.abs()
+        for e, r in spans([cap] if counts is None else counts):
+            if kind == "tn":
+                x, y, z = a[r].double().T, b[r].double(), e
+            else:
+                x, y, z = a[r].double(), b[e].double().T if kind == "nt" else b[e].double(), r
+            ref[z] += x @ y
+            mag[z] += x.abs() @ y.abs()
+        rows = len(ref) if kind == "tn" or counts is None else sum(counts)
+        check(c[:rows], ref[:rows], mag[:rows], max(cap, K) + 32, "split")
+        assert torch.equal(c[rows:].cpu(), c0[rows:])
+
+
 # ------------------------------------------------------------------ the layer
 
 def test_train_layer_step_that_is_refused_changes_nothing():
