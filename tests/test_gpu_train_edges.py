@@ -390,3 +390,42 @@ def test_train_layer_captured_micro_steps():
     b.step()                                                  # follows a replayed backward
     for n in a.weights:
         assert torch.equal(a.weights[n], b.weights[n]), n
+
+
+def test_train_layer_calls_captured_one_by_one():
+    """forward(), backward() and step() in graphs of their own: two micro-steps and a step, three times, equal eager
+    calls."""
+    from combine_dual_overlap_amd import TrainLayer
+    _B()
+    cfg, inp = _layer_inputs(2, "bf16", forced=False)
+    g = torch.Generator().manual_seed(8)
+    kw = dict(lr=2.0 ** -8, states="fp8", master=False)
+    a, b, warm = TrainLayer(inp, **kw), TrainLayer(inp, **kw), TrainLayer(inp, **kw)
+    x, dout = inp["x"].cuda(), rnd(g, *inp["x"].shape, dt=BF).cuda()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        warm.forward(x)
+        warm.backward(dout)
+        warm.step()
+    torch.cuda.synchronize()
+    graphs = []
+    for call in (lambda: b.forward(x), lambda: b.backward(dout), b.step):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        graphs.append(graph)
+    with pytest.raises(RuntimeError):
+        b.backward(dout)                                      # the captured step moves the weights
+    for _ in range(3):
+        for _ in range(2):
+            x.copy_(rnd(g, *x.shape, dt=BF))
+            a.forward(x)
+            a.backward(dout)
+            graphs[0].replay()
+            graphs[1].replay()
+        a.step()
+        graphs[2].replay()
+        torch.cuda.synchronize()
+        for n in a.weights:
+            assert torch.equal(a.weights[n], b.weights[n]), n
+            assert (b.grads[n] == 0).all(), n
