@@ -297,38 +297,55 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
       load8<false, FULL, EIGHT>(t.m, i, n, m);
       load8<false, FULL, EIGHT>(t.v, i, n, v);
     }
-    if constexpr (PARAM == PARAM_MASTER)
-      load8<false, FULL, EIGHT>(t.master, i, n, p);
-    else
-      load8<PARAM == PARAM_BF16, FULL, EIGHT>(t.p, i, n, p);
+    auto load_p = [&](int64_t at, float* x) {
+      if constexpr (PARAM == PARAM_MASTER)
+        load8<false, FULL, EIGHT>(t.master, at, n, x);
+      else
+        load8<PARAM == PARAM_BF16, FULL, EIGHT>(t.p, at, n, x);
+    };
+    auto updated = [&](float old, float mj, float rj) {      // (the reciprocal's argument is at least eps, a normal number)
+      return old * decay - step_size * (mj * __builtin_amdgcn_rcpf(rj * rbc2 + a.eps));
+    };
+    auto moment2 = [&](float old, float gj) { return old * a.b2 + (gj * a.omb2) * gj; };
+    // EARLY: the update before the branch for small roots, which then repeats its
+    // elements' update.  44 M elements, 8-bit states, us: bf16 weights 95 to 98 (late
+    // 98 to 101), where they are in fp32, or a master is, 137 and 152 (late 131 and 145).
+    constexpr bool EARLY = EIGHT && PARAM == PARAM_BF16;
+    load_p(i, p);
+    float low = INFINITY;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      g[j] = g[j] * gs;
-      m[j] = m[j] * a.b1 + g[j] * a.omb1;
-      v[j] = v[j] * a.b2 + (g[j] * a.omb2) * g[j];
+      const float gj = g[j] * gs;
+      m[j] = m[j] * a.b1 + gj * a.omb1;
+      v[j] = moment2(v[j], gj);
+      low = fminf(low, v[j]);
+      root[j] = EIGHT ? __builtin_amdgcn_sqrtf(v[j]) : root_f32(v[j]);
+      if constexpr (EARLY) p[j] = updated(p[j], m[j], root[j]);
     }
     if constexpr (EIGHT) {
-      float low = v[0];
+      if (low < 0x1p-120f) {
+        // Seldom, so a branch; what it needs is read again, which costs the rest
+        // less than keeping registers for it.
+        float r[8], h[8], old[8];
+        int64_t at = i;
+        asm volatile("" : "+v"(at));                         // (opaque, or the values above are kept)
+        load8<GRAD_BF16, FULL, EIGHT>(t.g, at, n, h);
+        decode8(load8_codes<FULL>(static_cast<const uint8_t*>(t.v), at, n), e8m0(t.vs[at >> 7]), r);
+        if constexpr (EARLY) load_p(at, old);
 #pragma unroll
-      for (int j = 1; j < 8; ++j) low = fminf(low, v[j]);
-      float r[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        r[j] = root[j];
-        root[j] = __builtin_amdgcn_sqrtf(v[j]);
+        for (int j = 0; j < 8; ++j) {
+          const float hj = h[j] * gs;
+          if (moment2(r[j] * r[j], hj) < 0x1p-120f) {
+            root[j] = small_root(r[j], hj, a.root_b2, a.root_omb2);
+            if constexpr (EARLY) p[j] = updated(old[j], m[j], root[j]);
+          }
+        }
       }
-      if (low < 0x1p-120f) {                                // seldom: a branch costs less than the work
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (v[j] < 0x1p-120f) root[j] = small_root(r[j], g[j], a.root_b2, a.root_omb2);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) root[j] = root_f32(v[j]);
     }
+    if constexpr (!EARLY) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)                             // (the reciprocal's argument is at least eps, a normal number)
-      p[j] = p[j] * decay - step_size * (m[j] * __builtin_amdgcn_rcpf(root[j] * rbc2 + a.eps));
+      for (int j = 0; j < 8; ++j) p[j] = updated(p[j], m[j], root[j]);
+    }
     uint32_t one[8], two[8];
     if constexpr (EIGHT || PARAM == PARAM_BF16) {
       const uint32_t key = key0 ^ (static_cast<uint32_t>(i >> 32) * 0x9e3779b9u);
@@ -339,15 +356,13 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
       }
     }
     if constexpr (EIGHT) {
-      // maxima of bit patterns: infinities and NaN are above every number
-      uint32_t bm = 0, bv = 0;
+      float tm = 0.f, tv = 0.f;                             // (fmaxf passes over NaN)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        bm = max(bm, __float_as_uint(m[j]) & 0x7fffffffu);
-        bv = max(bv, __float_as_uint(root[j]) & 0x7fffffffu);
+        tm = fmaxf(tm, fabsf(m[j]));
+        tv = fmaxf(tv, root[j]);
       }
-      float tm = __uint_as_float(bm), tv = __uint_as_float(bv);
-      if (max(bm, bv) >= 0x7f800000u) {
+      if (fmaxf(tm, tv) == INFINITY) {
         tm = tv = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -367,9 +382,9 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         ym[j] = m[j] * im;
-        // a nonzero value below the smallest code (2^-9) becomes that code; NaN stays
-        yv[j] = root[j] * iv;
-        if (root[j] > 0.f && yv[j] < 0.001953125f) yv[j] = 0.001953125f;
+        // a nonzero value below the smallest code (2^-9) becomes that code; NaN, whose
+        // bits are above every number's, stays
+        yv[j] = root[j] == 0.f ? 0.f : __uint_as_float(max(__float_as_uint(root[j] * iv), 0x3b000000u));
       }
       store8_codes<FULL>(static_cast<uint8_t*>(t.m), i, n, encode8(ym, one));
       store8_codes<FULL>(static_cast<uint8_t*>(t.v), i, n, encode8(yv, two));
