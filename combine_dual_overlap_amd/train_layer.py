@@ -33,9 +33,15 @@ class TrainLayer:
     one layer on several streams need the caller's ordering.
 
     forward(), backward() and step() can be captured, each by itself or together;
-    a replay is a call, in order with the others, and uses the same buffers.  From
-    the first capture on every backward() adds, and step() no longer checks that a
-    backward() came before it: the host does not see replays.
+    a replay is a call, in order with the others, on the same buffers and with the
+    number of tokens and the x and dout it was captured with.  The host does not
+    see replays: from the first capture on every backward() adds, step() no longer
+    checks that a backward() came before it, and an eager backward() takes the
+    tokens of the last forward() that was not a replay.
+
+    With a share of the experts (cfg.expert_begin, expert_end) out, dx and the
+    router's gradient are this share's part, to be summed over the shares; give the
+    shared experts to one share only, or their part is counted more than once.
     """
 
     def __init__(self, inp: dict, device: str = "cuda", T_max: int = None, grad_dtype=torch.float32,
