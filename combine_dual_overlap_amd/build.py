@@ -7,6 +7,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -14,8 +16,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdbomoe.so")
 SOURCES = ["route.hip", "dispatch.hip", "ffn.hip", "combine.hip", "layer.hip", "grouped_gemm.hip", "backward.hip",
-           "adamw.hip"]
+           "adamw.hip", "balance.hip", "int8.hip", "norms.hip"]
 ARCH = "gfx950"
+JOBS = min(8, int(os.environ.get("MAX_JOBS", os.cpu_count() or 1)))
 
 
 def hipcc() -> str:
@@ -26,21 +29,26 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source and link the shared library; returns its path."""
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
-           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-           "-Wall", "-Wno-unused-function", "-Wno-unused-variable",
-           f"-I{INCLUDE}", f"-I{CSRC}", "-o", LIB + ".tmp"]
-    cmd += [os.path.join(CSRC, s) for s in SOURCES]
+    """Compile every source, several at a time, and link the shared library; returns its path."""
+    cc = [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
+          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+          "-Wall", "-Wno-unused-function", "-Wno-unused-variable", f"-I{INCLUDE}", f"-I{CSRC}"]
+
+    def run(cmd) -> str:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        out = "\n".join(l for l in (r.stdout + r.stderr).splitlines() if "packed-fp32-ops" not in l)
+        if r.returncode != 0:
+            raise RuntimeError(f"hipcc failed ({r.returncode}):\n{' '.join(cmd)}\n{out}")
+        return out
+
     if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    out = "\n".join(l for l in (r.stdout + r.stderr).splitlines()
-                    if "packed-fp32-ops" not in l)
-    if r.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({r.returncode}):\n{out}")
-    if verbose and out.strip():
-        print(out)
+        print(" ".join(cc), flush=True)
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(JOBS) as pool:
+        objects = [os.path.join(tmp, s + ".o") for s in SOURCES]
+        outs = list(pool.map(lambda s, o: run(cc + ["-c", os.path.join(CSRC, s), "-o", o]), SOURCES, objects))
+        outs.append(run([cc[0], f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", LIB + ".tmp"] + objects))
+    if verbose:
+        print("\n".join(o for o in outs if o.strip()), flush=True)
     os.replace(LIB + ".tmp", LIB)
     return LIB
 
