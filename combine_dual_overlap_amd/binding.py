@@ -17,10 +17,11 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdbomoe.s
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_MISALIGNED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = \
     0, -1, -2, -3, -4, -5
-MOE_F32, MOE_BF16, MOE_FP8_E4M3FN = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_FP8_E4M3FN, MOE_INT8 = 0, 1, 2, 3
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 DBO_SCHED_UNSPLIT, DBO_SCHED_SERIAL, DBO_SCHED_DBO, DBO_SCHED_DBO_LATE_EVENT, DBO_SCHED_DBO_RECV_HOOK = 0, 1, 2, 3, 4
 MOE_GEMM_NT, MOE_GEMM_NN, MOE_GEMM_TN = 0, 1, 2
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = 0, 1, 2, 3
 GEMM_KINDS = {"nt": MOE_GEMM_NT, "nn": MOE_GEMM_NN, "tn": MOE_GEMM_TN}
 SCHEDULES = {"unsplit": 0, "serial": 1, "dbo": 2, "dbo_late_event": 3, "dbo_recv_hook": 4}
 
@@ -35,6 +36,10 @@ EXPORTED = [
     "moe_grouped_gemm_workspace_size", "moe_grouped_gemm", "moe_grouped_swiglu", "moe_grouped_swiglu_backward",
     "moe_combine_backward", "moe_route_backward", "moe_adamw_table_size", "moe_adamw_table_build",
     "moe_adamw_table_check", "moe_adamw_step",
+    "moe_route_select", "moe_route_balanced", "moe_route_bias_update", "moe_route_balance_loss_workspace_size",
+    "moe_route_balance_loss", "moe_quant_int8_rows", "moe_dispatch_int8", "moe_grouped_gemm_int8",
+    "moe_grouped_swiglu_int8", "moe_ffn_int8_workspace_size", "moe_grouped_ffn_int8", "moe_pre_norm", "moe_post_norm",
+    "moe_combine_post_norm", "moe_norm_backward_workspace_size", "moe_pre_norm_backward", "moe_post_norm_backward",
 ]
 
 
@@ -73,6 +78,11 @@ class moe_adamw_params(ctypes.Structure):
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("seed", ctypes.c_uint32)]
 
 
+class moe_post_norm_params(ctypes.Structure):
+    _fields_ = [("post_w", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("gate_kind", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("next_w", ctypes.c_void_p)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -80,7 +90,7 @@ class MoEError(RuntimeError):
 
 
 _LIB = None
-_vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 
 
 def lib():
@@ -139,6 +149,31 @@ def lib():
             "moe_adamw_table_build": (_i32, [ctypes.POINTER(moe_adamw_tensor), _i32, _vp, _sz]),
             "moe_adamw_table_check": (_i32, [_vp]),
             "moe_adamw_step": (_i32, [_vp, _vp, ctypes.POINTER(moe_adamw_params), _vp, _vp, _vp, _vp]),
+            "moe_route_select": (_i32, [_vp, _i64, _vp, ctypes.POINTER(moe_route_params), _vp, _vp, _vp, _vp]),
+            "moe_route_balanced": (_i32, [_vp, _i32, _i64, _i32, _vp, _vp, _vp, ctypes.POINTER(moe_route_params),
+                                          _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+            "moe_route_bias_update": (_i32, [_vp, _vp, _i32, _f32, _vp]),
+            "moe_route_balance_loss_workspace_size": (_sz, [_i64, _i32]),
+            "moe_route_balance_loss": (_i32, [_vp, _i64, _vp, ctypes.POINTER(moe_route_params), _f32, _vp, _vp, _i32,
+                                              _i32, _vp, _sz, _vp]),
+            "moe_quant_int8_rows": (_i32, [_vp, _i32, _i64, _i32, _vp, _vp, _vp]),
+            "moe_dispatch_int8": (_i32, [_vp, _i32, _i64, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
+                                         _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+            "moe_grouped_gemm_int8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _i32, _vp]),
+            "moe_grouped_swiglu_int8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _i32, _vp]),
+            "moe_ffn_int8_workspace_size": (_sz, [_i64, _i32]),
+            "moe_grouped_ffn_int8": (_i32, [_vp, _vp, _i32, _i32, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                            _vp]),
+            "moe_pre_norm": (_i32, [_vp, _i32, _i64, _i32, _vp, _f32, _vp, _vp, _vp]),
+            "moe_post_norm": (_i32, [_vp, _i32, _i64, _i32, _vp, ctypes.POINTER(moe_post_norm_params), _vp, _vp, _vp,
+                                     _vp, _vp]),
+            "moe_combine_post_norm": (_i32, [_vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp, _vp,
+                                             ctypes.POINTER(moe_post_norm_params), _vp, _vp, _vp, _vp, _vp, _vp]),
+            "moe_norm_backward_workspace_size": (_sz, [_i64, _i32]),
+            "moe_pre_norm_backward": (_i32, [_vp, _vp, _i32, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _sz,
+                                             _vp]),
+            "moe_post_norm_backward": (_i32, [_vp, _vp, _i32, _i64, _i32, _vp, ctypes.POINTER(moe_post_norm_params),
+                                              _vp, _vp, _vp, _i32, _vp, _sz, _vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -174,6 +209,8 @@ def dtype_code(t: torch.Tensor) -> int:
         return MOE_BF16
     if t.dtype in (torch.uint8, torch.float8_e4m3fn):
         return MOE_FP8_E4M3FN
+    if t.dtype == torch.int8:
+        return MOE_INT8
     raise ValueError(f"unsupported dtype {t.dtype}")
 
 
@@ -540,6 +577,296 @@ def moe_adamw_step(table: AdamWTable, hp: moe_adamw_params, step, lr_scale=None,
             raise ValueError("lr_scale, grad_scale: one float32")
     d = table.device
     _call("moe_adamw_step", d, stream, table.host_ptr, table.device_ptr, hp, *_ptrs(d, step, lr_scale, grad_scale))
+
+
+# ------------------------------------------------------------------ balanced routing
+# (with the checks, devices and streams of the training calls)
+
+def _nbytes(ws) -> int:
+    return 0 if ws is None else ws.nbytes
+
+
+def _typed(t, dtype, shape, what: str):
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{what}: {dtype} {list(shape)}")
+
+
+def _check_select(E, T, params, topk_ids, topk_w, select_bias, load):
+    if E != params.E:
+        raise ValueError("logits of params.E experts")
+    _typed(topk_ids, torch.int32, (T, params.k), "topk_ids")
+    _typed(topk_w, torch.float32, (T, params.k), "topk_w")
+    if select_bias is not None:
+        _typed(select_bias, torch.float32, (E,), "select_bias")
+    if load is not None:
+        _typed(load, torch.int32, (E,), "load")
+
+
+def moe_route_select(logits, params: moe_route_params, topk_ids, topk_w, select_bias=None, load=None, stream=None):
+    """topk_ids and topk_w [T, k] of logits [T, E] float32: chosen by score + select_bias [E], weighted by the score.
+    load [E] int32 (optional): the number of tokens of each expert is added."""
+    T, E = logits.shape
+    _typed(logits, torch.float32, (T, E), "logits")
+    _check_select(E, T, params, topk_ids, topk_w, select_bias, load)
+    d = _device(logits)
+    pl, pb, pi, pw, po = _ptrs(d, logits, select_bias, topk_ids, topk_w, load)
+    _call("moe_route_select", d, stream, pl, T, pb, params, pi, pw, po)
+
+
+def moe_route_balanced(x, w_router, params: moe_route_params, topk_ids, topk_w, ws, select_bias=None, load=None,
+                       logits_out=None, logit_bias=None, stream=None):
+    """moe_route_topk with moe_route_select's selection: x [T, H], w_router [E, H]."""
+    T, H = x.shape
+    E = w_router.numel() // H
+    if w_router.dtype != x.dtype or w_router.shape[-2:] != (E, H):
+        raise ValueError("w_router: [E, H] of x's type")
+    _check_select(E, T, params, topk_ids, topk_w, select_bias, load)
+    if logits_out is not None:
+        _typed(logits_out, torch.float32, (T, E), "logits_out")
+    if logit_bias is not None:
+        _typed(logit_bias, torch.float32, (E,), "logit_bias")
+    d = _device(x)
+    px, pr, pl, pb, pg, pi, pw, po, ps = _ptrs(d, x, w_router, logit_bias, select_bias, logits_out, topk_ids, topk_w,
+                                               load, ws)
+    _call("moe_route_balanced", d, stream, px, _code(x.dtype), T, H, pr, pl, pb, params, pg, pi, pw, po, ps, _nbytes(ws))
+
+
+def moe_route_bias_update(bias, load, rate: float, stream=None):
+    """bias [E] float32 += rate * sign(mean load - load); load [E] int32 becomes zero."""
+    E = bias.numel()
+    _typed(bias, torch.float32, (E,), "bias")
+    _typed(load, torch.int32, (E,), "load")
+    d = _device(bias)
+    pb, pl = _ptrs(d, bias, load)
+    _call("moe_route_bias_update", d, stream, pb, pl, E, rate)
+
+
+def moe_route_balance_loss_workspace_size(T: int, E: int) -> int:
+    return lib().moe_route_balance_loss_workspace_size(T, E)
+
+
+def moe_route_balance_loss(logits, load, params: moe_route_params, coef: float, loss, dlogits, ws, accumulate=False,
+                           stream=None):
+    """loss [1] = coef * E * sum_e (load_e / sum load) mean_t q_te and its gradient dlogits [T, E] (accumulate: added)."""
+    T, E = logits.shape
+    _typed(logits, torch.float32, (T, E), "logits")
+    _typed(load, torch.int32, (E,), "load")
+    if E != params.E or loss.dtype != torch.float32 or loss.numel() != 1 or dlogits.shape != (T, E):
+        raise ValueError("logits and dlogits [T, params.E], loss one float32")
+    d = _device(logits)
+    pl, pn, po, pd, pw = _ptrs(d, logits, load, loss, dlogits, ws)
+    _call("moe_route_balance_loss", d, stream, pl, T, pn, params, coef, po, pd, _code(dlogits.dtype),
+          1 if accumulate else 0, pw, _nbytes(ws))
+
+
+# ------------------------------------------------------------------ 8-bit integers
+
+def moe_quant_int8_rows(x, q, scale, stream=None):
+    """x [..., K] float32 or bfloat16 -> q int8 of its shape and scale [...] float32: x = q * scale of its row."""
+    K, n = x.shape[-1], scale.numel()
+    _typed(q, torch.int8, x.shape, "q")
+    _typed(scale, torch.float32, x.shape[:-1], "scale")
+    d = _device(x)
+    px, pq, ps = _ptrs(d, x, q, scale)
+    _call("moe_quant_int8_rows", d, stream, px, _code(x.dtype), n, K, pq, ps)
+
+
+def moe_dispatch_int8(x, topk_ids, E_total, expert_begin, expert_end, counts, offsets, perm, inv, xq_perm, xq_scale, ws,
+                      tile_m=0, tile_offsets=None, stream=None):
+    """moe_dispatch whose rows arrive as 8-bit integers xq_perm [T*k, H] with scales xq_scale [T*k]."""
+    T, H = x.shape
+    k = topk_ids.shape[1]
+    E_loc = expert_end - expert_begin
+    i32 = torch.int32
+    _typed(topk_ids, i32, (T, k), "topk_ids")
+    for t, n, what in ((counts, E_loc, "counts"), (offsets, E_loc + 1, "offsets"), (perm, T * k, "perm"), (inv, T * k, "inv")):
+        if t.dtype != i32 or t.numel() < n:
+            raise ValueError(f"{what}: int32 [{n}]")
+    if tile_offsets is not None and (tile_offsets.dtype != i32 or tile_offsets.numel() < E_loc + 1):
+        raise ValueError(f"tile_offsets: int32 [{E_loc + 1}]")
+    if xq_perm.dtype != torch.int8 or xq_perm.numel() < T * k * H or xq_scale.dtype != torch.float32 or xq_scale.numel() < T * k:
+        raise ValueError(f"xq_perm int8 [{T * k}, {H}], xq_scale float32 [{T * k}]")
+    d = _device(x)
+    px, pi, pc, po, pt, pp, pv, pq, ps, pw = _ptrs(d, x, topk_ids, counts, offsets, tile_offsets, perm, inv, xq_perm,
+                                                   xq_scale, ws)
+    _call("moe_dispatch_int8", d, stream, px, _code(x.dtype), T, H, pi, k, E_total, expert_begin, expert_end, tile_m,
+          pc, po, pt, pp, pv, pq, ps, pw, _nbytes(ws))
+
+
+def moe_grouped_gemm_int8(a, a_scale, b, b_scale, offsets, c, stream=None):
+    """c [rows, N] = (a [rows, K] b[e]^T) * a_scale [rows] * b_scale[e], b int8 [E, N, K]; offsets None: one group."""
+    (rows, K), (E, N, _) = a.shape, b.shape
+    _typed(b, torch.int8, (E, N, K), "b")
+    _typed(a, torch.int8, (rows, K), "a")
+    _typed(a_scale, torch.float32, (rows,), "a_scale")
+    _typed(b_scale, torch.float32, (E, N), "b_scale")
+    if c.shape != (rows, N):
+        raise ValueError(f"c: [{rows}, {N}]")
+    d = _device(a)
+    pa, ps, pb, pt, po, pc = _ptrs(d, a, a_scale, b, b_scale, offsets, c)
+    _call("moe_grouped_gemm_int8", d, stream, pa, ps, pb, pt, po, _groups(offsets, E), rows, N, K, pc, _code(c.dtype))
+
+
+def moe_grouped_swiglu_int8(xq, xq_scale, w13, w13_scale, offsets, h, stream=None):
+    """h [rows, I] = silu(g) * u of the products of xq [rows, H] with w13 int8 [E, 2I, H] and their scales."""
+    (rows, H), I, E = xq.shape, h.shape[1], w13.shape[0]
+    _typed(xq, torch.int8, (rows, H), "xq")
+    _typed(xq_scale, torch.float32, (rows,), "xq_scale")
+    _typed(w13, torch.int8, (E, 2 * I, H), "w13")
+    _typed(w13_scale, torch.float32, (E, 2 * I), "w13_scale")
+    if h.shape != (rows, I):
+        raise ValueError(f"h: [{rows}, {I}]")
+    d = _device(xq)
+    px, ps, pw, pt, po, ph = _ptrs(d, xq, xq_scale, w13, w13_scale, offsets, h)
+    _call("moe_grouped_swiglu_int8", d, stream, px, ps, pw, pt, po, _groups(offsets, E), rows, H, I, ph, _code(h.dtype))
+
+
+def moe_ffn_int8_workspace_size(cap_rows: int, I: int) -> int:
+    return lib().moe_ffn_int8_workspace_size(cap_rows, I)
+
+
+def moe_grouped_ffn_int8(xq, xq_scale, offsets, w13, w13_scale, w2, w2_scale, y, ws, stream=None):
+    """y [rows, H] bfloat16: SwiGLU experts in 8-bit integers; w13 [E, 2I, H], w2 [E, H, I] int8 with a scale per row."""
+    (rows, H), (E, _, I) = xq.shape, w2.shape
+    _typed(xq, torch.int8, (rows, H), "xq")
+    _typed(xq_scale, torch.float32, (rows,), "xq_scale")
+    _typed(w13, torch.int8, (E, 2 * I, H), "w13")
+    _typed(w13_scale, torch.float32, (E, 2 * I), "w13_scale")
+    _typed(w2, torch.int8, (E, H, I), "w2")
+    _typed(w2_scale, torch.float32, (E, H), "w2_scale")
+    _typed(y, torch.bfloat16, (rows, H), "y")
+    d = _device(xq)
+    px, ps, po, pa, pb, p2, p3, py, pw = _ptrs(d, xq, xq_scale, offsets, w13, w13_scale, w2, w2_scale, y, ws)
+    _call("moe_grouped_ffn_int8", d, stream, px, ps, H, I, po, _groups(offsets, E), rows, pa, p2, pb, p3, py, pw,
+          _nbytes(ws))
+
+
+# ------------------------------------------------------------------ norms before and after the layer
+
+def _rows_typed(t, like, what: str):
+    if t is not None and (t.dtype != like.dtype or t.shape != like.shape):
+        raise ValueError(f"{what}: {like.dtype} {list(like.shape)}")
+
+
+def _channel(t, like, what: str):
+    if t is not None:
+        _typed(t, like.dtype, like.shape[1:], what)
+
+
+def _token(t, T: int, what: str):
+    if t is not None:
+        _typed(t, torch.float32, (T,), what)
+
+
+def _gate_kind(gate, like) -> int:
+    """By shape: [H] and [T, H] of the rows' type, or [T, 1] float32."""
+    if gate is None:
+        return MOE_GATE_NONE
+    T, H = like.shape
+    if gate.dtype == like.dtype and gate.shape == (H,):
+        return MOE_GATE_CHANNEL
+    if gate.dtype == torch.float32 and gate.shape == (T, 1) and H != 1:
+        return MOE_GATE_TOKEN
+    if gate.dtype == like.dtype and gate.shape == (T, H):
+        return MOE_GATE_FULL
+    raise ValueError(f"gate: {like.dtype} [{H}] or [{T}, {H}], or float32 [{T}, 1]")
+
+
+def moe_pre_norm(x, w, n, eps: float, rstd=None, stream=None):
+    """n [T, H] = x / rms(x) * w; rstd [T] float32 (optional): 1 / rms, for the backward pass.  n may be x."""
+    T, H = x.shape
+    _rows_typed(n, x, "n")
+    _channel(w, x, "w")
+    _token(rstd, T, "rstd")
+    d = _device(x)
+    px, pw, pn, pr = _ptrs(d, x, w, n, rstd)
+    _call("moe_pre_norm", d, stream, px, _code(x.dtype), T, H, pw, eps, pn, pr)
+
+
+def _post_params(d, like, eps, post_w, gate, scale, next_w, next_n, rstd, next_rstd) -> moe_post_norm_params:
+    T = like.shape[0]
+    _channel(post_w, like, "post_w")
+    _channel(next_w, like, "next_w")
+    _rows_typed(next_n, like, "next_n")
+    _token(rstd, T, "rstd")
+    _token(next_rstd, T, "next_rstd")
+    kind = _gate_kind(gate, like)
+    pw, pg, pn = _ptrs(d, post_w, gate, next_w)
+    return moe_post_norm_params(pw, pg, kind, scale, eps, pn)
+
+
+def moe_post_norm(y, res, out, eps: float, post_w=None, gate=None, scale: float = 1.0, rstd=None, next_w=None,
+                  next_n=None, next_rstd=None, stream=None):
+    """out [T, H] = res + scale * gate * (y / rms(y) * post_w), and next_n = out / rms(out) * next_w.
+
+    res None: no residual; post_w None: no norm; gate [H] or [T, H] of y's type, or float32 [T, 1].  out may be res."""
+    T, H = y.shape
+    _rows_typed(res, y, "res")
+    _rows_typed(out, y, "out")
+    d = _device(y)
+    q = _post_params(d, y, eps, post_w, gate, scale, next_w, next_n, rstd, next_rstd)
+    py, pe, po, pr, pn, ps = _ptrs(d, y, res, out, rstd, next_n, next_rstd)
+    _call("moe_post_norm", d, stream, py, _code(y.dtype), T, H, pe, q, po, pr, pn, ps)
+
+
+def moe_combine_post_norm(y_perm, inv, topk_w, res, out, eps: float, post_w=None, gate=None, scale: float = 1.0,
+                          shared_out=None, y_out=None, rstd=None, next_w=None, next_n=None, next_rstd=None, stream=None):
+    """moe_post_norm of moe_combine's sum of y_perm, inv [T*k], topk_w [T, k] (+ shared_out [T, H]); y_out: that sum."""
+    T, H = out.shape
+    k = topk_w.shape[1]
+    if y_perm.dtype != out.dtype or y_perm.dim() != 2 or y_perm.shape[1] != H:
+        raise ValueError(f"y_perm: {out.dtype} [rows, {H}]")
+    if topk_w.dtype != torch.float32 or topk_w.shape != (T, k) or inv.dtype != torch.int32 or inv.numel() != T * k:
+        raise ValueError("topk_w float32 [T, k], inv int32 [T * k]")
+    for t, what in ((res, "res"), (shared_out, "shared_out"), (y_out, "y_out")):
+        _rows_typed(t, out, what)
+    d = _device(out)
+    q = _post_params(d, out, eps, post_w, gate, scale, next_w, next_n, rstd, next_rstd)
+    pp, pi, pk, ph, pe, po, py, pr, pn, ps = _ptrs(d, y_perm, inv, topk_w, shared_out, res, out, y_out, rstd, next_n,
+                                                   next_rstd)
+    _call("moe_combine_post_norm", d, stream, pp, _code(out.dtype), T, H, k, pi, pk, ph, pe, q, po, py, pr, pn, ps)
+
+
+def moe_norm_backward_workspace_size(T: int, H: int) -> int:
+    return lib().moe_norm_backward_workspace_size(T, H)
+
+
+def moe_pre_norm_backward(dn, x, rstd, w, dx, dw, ws, dres=None, accumulate=False, stream=None):
+    """dx [T, H] = dres + the gradient of moe_pre_norm's x; dw [H] float32 (or None).  dx may be dn or dres."""
+    T, H = x.shape
+    for t, what in ((dn, "dn"), (dx, "dx"), (dres, "dres")):
+        _rows_typed(t, x, what)
+    _channel(w, x, "w")
+    _token(rstd, T, "rstd")
+    if dw is not None:
+        _typed(dw, torch.float32, (H,), "dw")
+    d = _device(x)
+    pd, px, pr, pw, pe, po, pg, ps = _ptrs(d, dn, x, rstd, w, dres, dx, dw, ws)
+    _call("moe_pre_norm_backward", d, stream, pd, px, _code(x.dtype), T, H, pr, pw, pe, po, pg, 1 if accumulate else 0,
+          ps, _nbytes(ws))
+
+
+def moe_post_norm_backward(dout, y, dy, ws, rstd=None, post_w=None, dpost_w=None, gate=None, dgate=None,
+                           scale: float = 1.0, accumulate=False, stream=None):
+    """Gradients of moe_post_norm's out: dy [T, H], dpost_w [H] float32 (or None), dgate (or None): float32 [H] or
+    [T, 1], or [T, H] of y's type, as the gate.  The residual's gradient is dout."""
+    T, H = y.shape
+    _rows_typed(dout, y, "dout")
+    _rows_typed(dy, y, "dy")
+    _channel(post_w, y, "post_w")
+    _token(rstd, T, "rstd")
+    kind = _gate_kind(gate, y)
+    if dpost_w is not None:
+        _typed(dpost_w, torch.float32, (H,), "dpost_w")
+    if dgate is not None:
+        if gate is None:
+            raise ValueError("dgate goes with gate")
+        _typed(dgate, y.dtype if kind == MOE_GATE_FULL else torch.float32, gate.shape, "dgate")
+    d = _device(y)
+    pd, py, po, ps, pr, pw, pc, pg, pt = _ptrs(d, dout, y, dy, ws, rstd, post_w, dpost_w, gate, dgate)
+    q = moe_post_norm_params(pw, pg, kind, scale, 1.0, None)
+    _call("moe_post_norm_backward", d, stream, pd, py, _code(y.dtype), T, H, pr, q, po, pc, pt, 1 if accumulate else 0,
+          ps, _nbytes(ws))
 
 
 class DboContext:

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <stddef.h>
+#include <algorithm>
 
 #include "dbomoe.h"
 
@@ -82,6 +83,7 @@ inline size_t dtype_size(moe_dtype d) {
     case MOE_F32: return 4;
     case MOE_BF16: return 2;
     case MOE_FP8_E4M3FN: return 1;
+    case MOE_INT8: return 1;
   }
   return 0;
 }
@@ -104,6 +106,10 @@ struct RouteArgs {
 int route_splits(int64_t T, int32_t H, int32_t E);
 size_t route_ws_bytes(int64_t T, int32_t H, int32_t E);
 moe_status launch_route(const RouteArgs& a, hipStream_t s);
+moe_status launch_route_logits(const RouteArgs& a, hipStream_t s);
+// moe_route_balanced: the selection sees select_bias, the weights do not; load
+// (or NULL) is added to.  a.forced is not used.
+moe_status launch_route_balanced(const RouteArgs& a, const float* select_bias, int32_t* load, hipStream_t s);
 
 struct DispatchArgs {
   const void* x; moe_dtype act; int64_t T; int32_t H;
@@ -113,6 +119,7 @@ struct DispatchArgs {
   uint8_t* x_scale;        // non-NULL: x_perm receives fp8 codes and x_scale the E8M0 bytes [rows][H/128]
   bool beside_ffn;         // issued to run beside an FFN launch on the other stream: kernels that fit
                            // into what the GEMM's resident workgroups leave free on a CU
+  float* x_scale_i8;       // non-NULL: x_perm receives 8-bit integers and x_scale_i8 their scales [rows]
 };
 size_t dispatch_ws_bytes(int64_t T, int32_t k, int32_t E_loc);
 moe_status launch_dispatch(const DispatchArgs& a, hipStream_t s);
@@ -153,6 +160,34 @@ struct CombineArgs {
   bool beside_ffn;         // as in DispatchArgs
 };
 moe_status launch_combine(const CombineArgs& a, hipStream_t s);
+
+// moe_post_norm on what launch_combine would have written (a.out receives out).
+moe_status check_post_norm(const moe_post_norm_params* p);
+moe_status launch_combine_post_norm(const CombineArgs& a, const void* res, const moe_post_norm_params& q, void* y_out,
+                                    float* rstd, void* next_n, float* next_rstd, hipStream_t s);
+moe_status launch_pre_norm(const void* x, moe_dtype act, int64_t T, int32_t H, const void* w, float eps, void* n,
+                           float* rstd, hipStream_t s);
+
+// Rows x [T, K] to 8-bit integers with a scale each: to row t, or to the rows
+// inv[t k + j] >= 0 of each.  offsets: only rows [offsets[0], offsets[E]) exist.
+struct QuantInt8Args {
+  const void* x; moe_dtype act; int64_t T; int32_t K;
+  int32_t k; const int32_t* inv;
+  const int32_t* offsets; int32_t E;
+  int8_t* q; float* scale; int32_t max_blocks;
+};
+moe_status launch_quant_int8(const QuantInt8Args& a, hipStream_t s);
+
+struct FfnInt8Args {
+  const int8_t* xq; const float* xs; int32_t H; int32_t I;
+  const int32_t* offsets; int32_t E_loc; int64_t cap_rows;
+  const int8_t* w13; const int8_t* w2; const float* s13; const float* s2;
+  void* y; void* ws;
+  hipEvent_t t0, t1, t2;   // as in FfnArgs
+};
+size_t ffn_int8_ws_bytes(int64_t cap_rows, int32_t I);
+moe_status check_ffn_int8_shapes(const int32_t* offsets, int32_t E_loc, int64_t cap, int32_t H, int32_t I);
+moe_status launch_ffn_int8(const FfnInt8Args& a, hipStream_t s);
 
 moe_status check_route_params(const moe_route_params* p);
 

@@ -859,6 +859,19 @@ __global__ __launch_bounds__(64 * TOK) void k_disp_rank_gather(
 }
 
 static moe_status launch_gather(const DispatchArgs& a, hipStream_t s) {
+  if (a.x_scale_i8) {
+    QuantInt8Args q{};
+    q.x = a.x;
+    q.act = a.act;
+    q.T = a.T;
+    q.K = a.H;
+    q.k = a.k;
+    q.inv = a.inv;
+    q.q = static_cast<int8_t*>(a.x_perm);
+    q.scale = a.x_scale_i8;
+    q.max_blocks = a.max_blocks;
+    return launch_quant_int8(q, s);
+  }
   int64_t blocks = (a.T + 3) / 4;
   if (a.max_blocks > 0 && blocks > a.max_blocks) blocks = a.max_blocks;
   const int row_chunks = static_cast<int>(static_cast<int64_t>(a.H) * dtype_size(a.act) / 16);
@@ -952,7 +965,7 @@ moe_status launch_dispatch(const DispatchArgs& a, hipStream_t s) {
   // Few pairs (decode): one kernel whose workgroups each count all the pairs
   // from the ids themselves.
   const bool small = n_pairs <= kSmallMaxPairs && E_loc <= kSmallMaxELoc;
-  const bool fused = !a.beside_ffn && a.T > 0 && E_loc <= kMidMaxELoc && a.k <= kFusedMaxK &&
+  const bool fused = !a.beside_ffn && !a.x_scale_i8 && a.T > 0 && E_loc <= kMidMaxELoc && a.k <= kFusedMaxK &&
                      (small || nb_mid * E_loc <= kFusedMaxHist) && (a.max_blocks <= 0 || groups <= a.max_blocks);
   if (!fused) {
     const moe_status st = launch_dispatch_send(a, s);
@@ -1161,6 +1174,32 @@ extern "C" moe_status moe_dispatch_fp8(const void* x, int64_t T, int32_t H, cons
   if (ws_bytes < dispatch_ws_bytes(T, k, E_loc)) return MOE_ERR_WORKSPACE;
   DispatchArgs a{x, MOE_BF16, T, H, topk_ids, k, E_total, expert_begin, expert_end, tile_m,
                  counts, offsets, tile_offsets, perm, inv, xq_perm, ws, 0, xq_scale};
+  return launch_dispatch(a, as_stream(stream));
+}
+
+extern "C" moe_status moe_dispatch_int8(const void* x, moe_dtype act, int64_t T, int32_t H, const int32_t* topk_ids,
+                                        int32_t k, int32_t E_total, int32_t expert_begin, int32_t expert_end,
+                                        int32_t tile_m, int32_t* counts, int32_t* offsets, int32_t* tile_offsets,
+                                        int32_t* perm, int32_t* inv, int8_t* xq_perm, float* xq_scale, void* ws,
+                                        size_t ws_bytes, void* stream) {
+  if (T < 0 || H <= 0 || k < 1 || k > 16 || E_total < 1) return MOE_ERR_INVALID_ARG;
+  if (expert_begin < 0 || expert_end <= expert_begin || expert_end > E_total) return MOE_ERR_INVALID_ARG;
+  const int E_loc = expert_end - expert_begin;
+  if (E_loc > kMaxELoc) return MOE_ERR_UNSUPPORTED;
+  if (act != MOE_F32 && act != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (tile_offsets && tile_m <= 0) return MOE_ERR_INVALID_ARG;
+  if (!counts || !offsets || !ws) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!x || !topk_ids || !perm || !inv || !xq_perm || !xq_scale)) return MOE_ERR_INVALID_ARG;
+  if (H % 16) return MOE_ERR_MISALIGNED;
+  if (!aligned16(x) || !aligned16(topk_ids) || !aligned16(counts) || !aligned16(offsets) ||
+      (tile_offsets && !aligned16(tile_offsets)) || !aligned16(perm) || !aligned16(inv) || !aligned16(xq_perm) ||
+      !aligned16(xq_scale) || !aligned256(ws))
+    return MOE_ERR_MISALIGNED;
+  if (T * k > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (ws_bytes < dispatch_ws_bytes(T, k, E_loc)) return MOE_ERR_WORKSPACE;
+  DispatchArgs a{x, act, T, H, topk_ids, k, E_total, expert_begin, expert_end, tile_m,
+                 counts, offsets, tile_offsets, perm, inv, xq_perm, ws, 0, nullptr};
+  a.x_scale_i8 = xq_scale;
   return launch_dispatch(a, as_stream(stream));
 }
 

@@ -1,0 +1,583 @@
+// Norms before and after the layer, with its gate, scale and residual, and their
+// gradients, for gfx950.
+//   r(v) = 1 / sqrt(mean(v^2) + eps)
+//   before   n   = x r(x) w
+//   after    out = res + scale * g * (y r(y) w_post)      and, in the same pass, the
+//            next layer's n = out r(out) w_next
+// y is a tensor, or the combine's weighted sum of expert rows, which then never
+// leaves the registers (unless the backward pass needs it).  Everything is fp32
+// between loading a row and the one rounding of each output; out's rounding is not
+// in what follows from it in the same pass.
+// HBM-bound: each row is read once into registers and written once.
+#include "rows.h"
+
+namespace dbomoe {
+
+struct NormOutParams {
+  const u32x4_t* y;            // [T] rows, or the dispatched rows (GATHER)
+  const int32_t* inv;          // GATHER: [T k]
+  const float* topk_w;         // GATHER: [T, k]
+  const u32x4_t* shared;       // GATHER: n_shared slabs of [T] rows, weight 1, or NULL
+  int k, n_shared;
+  int64_t T;
+  int rc;                      // 16-byte chunks of a row
+  float inv_h, eps, scale;
+  const u32x4_t* res;          // NULL: no residual
+  const u32x4_t* post_w;       // NULL: no norm
+  const void* gate;
+  int gate_kind;
+  const u32x4_t* next_w;       // NULL: no next norm
+  u32x4_t* out;
+  u32x4_t* y_out;              // GATHER: y rounded, or NULL
+  float* rstd;
+  u32x4_t* next_n;
+  float* next_rstd;
+};
+
+// The sum of a token's expert rows and shared rows, four rows' loads in flight.
+template <bool BF16, int W, int CH>
+__device__ __forceinline__ void gather_sum(const NormOutParams& p, int64_t t, int l,
+                                           float (&v)[CH][Chunk<BF16>::N]) {
+  constexpr int N = Chunk<BF16>::N, G = CH == 1 ? 8 : 4;
+  const int lane = threadIdx.x & 63;
+  const int my_pos = lane < p.k ? p.inv[t * p.k + lane] : -1;
+  const float my_w = lane < p.k ? p.topk_w[t * p.k + lane] : 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[i][e] = 0.f;
+  const int rows = p.k + p.n_shared;
+  for (int j0 = 0; j0 < rows; j0 += G) {
+    u32x4_t c[G][CH];
+    float w[G];
+    unsigned used = 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int j = j0 + g;
+      const int pos = __builtin_amdgcn_readfirstlane(__shfl(my_pos, j < p.k ? j : 0, kWave));
+      w[g] = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(__shfl(my_w, j < p.k ? j : 0, kWave))));
+      const u32x4_t* src = nullptr;
+      if (j < p.k) {
+        if (pos >= 0) src = p.y + static_cast<int64_t>(pos) * p.rc;
+      } else if (j < rows) {
+        src = p.shared + (static_cast<int64_t>(j - p.k) * p.T + t) * p.rc;
+        w[g] = 1.f;
+      }
+      if (src) {
+        used |= 1u << g;
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+          if (i * 64 * W + l < p.rc) c[g][i] = src[i * 64 * W + l];
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (!(used & (1u << g))) continue;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        if (i * 64 * W + l >= p.rc) continue;
+        float f[N];
+        Chunk<BF16>::unpack(c[g][i], f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[i][e] += w[g] * f[e];
+      }
+    }
+  }
+}
+
+template <bool BF16, int W, int CH, bool GATHER>
+__global__ __launch_bounds__(RowShape<W>::THREADS) void k_norm_out(NormOutParams p) {
+  constexpr int N = Chunk<BF16>::N;
+  using C = Chunk<BF16>;
+  __shared__ float s_one[W], s_two[W];
+  const int l = W == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * RowShape<W>::ROWS + (W == 1 ? threadIdx.x >> 6 : 0);
+  if (t >= p.T) return;                                     // (a whole row's waves)
+  auto at = [&](int i) { return i * 64 * W + l; };
+  float v[CH][N];
+  if constexpr (GATHER) {
+    gather_sum<BF16, W, CH>(p, t, l, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      C::unpack(at(i) < p.rc ? p.y[t * p.rc + at(i)] : u32x4_t{0, 0, 0, 0}, v[i]);
+  }
+  if constexpr (GATHER) {
+    if (p.y_out)
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (at(i) < p.rc) p.y_out[t * p.rc + at(i)] = C::pack(v[i]);
+  }
+  // what the outputs need besides y, asked for before the sum over the row
+  u32x4_t res[CH], pw[CH], gt[CH], nw[CH];
+  const u32x4_t* gate = static_cast<const u32x4_t*>(p.gate);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    if (at(i) >= p.rc) continue;
+    if (p.res) res[i] = p.res[t * p.rc + at(i)];
+    if (p.post_w) pw[i] = p.post_w[at(i)];
+    if (p.gate_kind == MOE_GATE_CHANNEL) gt[i] = gate[at(i)];
+    if (p.gate_kind == MOE_GATE_FULL) gt[i] = gate[t * p.rc + at(i)];
+    if (p.next_w) nw[i] = p.next_w[at(i)];
+  }
+  float a = p.scale;
+  if (p.gate_kind == MOE_GATE_TOKEN) a *= static_cast<const float*>(p.gate)[t];
+  if (p.post_w) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int e = 0; e < N; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+    const float r = 1.0f / sqrtf(row_sum<W>(ss, s_one) * p.inv_h + p.eps);
+    if (p.rstd && l == 0) p.rstd[t] = r;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (at(i) >= p.rc) continue;
+      float w[N];
+      C::unpack(pw[i], w);
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[i][e] = v[i][e] * r * w[e];
+    }
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    if (at(i) >= p.rc) continue;
+    if (p.gate_kind == MOE_GATE_CHANNEL || p.gate_kind == MOE_GATE_FULL) {
+      float g[N];
+      C::unpack(gt[i], g);
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[i][e] *= g[e];
+    }
+    float f[N];
+    if (p.res) {
+      C::unpack(res[i], f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) f[e] = 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      v[i][e] = fmaf(a, v[i][e], f[e]);
+      ss = fmaf(v[i][e], v[i][e], ss);
+    }
+    if (p.out) p.out[t * p.rc + at(i)] = C::pack(v[i]);
+  }
+  if (!p.next_w) return;
+  const float r = 1.0f / sqrtf(row_sum<W>(ss, s_two) * p.inv_h + p.eps);
+  if (p.next_rstd && l == 0) p.next_rstd[t] = r;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    if (at(i) >= p.rc) continue;
+    float w[N];
+    C::unpack(nw[i], w);
+#pragma unroll
+    for (int e = 0; e < N; ++e) w[e] *= v[i][e] * r;
+    p.next_n[t * p.rc + at(i)] = C::pack(w);
+  }
+}
+
+static moe_status launch_norm_out(const NormOutParams& p, bool bf16, bool gather, hipStream_t s) {
+  if (p.T == 0) return MOE_OK;
+  with_row_shape(p.T, p.rc, [&](auto w, auto ch) {
+    constexpr int W = decltype(w)::value, CH = decltype(ch)::value;
+    const dim3 grid(static_cast<unsigned>((p.T + RowShape<W>::ROWS - 1) / RowShape<W>::ROWS));
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(RowShape<W>::THREADS), 0, s, p); };
+    if (bf16)
+      gather ? go(k_norm_out<true, W, CH, true>) : go(k_norm_out<true, W, CH, false>);
+    else
+      gather ? go(k_norm_out<false, W, CH, true>) : go(k_norm_out<false, W, CH, false>);
+  });
+  DBOMOE_CHECK_LAUNCH();
+  return MOE_OK;
+}
+
+// ---- gradients --------------------------------------------------------------------
+// With yh = y r and the incoming gradient d (post: a = scale * dout, else a = d):
+//   q  = a g w                      the gradient of yh
+//   dy = r (q - yh mean(q yh)) + dres
+//   dw = sum_t a g yh,  dg = a yh w (summed over what the gate is shared by)
+// Without a norm w is 1, r is 1 and the mean is left out.  A gate per channel
+// leaves one column sum for both: S_h = sum_t a yh, dw = g S, dg = w S.
+// A workgroup walks rows gridDim.x apart with the column sums of its lanes in
+// registers, leaves one row of partial sums, and k_norm_cols adds these in order.
+struct NormBwdParams {
+  const u32x4_t* d;
+  const u32x4_t* y;
+  int64_t T;
+  int rc;
+  float inv_h, scale;
+  const float* rstd;           // NULL: no norm
+  const u32x4_t* w;            // NULL: no norm
+  const void* gate;
+  int gate_kind;
+  const u32x4_t* dres;         // or NULL
+  u32x4_t* dy;
+  void* dgate;                 // token: fp32 [T]; full: [T] rows; (channel: k_norm_cols)
+  float* part;                 // [gridDim.x][H] or NULL
+};
+
+template <bool BF16, int W, int CH>
+__global__ __launch_bounds__(RowShape<W>::THREADS) void k_norm_bwd(NormBwdParams p) {
+  constexpr int N = Chunk<BF16>::N, ROWS = RowShape<W>::ROWS;
+  using C = Chunk<BF16>;
+  __shared__ float s_one[W], s_two[W];
+  __shared__ float s_col[W == 1 ? 4 * 64 * N : 1];
+  const int l = W == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int sub = W == 1 ? threadIdx.x >> 6 : 0;
+  auto at = [&](int i) { return i * 64 * W + l; };
+  float w[CH][N], g[CH][N], col[CH][N];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const bool in = at(i) < p.rc;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      w[i][e] = g[i][e] = 1.f;
+      col[i][e] = 0.f;
+    }
+    if (in && p.w) C::unpack(p.w[at(i)], w[i]);
+    if (in && p.gate_kind == MOE_GATE_CHANNEL) C::unpack(static_cast<const u32x4_t*>(p.gate)[at(i)], g[i]);
+  }
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * ROWS + sub; t < p.T; t += static_cast<int64_t>(gridDim.x) * ROWS) {
+    u32x4_t dv[CH], yv[CH], rv[CH], gv[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (at(i) >= p.rc) {
+        dv[i] = yv[i] = u32x4_t{0, 0, 0, 0};
+        continue;
+      }
+      dv[i] = p.d[t * p.rc + at(i)];
+      yv[i] = p.y[t * p.rc + at(i)];
+      if (p.dres) rv[i] = p.dres[t * p.rc + at(i)];
+      if (p.gate_kind == MOE_GATE_FULL) gv[i] = static_cast<const u32x4_t*>(p.gate)[t * p.rc + at(i)];
+    }
+    const float r = p.rstd ? p.rstd[t] : 1.f;
+    const float gt = p.gate_kind == MOE_GATE_TOKEN ? static_cast<const float*>(p.gate)[t] : 1.f;
+    float q[CH][N], yh[CH][N], dot = 0.f, tok = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      C::unpack(dv[i], q[i]);
+      C::unpack(yv[i], yh[i]);
+      float gf[N];
+      if (p.gate_kind == MOE_GATE_FULL && at(i) < p.rc) {
+        C::unpack(gv[i], gf);
+        float dg[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) dg[e] = p.scale * q[i][e] * (yh[i][e] * r) * w[i][e];
+        if (p.dgate) static_cast<u32x4_t*>(p.dgate)[t * p.rc + at(i)] = C::pack(dg);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) gf[e] = g[i][e];
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float a = p.scale * q[i][e];
+        yh[i][e] *= r;
+        const float ay = a * yh[i][e];
+        // the column sums leave a channel's gate out
+        col[i][e] = fmaf(p.gate_kind == MOE_GATE_FULL ? gf[e] : gt, ay, col[i][e]);
+        tok = fmaf(ay, w[i][e], tok);
+        q[i][e] = a * gt * gf[e] * w[i][e];
+        dot = fmaf(q[i][e], yh[i][e], dot);
+      }
+    }
+    if (p.gate_kind == MOE_GATE_TOKEN) {
+      tok = row_sum<W>(tok, s_one);
+      if (p.dgate && l == 0) static_cast<float*>(p.dgate)[t] = tok;
+    }
+    float mean = 0.f;
+    if (p.rstd) mean = row_sum<W>(dot, s_two) * p.inv_h;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (at(i) >= p.rc) continue;
+      float f[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) f[e] = 0.f;
+      if (p.dres) C::unpack(rv[i], f);
+#pragma unroll
+      for (int e = 0; e < N; ++e) f[e] = fmaf(r, q[i][e] - yh[i][e] * mean, f[e]);
+      p.dy[t * p.rc + at(i)] = C::pack(f);
+    }
+    if constexpr (W > 1) __syncthreads();                   // the exchanges read by all before the next row's
+  }
+  if (!p.part) return;
+  float* mine = p.part + static_cast<int64_t>(blockIdx.x) * p.rc * N;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    if constexpr (W == 1) {                                 // the four rows' lanes hold the same columns
+#pragma unroll
+      for (int e = 0; e < N; ++e) s_col[(sub * 64 + l) * N + e] = col[i][e];
+      __syncthreads();
+      for (int x = threadIdx.x; x < 64 * N; x += 256) {
+        const int c = i * 64 * N + x;
+        if (c < p.rc * N) mine[c] = ((s_col[x] + s_col[64 * N + x]) + s_col[128 * N + x]) + s_col[192 * N + x];
+      }
+      __syncthreads();
+    } else if (at(i) < p.rc) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) mine[at(i) * N + e] = col[i][e];
+    }
+  }
+}
+
+// Column sums of the partial rows: S_h; dw = S g (g per channel, else 1), dgate = S w.
+// 32 columns by 16 parts of the rows in a workgroup.
+template <bool BF16>
+__global__ __launch_bounds__(512) void k_norm_cols(const float* __restrict__ part, int rows, int H,
+                                                   const void* __restrict__ w, const void* __restrict__ gate,
+                                                   float* __restrict__ dw, float* __restrict__ dgate, int accumulate) {
+  __shared__ float s[16][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, h = blockIdx.x * 32 + x;
+  float v = 0.f;
+  if (h < H)
+    for (int r = y; r < rows; r += 16) v += part[static_cast<int64_t>(r) * H + h];
+  s[y][x] = v;
+  __syncthreads();
+  if (y != 0 || h >= H) return;
+#pragma unroll
+  for (int i = 1; i < 16; ++i) v += s[i][x];
+  auto get = [&](const void* p) {
+    return p == nullptr ? 1.f : BF16 ? bf16_to_f32(static_cast<const bf16_t*>(p)[h]) : static_cast<const float*>(p)[h];
+  };
+  if (dw) dw[h] = (accumulate ? dw[h] : 0.f) + v * get(gate);
+  if (dgate) dgate[h] = (accumulate ? dgate[h] : 0.f) + v * get(w);
+}
+
+static int64_t norm_bwd_blocks(int64_t T) { return std::min<int64_t>((T + 3) / 4, 512); }
+
+static moe_status launch_norm_bwd(NormBwdParams& p, bool bf16, int32_t H, float* dw, float* dgate_cols, bool accumulate,
+                                  void* ws, hipStream_t s) {
+  const bool cols = dw || dgate_cols;
+  const int blocks = static_cast<int>(norm_bwd_blocks(p.T));
+  p.part = cols ? static_cast<float*>(ws) : nullptr;
+  if (p.T > 0) {
+    with_row_shape(p.T, p.rc, [&](auto w, auto ch) {
+      constexpr int W = decltype(w)::value, CH = decltype(ch)::value;
+      auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(blocks), dim3(RowShape<W>::THREADS), 0, s, p); };
+      bf16 ? go(k_norm_bwd<true, W, CH>) : go(k_norm_bwd<false, W, CH>);
+    });
+    DBOMOE_CHECK_LAUNCH();
+  }
+  if (cols && !(p.T == 0 && accumulate)) {
+    const void* gate = p.gate_kind == MOE_GATE_CHANNEL ? p.gate : nullptr;
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((H + 31) / 32)), dim3(512), 0, s, p.part,
+                         p.T > 0 ? blocks : 0, H, static_cast<const void*>(p.w), gate, dw, dgate_cols, accumulate ? 1 : 0);
+    };
+    bf16 ? go(k_norm_cols<true>) : go(k_norm_cols<false>);
+    DBOMOE_CHECK_LAUNCH();
+  }
+  return MOE_OK;
+}
+
+// ---- checks -----------------------------------------------------------------------
+
+static moe_status norm_check_sizes(moe_dtype act, int64_t T, int32_t H) {
+  if (T < 0 || H <= 0) return MOE_ERR_INVALID_ARG;
+  if (act != MOE_F32 && act != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  const int64_t bytes = static_cast<int64_t>(H) * dtype_size(act);
+  if (bytes % 16) return MOE_ERR_MISALIGNED;
+  if (bytes / 16 > kRowMaxChunks) return MOE_ERR_UNSUPPORTED;
+  if (T >= (int64_t{1} << 22)) return MOE_ERR_UNSUPPORTED;          // 1024 threads a row, 2^32 in a grid
+  return MOE_OK;
+}
+
+moe_status check_post_norm(const moe_post_norm_params* q) {
+  if (!q) return MOE_ERR_INVALID_ARG;
+  if (q->gate_kind < MOE_GATE_NONE || q->gate_kind > MOE_GATE_FULL) return MOE_ERR_INVALID_ARG;
+  if ((q->gate_kind == MOE_GATE_NONE) != (q->gate == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!(q->eps > 0.f) || !(q->eps <= 3.4e38f) || !(q->scale >= -3.4e38f && q->scale <= 3.4e38f)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(q->post_w) || !aligned16(q->gate) || !aligned16(q->next_w)) return MOE_ERR_MISALIGNED;
+  return MOE_OK;
+}
+
+static NormOutParams norm_out_params(const moe_post_norm_params& q, int64_t T, int32_t H, moe_dtype act) {
+  NormOutParams p{};
+  p.T = T;
+  p.rc = static_cast<int>(static_cast<int64_t>(H) * dtype_size(act) / 16);
+  p.inv_h = 1.0f / static_cast<float>(H);
+  p.eps = q.eps;
+  p.scale = q.scale;
+  p.post_w = static_cast<const u32x4_t*>(q.post_w);
+  p.gate = q.gate;
+  p.gate_kind = q.gate_kind;
+  p.next_w = static_cast<const u32x4_t*>(q.next_w);
+  return p;
+}
+
+moe_status launch_pre_norm(const void* x, moe_dtype act, int64_t T, int32_t H, const void* w, float eps, void* n,
+                           float* rstd, hipStream_t s) {
+  // n = x r(x) w: what follows the residual sum, with x as that sum
+  moe_post_norm_params q{};
+  q.eps = eps;
+  q.scale = 1.f;
+  q.next_w = w;
+  NormOutParams p = norm_out_params(q, T, H, act);
+  p.y = static_cast<const u32x4_t*>(x);
+  p.next_n = static_cast<u32x4_t*>(n);
+  p.next_rstd = rstd;
+  return launch_norm_out(p, act == MOE_BF16, false, s);
+}
+
+moe_status launch_combine_post_norm(const CombineArgs& a, const void* res, const moe_post_norm_params& q, void* y_out,
+                                    float* rstd, void* next_n, float* next_rstd, hipStream_t s) {
+  NormOutParams p = norm_out_params(q, a.T, a.H, a.act);
+  p.y = static_cast<const u32x4_t*>(a.y);
+  p.inv = a.inv;
+  p.topk_w = a.w;
+  p.shared = static_cast<const u32x4_t*>(a.shared);
+  p.k = a.k;
+  p.n_shared = a.shared ? std::max(a.n_shared, 1) : 0;
+  p.res = static_cast<const u32x4_t*>(res);
+  p.out = static_cast<u32x4_t*>(a.out);
+  p.y_out = static_cast<u32x4_t*>(y_out);
+  p.rstd = rstd;
+  p.next_n = static_cast<u32x4_t*>(next_n);
+  p.next_rstd = next_rstd;
+  return launch_norm_out(p, a.act == MOE_BF16, true, s);
+}
+
+}  // namespace dbomoe
+
+using namespace dbomoe;
+
+extern "C" moe_status moe_pre_norm(const void* x, moe_dtype act, int64_t T, int32_t H, const void* w, float eps, void* n,
+                                   float* rstd, void* stream) {
+  const moe_status st = norm_check_sizes(act, T, H);
+  if (st != MOE_OK) return st;
+  if (!(eps > 0.f) || !(eps <= 3.4e38f)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !w || !n || n == w) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(n) || !aligned16(rstd)) return MOE_ERR_MISALIGNED;
+  return launch_pre_norm(x, act, T, H, w, eps, n, rstd, as_stream(stream));
+}
+
+// What moe_post_norm and moe_combine_post_norm share.
+static moe_status post_norm_check(const void* y, moe_dtype act, int64_t T, int32_t H, const void* res,
+                                  const moe_post_norm_params* q, const void* out, const void* next_n, const float* rstd,
+                                  const float* next_rstd) {
+  moe_status st = norm_check_sizes(act, T, H);
+  if (st != MOE_OK) return st;
+  st = check_post_norm(q);
+  if (st != MOE_OK) return st;
+  if ((q->next_w == nullptr) != (next_n == nullptr)) return MOE_ERR_INVALID_ARG;
+  if ((rstd && !q->post_w) || (next_rstd && !q->next_w)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!y || !out) return MOE_ERR_INVALID_ARG;
+  if (out == y || out == q->gate || out == q->post_w || out == q->next_w || out == next_n) return MOE_ERR_INVALID_ARG;
+  if (next_n && (next_n == y || next_n == res || next_n == q->gate || next_n == q->post_w || next_n == q->next_w))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(y) || !aligned16(res) || !aligned16(out) || !aligned16(next_n) || !aligned16(rstd) ||
+      !aligned16(next_rstd))
+    return MOE_ERR_MISALIGNED;
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_post_norm(const void* y, moe_dtype act, int64_t T, int32_t H, const void* res,
+                                    const moe_post_norm_params* params, void* out, float* rstd, void* next_n,
+                                    float* next_rstd, void* stream) {
+  const moe_status st = post_norm_check(y, act, T, H, res, params, out, next_n, rstd, next_rstd);
+  if (st != MOE_OK || T == 0) return st;
+  NormOutParams p = norm_out_params(*params, T, H, act);
+  p.y = static_cast<const u32x4_t*>(y);
+  p.res = static_cast<const u32x4_t*>(res);
+  p.out = static_cast<u32x4_t*>(out);
+  p.rstd = rstd;
+  p.next_n = static_cast<u32x4_t*>(next_n);
+  p.next_rstd = next_rstd;
+  return launch_norm_out(p, act == MOE_BF16, false, as_stream(stream));
+}
+
+extern "C" moe_status moe_combine_post_norm(const void* y_perm, moe_dtype act, int64_t T, int32_t H, int32_t k,
+                                            const int32_t* inv, const float* topk_w, const void* shared_out,
+                                            const void* res, const moe_post_norm_params* params, void* out, void* y_out,
+                                            float* rstd, void* next_n, float* next_rstd, void* stream) {
+  if (k < 1 || k > 16) return MOE_ERR_INVALID_ARG;
+  const moe_status st = post_norm_check(y_perm, act, T, H, res, params, out, next_n, rstd, next_rstd);
+  if (st != MOE_OK || T == 0) return st;
+  if (!inv || !topk_w) return MOE_ERR_INVALID_ARG;
+  if (shared_out && (out == shared_out || next_n == shared_out)) return MOE_ERR_INVALID_ARG;
+  if (y_out && (y_out == y_perm || y_out == shared_out || y_out == res || y_out == out || y_out == next_n ||
+                y_out == params->gate || y_out == params->post_w || y_out == params->next_w))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(inv) || !aligned16(topk_w) || !aligned16(shared_out) || !aligned16(y_out)) return MOE_ERR_MISALIGNED;
+  CombineArgs a{y_perm, act, T, H, k, inv, topk_w, shared_out, out, 0, shared_out ? 1 : 0};
+  return launch_combine_post_norm(a, res, *params, y_out, rstd, next_n, next_rstd, as_stream(stream));
+}
+
+extern "C" size_t moe_norm_backward_workspace_size(int64_t T, int32_t H) {
+  if (T <= 0 || H <= 0) return 0;
+  return align_up(static_cast<size_t>(norm_bwd_blocks(T)) * H * sizeof(float), 256);
+}
+
+extern "C" moe_status moe_pre_norm_backward(const void* dn, const void* x, moe_dtype act, int64_t T, int32_t H,
+                                            const float* rstd, const void* w, const void* dres, void* dx, float* dw,
+                                            int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+  const moe_status st = norm_check_sizes(act, T, H);
+  if (st != MOE_OK) return st;
+  if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID_ARG;
+  if (!w) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!dn || !x || !rstd || !dx)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (dx == x || dx == w || static_cast<const void*>(rstd) == dx || static_cast<void*>(dw) == dx))
+    return MOE_ERR_INVALID_ARG;
+  if (dw && (dw == w || dw == rstd || dw == dn || dw == x || dw == dres || dw == ws)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dn) || !aligned16(x) || !aligned16(rstd) || !aligned16(w) || !aligned16(dres) || !aligned16(dx) ||
+      !aligned16(dw) || !aligned256(ws))
+    return MOE_ERR_MISALIGNED;
+  if (dw && T > 0 && !ws) return MOE_ERR_INVALID_ARG;
+  if (dw && ws_bytes < moe_norm_backward_workspace_size(T, H)) return MOE_ERR_WORKSPACE;
+  NormBwdParams p{};
+  p.d = static_cast<const u32x4_t*>(dn);
+  p.y = static_cast<const u32x4_t*>(x);
+  p.T = T;
+  p.rc = static_cast<int>(static_cast<int64_t>(H) * dtype_size(act) / 16);
+  p.inv_h = 1.0f / static_cast<float>(H);
+  p.scale = 1.f;
+  p.rstd = rstd;
+  p.w = static_cast<const u32x4_t*>(w);
+  p.dres = static_cast<const u32x4_t*>(dres);
+  p.dy = static_cast<u32x4_t*>(dx);
+  return launch_norm_bwd(p, act == MOE_BF16, H, dw, nullptr, accumulate != 0, ws, as_stream(stream));
+}
+
+extern "C" moe_status moe_post_norm_backward(const void* dout, const void* y, moe_dtype act, int64_t T, int32_t H,
+                                             const float* rstd, const moe_post_norm_params* params, void* dy,
+                                             float* dpost_w, void* dgate, int32_t accumulate, void* ws, size_t ws_bytes,
+                                             void* stream) {
+  moe_status st = norm_check_sizes(act, T, H);
+  if (st != MOE_OK) return st;
+  st = check_post_norm(params);
+  if (st != MOE_OK) return st;
+  if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID_ARG;
+  if ((dpost_w && !params->post_w) || (dgate && !params->gate)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!dout || !y || !dy || (params->post_w == nullptr) != (rstd == nullptr))) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (dy == y || dy == params->post_w || dy == params->gate || static_cast<const void*>(rstd) == dy ||
+                static_cast<void*>(dpost_w) == dy || dgate == dy))
+    return MOE_ERR_INVALID_ARG;
+  for (void* o : {static_cast<void*>(dpost_w), dgate})
+    if (o && (o == params->post_w || o == params->gate || o == rstd || o == dout || o == y || o == ws))
+      return MOE_ERR_INVALID_ARG;
+  if (dgate && dgate == static_cast<void*>(dpost_w)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dout) || !aligned16(y) || !aligned16(rstd) || !aligned16(dy) || !aligned16(dpost_w) ||
+      !aligned16(dgate) || !aligned256(ws))
+    return MOE_ERR_MISALIGNED;
+  const bool cols = dpost_w || (dgate && params->gate_kind == MOE_GATE_CHANNEL);
+  if (cols && T > 0 && !ws) return MOE_ERR_INVALID_ARG;
+  if (cols && ws_bytes < moe_norm_backward_workspace_size(T, H)) return MOE_ERR_WORKSPACE;
+  NormBwdParams p{};
+  p.d = static_cast<const u32x4_t*>(dout);
+  p.y = static_cast<const u32x4_t*>(y);
+  p.T = T;
+  p.rc = static_cast<int>(static_cast<int64_t>(H) * dtype_size(act) / 16);
+  p.inv_h = 1.0f / static_cast<float>(H);
+  p.scale = params->scale;
+  p.rstd = rstd;
+  p.w = static_cast<const u32x4_t*>(params->post_w);
+  p.gate = params->gate;
+  p.gate_kind = params->gate_kind;
+  p.dy = static_cast<u32x4_t*>(dy);
+  const bool channel = params->gate_kind == MOE_GATE_CHANNEL;
+  p.dgate = channel ? nullptr : dgate;
+  return launch_norm_bwd(p, act == MOE_BF16, H, dpost_w, channel ? static_cast<float*>(dgate) : nullptr,
+                         accumulate != 0, ws, as_stream(stream));
+}

@@ -213,8 +213,8 @@ __global__ __launch_bounds__(256) void k_topk(TopkParams p) {
   topk_token(p, t, v, s_score[wave]);
 }
 
-moe_status launch_route(const RouteArgs& a, hipStream_t s) {
-  if (a.T == 0) return MOE_OK;
+// The split-K partial logits [S][T][E] of a.x, into a.part.
+moe_status launch_route_logits(const RouteArgs& a, hipStream_t s) {
   const int E = a.p.E;
   const int S = route_splits(a.T, a.H, E);
   GemmParams p{};
@@ -251,6 +251,14 @@ moe_status launch_route(const RouteArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_gemm_nt_f32<MODE_ROUTER>), grid, dim3(256), 0, s, p);
   }
   DBOMOE_CHECK_LAUNCH();
+  return MOE_OK;
+}
+
+moe_status launch_route(const RouteArgs& a, hipStream_t s) {
+  if (a.T == 0) return MOE_OK;
+  const moe_status st = launch_route_logits(a, s);
+  if (st != MOE_OK) return st;
+  const int E = a.p.E, S = route_splits(a.T, a.H, E);
   TopkParams tp{a.part, S, a.T, E, a.bias, a.forced, a.p, a.logits, a.ids, a.w};
   hipLaunchKernelGGL(k_topk, dim3(static_cast<unsigned>((a.T + 3) / 4)), dim3(256), 0, s, tp);
   DBOMOE_CHECK_LAUNCH();

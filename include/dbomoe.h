@@ -50,7 +50,7 @@ typedef enum {
   MOE_ERR_HIP = -5           /* a HIP runtime call or kernel launch failed */
 } moe_status;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3FN = 2 } moe_dtype;
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3FN = 2, MOE_INT8 = 3 } moe_dtype;
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 
 /* Routing parameters.  The pages fix no routing rule; this is the reading:
@@ -424,6 +424,167 @@ moe_status moe_adamw_table_build(const moe_adamw_tensor* tensors, int32_t n_tens
 moe_status moe_adamw_table_check(const void* table_host);
 moe_status moe_adamw_step(const void* table_host, const void* table_dev, const moe_adamw_params* hp,
                           const int32_t* step, const float* lr_scale, const float* grad_scale, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Routing that keeps the experts balanced.
+ *
+ * moe_route_select - selection and weights from logits that the caller has.
+ *   scores p = softmax(logits) over all E, or sigmoid(logits) (params->score);
+ *   keys p + select_bias; n_groups > 1 (either score): a group's score is the
+ *   sum of its group_topn best keys, and experts of the topk_groups best groups
+ *   are candidates; the k best keys are chosen (slot j = rank j), every tie goes
+ *   to the lower index.  Weight of slot j: p of its expert (the bias is not in
+ *   it), divided by the sum over the slots if renormalize, times routed_scale.
+ *   logits      [T, E] fp32
+ *   select_bias [E] fp32 or NULL (zero); finite
+ *   topk_ids    [T, k] int32 out; topk_w [T, k] fp32 out
+ *   load        [E] int32 or NULL: the number of tokens that chose each expert is
+ *               ADDED (start from zeros)
+ * Scores, keys and their sums are held in 64 bits, weights rounded once to fp32.
+ * An expert whose logit is -inf or NaN is masked: its score is 0, and it is only
+ * chosen where fewer than k candidates are left, then lowest index first, with
+ * weight 0 and not counted in load; it does not count in a group's score, nor
+ * for a group that has no other expert.  A logit of +inf is taken as the largest
+ * finite one.  moe_route_backward gives the gradient of the weights.
+ *
+ * moe_route_balanced - moe_route_topk with this selection: the router's product,
+ *   then moe_route_select of logits + logit_bias.  Arguments and workspace as
+ *   moe_route_topk.
+ *
+ * moe_route_bias_update - bias[e] += rate * sign(mean(load) - load[e]) (compared in
+ *   whole numbers), then load = 0.  E <= 256, rate >= 0.
+ *
+ * moe_route_balance_loss - the balance loss of T tokens and its gradient.
+ *   f_e = E load_e / sum(load) (0 without load);  q_te = p_te (softmax) or
+ *   p_te / sum_j p_tj (sigmoid);  f has no gradient
+ *   loss [1] fp32 out   = coef / T * sum_t sum_e f_e q_te
+ *   dlogits [T, E], fp32 or bf16 (dl): coef / T q_te (f_e - sum_j f_j q_tj), times
+ *                1 - p_te (sigmoid); accumulate 1: added to what is there, rounded once
+ *   ws           moe_route_balance_loss_workspace_size(T, E) bytes
+ * Of params only E and score are used.  Masked logits (-inf, NaN) have q = 0 and no
+ * gradient.  T == 0: loss = 0.
+ * ------------------------------------------------------------------------- */
+moe_status moe_route_select(const float* logits, int64_t T, const float* select_bias,
+                            const moe_route_params* params, int32_t* topk_ids, float* topk_w, int32_t* load,
+                            void* stream);
+moe_status moe_route_balanced(const void* x, moe_dtype act, int64_t T, int32_t H, const void* w_router,
+                              const float* logit_bias, const float* select_bias, const moe_route_params* params,
+                              float* logits_out, int32_t* topk_ids, float* topk_w, int32_t* load, void* ws,
+                              size_t ws_bytes, void* stream);
+moe_status moe_route_bias_update(float* bias, int32_t* load, int32_t E, float rate, void* stream);
+size_t moe_route_balance_loss_workspace_size(int64_t T, int32_t E);
+moe_status moe_route_balance_loss(const float* logits, int64_t T, const int32_t* load,
+                                  const moe_route_params* params, float coef, float* loss, void* dlogits,
+                                  moe_dtype dl, int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit integers with a scale for each token and each output channel.
+ *
+ * moe_quant_int8_rows - rows x [n, K] (fp32 or bf16) to q [n, K] and scale [n]:
+ *   scale = max|row| * (1 / 127), each rounded to fp32, q = the integer nearest to x / scale, ties to
+ *   even (0 for a row of zeros).  Real value = q * scale.  A row that holds an
+ *   infinity or NaN gets q = 0 and scale = NaN, so that every product of it is NaN.
+ *   Weights [E, N, K] are quantised by the same call as E * N rows.  K % 16 == 0.
+ *
+ * moe_dispatch_int8 - moe_dispatch whose row gather quantises each token row once:
+ *   xq_perm [T*k, H] integers, xq_scale [T*k] fp32.  Other arguments, outputs and
+ *   errors as moe_dispatch; act fp32 or bf16; H % 16 == 0.
+ *
+ * moe_grouped_gemm_int8 - c[r, n] = (sum_k a[r, k] b[e, n, k]) * a_scale[r] *
+ *   b_scale[e, n] for the rows of expert e (offsets, rows and cap_rows as in
+ *   moe_grouped_gemm NT).  a [cap_rows, K], b [E_loc, N, K], a_scale [cap_rows],
+ *   b_scale [E_loc, N], c [cap_rows, N] fp32 or bf16 (ct).  The sum is exact (int32);
+ *   it is rounded to fp32, and so is each of the two products with a scale, then
+ *   once to ct.
+ *
+ * moe_grouped_swiglu_int8 - that product with w13 [E_loc, 2I, H] (gate rows over up
+ *   rows, w13_scale [E_loc, 2I]) and h = silu(g) * u [cap_rows, I], fp32 or bf16 (ht).
+ *
+ * moe_grouped_ffn_int8 - a whole expert: moe_grouped_swiglu_int8 with h in fp32,
+ *   h quantised as moe_quant_int8_rows does, and the product with w2 [E_loc, H, I],
+ *   w2_scale [E_loc, H]; y [cap_rows, H] bf16.
+ *   ws  moe_ffn_int8_workspace_size(cap_rows, I) bytes
+ * Rows outside the experts' ranges are left as they are.  N % 8 == 0 and K % 16 == 0
+ * (the FFN: H and I both multiples of 16), else MOE_ERR_MISALIGNED; K <= 2^17 (the sums
+ * stay in int32) and N <= 2^22; E_loc <= 256.  Integers are -127 .. 127 (-128 is
+ * taken as it is, and then K <= 2^16 keeps the sums).
+ * ------------------------------------------------------------------------- */
+moe_status moe_quant_int8_rows(const void* x, moe_dtype act, int64_t n, int32_t K, int8_t* q, float* scale,
+                               void* stream);
+moe_status moe_dispatch_int8(const void* x, moe_dtype act, int64_t T, int32_t H, const int32_t* topk_ids,
+                             int32_t k, int32_t E_total, int32_t expert_begin, int32_t expert_end, int32_t tile_m,
+                             int32_t* counts, int32_t* offsets, int32_t* tile_offsets, int32_t* perm,
+                             int32_t* inv, int8_t* xq_perm, float* xq_scale, void* ws, size_t ws_bytes,
+                             void* stream);
+moe_status moe_grouped_gemm_int8(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
+                                 const int32_t* offsets, int32_t E_loc, int64_t cap_rows, int32_t N, int32_t K,
+                                 void* c, moe_dtype ct, void* stream);
+moe_status moe_grouped_swiglu_int8(const int8_t* xq, const float* xq_scale, const int8_t* w13,
+                                   const float* w13_scale, const int32_t* offsets, int32_t E_loc,
+                                   int64_t cap_rows, int32_t H, int32_t I, void* h, moe_dtype ht, void* stream);
+size_t moe_ffn_int8_workspace_size(int64_t cap_rows, int32_t I);
+moe_status moe_grouped_ffn_int8(const int8_t* xq, const float* xq_scale, int32_t H, int32_t I,
+                                const int32_t* offsets, int32_t E_loc, int64_t cap_rows, const int8_t* w13,
+                                const int8_t* w2, const float* w13_scale, const float* w2_scale, void* y, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Norms before and after the layer, with its gate, scale and residual.
+ * r(v) = 1 / sqrt(mean(v^2) + eps) over a row; all in fp32, each output rounded once.
+ *
+ * moe_pre_norm - n = x r(x) w.  x, n [T, H], w [H] act; rstd [T] fp32 out = r, or NULL.
+ *   n may be x.
+ *
+ * moe_post_norm - out = res + scale * g * (y r(y) post_w), and with next_w also
+ *   next_n = out r(out) next_w (of out before its rounding).
+ *   y, res, out, next_n [T, H] act; res NULL: no residual; out may be res
+ *   post_w NULL: no norm (y itself); next_w and next_n go together
+ *   gate: MOE_GATE_CHANNEL [H] act, MOE_GATE_TOKEN [T] fp32, MOE_GATE_FULL [T, H] act
+ *   rstd [T] fp32 out = r(y) (with post_w), next_rstd [T] = r(out) (with next_w), or NULL
+ *
+ * moe_combine_post_norm - the same with y = what moe_combine would give (y_perm, inv,
+ *   topk_w, shared_out as there), which stays in fp32; y_out [T, H] act: y, rounded,
+ *   for the backward pass, or NULL.
+ *
+ * moe_pre_norm_backward - dx = dres + r (q - xh mean(q xh)), xh = x r, q = dn w;
+ *   dw [H] fp32 = sum_t dn xh (NULL: not wanted).  rstd [T] as moe_pre_norm gave it; dres
+ *   [T, H] act or NULL: the gradient that reaches x beside the norm; dx may be dn or dres.
+ *
+ * moe_post_norm_backward - gradients of moe_post_norm's out (the residual's is dout):
+ *   dy [T, H] act (may be dout); dpost_w [H] fp32 or NULL; dgate or NULL: fp32 [H]
+ *   (channel), fp32 [T] (token) or act [T, H] (full).  rstd [T] and params as given to
+ *   the forward pass (next_w is not used).
+ * accumulate 1: dw, dpost_w and a channel gate's dgate are added to (dx, dy and the other
+ * gates' are written).  Column sums are added in a fixed order.
+ *   ws  moe_norm_backward_workspace_size(T, H) bytes (for dw, dpost_w or a channel's dgate)
+ * A row is at most 64 KB; H * sizeof(act) % 16 == 0; T < 2^22; eps > 0.
+ * ------------------------------------------------------------------------- */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 } moe_gate_kind;
+typedef struct {
+  const void* post_w;           /* [H] act or NULL */
+  const void* gate;             /* see gate_kind; NULL with MOE_GATE_NONE */
+  int32_t gate_kind;            /* moe_gate_kind */
+  float scale;
+  float eps;
+  const void* next_w;           /* [H] act or NULL */
+} moe_post_norm_params;
+
+moe_status moe_pre_norm(const void* x, moe_dtype act, int64_t T, int32_t H, const void* w, float eps, void* n,
+                        float* rstd, void* stream);
+moe_status moe_post_norm(const void* y, moe_dtype act, int64_t T, int32_t H, const void* res,
+                         const moe_post_norm_params* params, void* out, float* rstd, void* next_n,
+                         float* next_rstd, void* stream);
+moe_status moe_combine_post_norm(const void* y_perm, moe_dtype act, int64_t T, int32_t H, int32_t k,
+                                 const int32_t* inv, const float* topk_w, const void* shared_out, const void* res,
+                                 const moe_post_norm_params* params, void* out, void* y_out, float* rstd,
+                                 void* next_n, float* next_rstd, void* stream);
+size_t moe_norm_backward_workspace_size(int64_t T, int32_t H);
+moe_status moe_pre_norm_backward(const void* dn, const void* x, moe_dtype act, int64_t T, int32_t H,
+                                 const float* rstd, const void* w, const void* dres, void* dx, float* dw,
+                                 int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+moe_status moe_post_norm_backward(const void* dout, const void* y, moe_dtype act, int64_t T, int32_t H,
+                                  const float* rstd, const moe_post_norm_params* params, void* dy, float* dpost_w,
+                                  void* dgate, int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * dbo_moe_layer - the whole layer under Dual-Batch Overlap.
