@@ -50,6 +50,15 @@ class moe_route_params(ctypes.Structure):
                 ("routed_scale", ctypes.c_float)]
 
 
+class moe_post_norm_params(ctypes.Structure):
+    _fields_ = [("post_w", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("gate_kind", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("next_w", ctypes.c_void_p)]
+
+
+class moe_block_params(ctypes.Structure):
+    _fields_ = [("pre_w", ctypes.c_void_p), ("post", moe_post_norm_params), ("residual", ctypes.c_int32)]
+
+
 class moe_layer_desc(ctypes.Structure):
     _fields_ = [("H", ctypes.c_int32), ("I", ctypes.c_int32), ("act", ctypes.c_int32),
                 ("wdt", ctypes.c_int32), ("route", moe_route_params),
@@ -57,7 +66,8 @@ class moe_layer_desc(ctypes.Structure):
                 ("w_router", ctypes.c_void_p), ("w13", ctypes.c_void_p), ("w2", ctypes.c_void_p),
                 ("w13_scale", ctypes.c_void_p), ("w2_scale", ctypes.c_void_p),
                 ("shared_I", ctypes.c_int32), ("shared_w13", ctypes.c_void_p),
-                ("shared_w2", ctypes.c_void_p), ("fp8_act", ctypes.c_int32)]
+                ("shared_w2", ctypes.c_void_p), ("fp8_act", ctypes.c_int32),
+                ("select_bias", ctypes.c_void_p), ("block", ctypes.POINTER(moe_block_params))]
 
 
 class dbo_opts(ctypes.Structure):
@@ -76,11 +86,6 @@ class moe_adamw_tensor(ctypes.Structure):
 class moe_adamw_params(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("seed", ctypes.c_uint32)]
-
-
-class moe_post_norm_params(ctypes.Structure):
-    _fields_ = [("post_w", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("gate_kind", ctypes.c_int32),
-                ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("next_w", ctypes.c_void_p)]
 
 
 class MoEError(RuntimeError):

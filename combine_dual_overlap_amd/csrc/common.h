@@ -161,6 +161,7 @@ struct CombineArgs {
 };
 moe_status launch_combine(const CombineArgs& a, hipStream_t s);
 
+constexpr int kRowMaxBytes = 65536;      // largest row of a norm
 // moe_post_norm on what launch_combine would have written (a.out receives out).
 moe_status check_post_norm(const moe_post_norm_params* p);
 moe_status launch_combine_post_norm(const CombineArgs& a, const void* res, const moe_post_norm_params& q, void* y_out,
@@ -186,7 +187,7 @@ struct FfnInt8Args {
   hipEvent_t t0, t1, t2;   // as in FfnArgs
 };
 size_t ffn_int8_ws_bytes(int64_t cap_rows, int32_t I);
-moe_status check_ffn_int8_shapes(const int32_t* offsets, int32_t E_loc, int64_t cap, int32_t H, int32_t I);
+moe_status check_ffn_int8_shapes(bool dense, int32_t E_loc, int64_t cap, int32_t H, int32_t I);
 moe_status launch_ffn_int8(const FfnInt8Args& a, hipStream_t s);
 
 moe_status check_route_params(const moe_route_params* p);

@@ -426,13 +426,17 @@ static moe_status launch_int8(I8Params& p, hipStream_t s) {
 }
 
 // What every product checks: sizes, then pointers.
-static moe_status int8_check_sizes(const int32_t* offsets, int32_t E_loc, int64_t cap, int32_t N, int32_t K) {
+static moe_status int8_check_sizes(bool dense, int32_t E_loc, int64_t cap, int32_t N, int32_t K) {
   if (E_loc < 1 || E_loc > 256 || cap < 0 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
-  if (!offsets && E_loc != 1) return MOE_ERR_INVALID_ARG;
+  if (dense && E_loc != 1) return MOE_ERR_INVALID_ARG;
   // 127^2 K stays below 2^31
   if (cap > (1 << 30) || N > (1 << 22) || K > (1 << 17)) return MOE_ERR_UNSUPPORTED;
-  if (N % 8 || K % 16) return MOE_ERR_MISALIGNED;
-  return offsets && !aligned16(offsets) ? MOE_ERR_MISALIGNED : MOE_OK;
+  return N % 8 || K % 16 ? MOE_ERR_MISALIGNED : MOE_OK;
+}
+
+static moe_status int8_check(const int32_t* offsets, int32_t E_loc, int64_t cap, int32_t N, int32_t K) {
+  const moe_status st = int8_check_sizes(!offsets, E_loc, cap, N, K);
+  return st == MOE_OK && offsets && !aligned16(offsets) ? MOE_ERR_MISALIGNED : st;
 }
 
 static I8Params int8_params(const int8_t* a, const float* as, const int8_t* b, const float* bs, const int32_t* offsets,
@@ -466,9 +470,9 @@ static FfnInt8Ws ffn_int8_ws(int64_t cap, int32_t I) {
 
 size_t ffn_int8_ws_bytes(int64_t cap, int32_t I) { return ffn_int8_ws(cap, I).bytes; }
 
-moe_status check_ffn_int8_shapes(const int32_t* offsets, int32_t E_loc, int64_t cap, int32_t H, int32_t I) {
-  moe_status st = int8_check_sizes(offsets, E_loc, cap, I, H);
-  if (st == MOE_OK) st = int8_check_sizes(offsets, E_loc, cap, H, I);
+moe_status check_ffn_int8_shapes(bool dense, int32_t E_loc, int64_t cap, int32_t H, int32_t I) {
+  moe_status st = int8_check_sizes(dense, E_loc, cap, I, H);
+  if (st == MOE_OK) st = int8_check_sizes(dense, E_loc, cap, H, I);
   if (st != MOE_OK) return st;
   // the up rows are addressed by 32-bit byte offsets from the gate rows
   return (static_cast<int64_t>(I) + 256) * H >= (int64_t{1} << 32) ? MOE_ERR_UNSUPPORTED : MOE_OK;
@@ -531,7 +535,7 @@ extern "C" moe_status moe_quant_int8_rows(const void* x, moe_dtype act, int64_t 
 extern "C" moe_status moe_grouped_gemm_int8(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
                                             const int32_t* offsets, int32_t E_loc, int64_t cap_rows, int32_t N,
                                             int32_t K, void* c, moe_dtype ct, void* stream) {
-  const moe_status st = int8_check_sizes(offsets, E_loc, cap_rows, N, K);
+  const moe_status st = int8_check(offsets, E_loc, cap_rows, N, K);
   if (st != MOE_OK) return st;
   if (ct != MOE_F32 && ct != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (cap_rows == 0) return MOE_OK;
@@ -547,7 +551,7 @@ extern "C" moe_status moe_grouped_swiglu_int8(const int8_t* xq, const float* xq_
                                               const float* w13_scale, const int32_t* offsets, int32_t E_loc,
                                               int64_t cap_rows, int32_t H, int32_t I, void* h, moe_dtype ht,
                                               void* stream) {
-  const moe_status st = int8_check_sizes(offsets, E_loc, cap_rows, I, H);
+  const moe_status st = int8_check(offsets, E_loc, cap_rows, I, H);
   if (st != MOE_OK) return st;
   if (ht != MOE_F32 && ht != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if ((static_cast<int64_t>(I) + 256) * H >= (int64_t{1} << 32)) return MOE_ERR_UNSUPPORTED;
@@ -569,8 +573,9 @@ extern "C" moe_status moe_grouped_ffn_int8(const int8_t* xq, const float* xq_sca
                                            const int32_t* offsets, int32_t E_loc, int64_t cap_rows, const int8_t* w13,
                                            const int8_t* w2, const float* w13_scale, const float* w2_scale, void* y,
                                            void* ws, size_t ws_bytes, void* stream) {
-  const moe_status st = check_ffn_int8_shapes(offsets, E_loc, cap_rows, H, I);
+  const moe_status st = check_ffn_int8_shapes(!offsets, E_loc, cap_rows, H, I);
   if (st != MOE_OK) return st;
+  if (offsets && !aligned16(offsets)) return MOE_ERR_MISALIGNED;
   if (cap_rows == 0) return MOE_OK;
   if (!xq || !xq_scale || !w13 || !w13_scale || !w2 || !w2_scale || !y || !ws) return MOE_ERR_INVALID_ARG;
   if (y == xq || y == xq_scale || y == w13 || y == w2 || y == w13_scale || y == w2_scale || y == ws)

@@ -37,7 +37,7 @@ namespace dbomoe {
 namespace {
 
 enum Buf { B_LOGITS, B_IDS, B_W, B_COUNTS, B_OFFSETS, B_TILE_OFF, B_PERM, B_INV, B_XPERM, B_YPERM,
-           B_SHOUT, B_DISPWS, B_ROUTEWS, B_H, B_SHH, B_XSCALE, B_COUNT };
+           B_SHOUT, B_DISPWS, B_ROUTEWS, B_H, B_SHH, B_XSCALE, B_XN, B_COUNT };
 
 struct HalfLayout {
   size_t off[B_COUNT];
@@ -48,6 +48,13 @@ struct HalfLayout {
 size_t route_ws_bound(int64_t T, int32_t E) {
   const int64_t rows = T > 16384 ? T : 16384;
   return align_up(static_cast<size_t>(rows) * E * 4, 256);
+}
+
+// Output slabs of the shared experts' down projection.  (Integer experts run in
+// launches of their own, and so do the shared experts then.)
+int shared_slabs(const moe_layer_desc* d) {
+  if (d->shared_I == 0) return 0;
+  return d->wdt == MOE_INT8 ? 1 : dense_down_chunks(d->act, d->shared_I, d->I);
 }
 
 HalfLayout half_layout(const moe_layer_desc* d, int64_t T) {
@@ -64,16 +71,15 @@ HalfLayout half_layout(const moe_layer_desc* d, int64_t T) {
   sz[B_TILE_OFF] = static_cast<size_t>(E_loc + 1) * 4;
   sz[B_PERM] = static_cast<size_t>(cap) * 4;
   sz[B_INV] = static_cast<size_t>(cap) * 4;
-  const bool f8 = d->fp8_act != 0;
-  sz[B_XPERM] = static_cast<size_t>(cap) * d->H * (f8 ? 1 : as);
-  sz[B_XSCALE] = f8 ? static_cast<size_t>(cap) * (d->H / 128) : 0;
+  const bool f8 = d->fp8_act != 0, i8 = d->wdt == MOE_INT8;
+  sz[B_XPERM] = static_cast<size_t>(cap) * d->H * (f8 || i8 ? 1 : as);
+  sz[B_XSCALE] = f8 ? static_cast<size_t>(cap) * (d->H / 128) : i8 ? static_cast<size_t>(cap) * 4 : 0;
   sz[B_YPERM] = static_cast<size_t>(cap) * d->H * as;
-  sz[B_SHOUT] = d->shared_I > 0
-                    ? static_cast<size_t>(dense_down_chunks(d->act, d->shared_I, d->I)) * T * d->H * as
-                    : 0;
+  sz[B_SHOUT] = static_cast<size_t>(shared_slabs(d)) * T * d->H * as;
   sz[B_DISPWS] = dispatch_ws_bytes(T, k, E_loc);
   sz[B_ROUTEWS] = route_ws_bound(T, E);
-  sz[B_H] = f8 ? ffn_fp8_ws_bytes(cap, d->I) : ffn_ws_bytes(cap, d->I, d->act);
+  sz[B_H] = f8 ? ffn_fp8_ws_bytes(cap, d->I) : i8 ? ffn_int8_ws_bytes(cap, d->I) : ffn_ws_bytes(cap, d->I, d->act);
+  sz[B_XN] = d->block && d->block->pre_w ? static_cast<size_t>(T) * d->H * as : 0;
   sz[B_SHH] = d->shared_I > 0 ? ffn_ws_bytes(T, d->shared_I, d->act) : 0;
   HalfLayout L;
   size_t o = 0;
@@ -85,6 +91,15 @@ HalfLayout half_layout(const moe_layer_desc* d, int64_t T) {
   return L;
 }
 
+moe_status check_block(const moe_layer_desc* d) {
+  const moe_block_params* b = d->block;
+  const moe_status st = check_post_norm(&b->post);
+  if (st != MOE_OK) return st;
+  if (b->post.next_w || (b->residual != 0 && b->residual != 1)) return MOE_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(d->H) * dtype_size(d->act) > kRowMaxBytes) return MOE_ERR_UNSUPPORTED;
+  return b->pre_w && !aligned16(b->pre_w) ? MOE_ERR_MISALIGNED : MOE_OK;
+}
+
 moe_status check_desc(const moe_layer_desc* d) {
   if (!d) return MOE_ERR_INVALID_ARG;
   moe_status st = check_route_params(&d->route);
@@ -92,8 +107,19 @@ moe_status check_desc(const moe_layer_desc* d) {
   if (d->expert_begin < 0 || d->expert_end <= d->expert_begin || d->expert_end > d->route.E)
     return MOE_ERR_INVALID_ARG;
   const int E_loc = d->expert_end - d->expert_begin;
-  st = check_ffn_shapes(d->act, d->wdt, d->H, d->I, E_loc, d->w13_scale, d->w2_scale);
+  if (d->wdt == MOE_INT8) {
+    if (d->act != MOE_BF16 || d->H % 128) return MOE_ERR_UNSUPPORTED;      // (the router's product takes 128 columns)
+    if (!d->w13_scale || !d->w2_scale) return MOE_ERR_INVALID_ARG;
+    st = check_ffn_int8_shapes(false, E_loc, 0, d->H, d->I);
+  } else {
+    st = check_ffn_shapes(d->act, d->wdt, d->H, d->I, E_loc, d->w13_scale, d->w2_scale);
+  }
   if (st != MOE_OK) return st;
+  if (d->select_bias && !aligned16(d->select_bias)) return MOE_ERR_MISALIGNED;
+  if (d->block) {
+    st = check_block(d);
+    if (st != MOE_OK) return st;
+  }
   if (d->fp8_act != 0 && d->fp8_act != 1) return MOE_ERR_INVALID_ARG;
   if (d->fp8_act) {
     if (d->act != MOE_BF16 || d->wdt != MOE_FP8_E4M3FN) return MOE_ERR_UNSUPPORTED;
@@ -111,7 +137,7 @@ moe_status check_desc(const moe_layer_desc* d) {
     if (!d->shared_w13 || !d->shared_w2) return MOE_ERR_INVALID_ARG;
     if (!aligned16(d->shared_w13) || !aligned16(d->shared_w2)) return MOE_ERR_MISALIGNED;
     // the combine sums k routed rows and the shared down projection's slabs
-    if (d->route.k + dense_down_chunks(d->act, d->shared_I, d->I) > 32) return MOE_ERR_UNSUPPORTED;
+    if (d->route.k + shared_slabs(d) > 32) return MOE_ERR_UNSUPPORTED;
   }
   return MOE_OK;
 }
@@ -138,11 +164,44 @@ struct HipBackend {
     return reinterpret_cast<T*>(ws + static_cast<size_t>(mb) * L.bytes + L.off[b]);
   }
 
+  // The experts in 8-bit integers, then the shared experts in act.
+  moe_status launch_int8_experts(int mb, const char* xm, int64_t T, hipStream_t s) const {
+    FfnInt8Args a{buf<int8_t>(mb, B_XPERM), buf<float>(mb, B_XSCALE), d->H, d->I, buf<int32_t>(mb, B_OFFSETS),
+                  d->expert_end - d->expert_begin, T * d->route.k, static_cast<const int8_t*>(d->w13),
+                  static_cast<const int8_t*>(d->w2), d->w13_scale, d->w2_scale, buf<void>(mb, B_YPERM),
+                  buf<void>(mb, B_H)};
+    if (ctx->timing) {
+      a.t0 = ctx->tev[ctx->slot][mb][0];
+      a.t1 = ctx->tev[ctx->slot][mb][1];
+      a.t2 = ctx->tev[ctx->slot][mb][2];
+      ctx->timed[ctx->slot][mb] = true;
+    }
+    const moe_status st = launch_ffn_int8(a, s);
+    if (st != MOE_OK || d->shared_I == 0) return st;
+    FfnArgs sh{};
+    sh.x = xm;
+    sh.act = d->act;
+    sh.H = d->H;
+    sh.I = d->shared_I;
+    sh.E_loc = 1;
+    sh.cap_rows = T;
+    sh.rows_hint = T;
+    sh.w13 = d->shared_w13;
+    sh.w2 = d->shared_w2;
+    sh.wdt = d->act;
+    sh.y = buf<void>(mb, B_SHOUT);
+    sh.h = buf<void>(mb, B_SHH);
+    return launch_ffn(sh, s);
+  }
+
   int launch(int stream, int mb, int stage) {
     hipStream_t s = streams[stream];
     const size_t as = dtype_size(d->act);
     const int64_t T = rows[mb];
-    const char* xm = x + row0[mb] * d->H * as;
+    const char* x_in = x + row0[mb] * d->H * as;
+    // what the layer computes from: the tokens, or their norm (written by the route stage)
+    const bool pre = d->block && d->block->pre_w;
+    const char* xm = pre ? buf<char>(mb, B_XN) : x_in;
     const int k = d->route.k;
     const int E_loc = d->expert_end - d->expert_begin;
     // The comm-stream stages that can run beside the other microbatch's FFN
@@ -158,10 +217,14 @@ struct HipBackend {
     moe_status st = MOE_OK;
     switch (stage) {
       case sched::kRoute: {
+        if (pre) {
+          st = launch_pre_norm(x_in, d->act, T, d->H, d->block->pre_w, d->block->post.eps, buf<void>(mb, B_XN), nullptr, s);
+          if (st != MOE_OK) return st;
+        }
         RouteArgs a{xm, d->act, T, d->H, d->w_router, bias, forced ? forced + row0[mb] * k : nullptr,
                     d->route, buf<float>(mb, B_LOGITS), buf<int32_t>(mb, B_IDS), buf<float>(mb, B_W),
                     buf<float>(mb, B_ROUTEWS)};
-        st = launch_route(a, s);
+        st = d->select_bias && !forced ? launch_route_balanced(a, d->select_bias, nullptr, s) : launch_route(a, s);
         break;
       }
       case sched::kDispatch:
@@ -171,7 +234,8 @@ struct HipBackend {
                        d->expert_end, 0, buf<int32_t>(mb, B_COUNTS), buf<int32_t>(mb, B_OFFSETS),
                        nullptr, buf<int32_t>(mb, B_PERM), buf<int32_t>(mb, B_INV),
                        buf<void>(mb, B_XPERM), buf<void>(mb, B_DISPWS), o->comm_cu_budget,
-                       d->fp8_act ? buf<uint8_t>(mb, B_XSCALE) : nullptr, beside_ffn};
+                       d->fp8_act ? buf<uint8_t>(mb, B_XSCALE) : nullptr, beside_ffn,
+                       d->wdt == MOE_INT8 ? buf<float>(mb, B_XSCALE) : nullptr};
         // timing: from the first dispatch kernel to the last (send start .. recv end)
         if (stage != sched::kDispatchRecv && ctx->timing &&
             hipEventRecord(ctx->tev[ctx->slot][mb][3], s) != hipSuccess)
@@ -188,6 +252,10 @@ struct HipBackend {
         // Routed experts on the dispatched rows plus the shared experts on the
         // microbatch's own rows, in the same two launches.
         const int64_t hint = (T * k + d->route.E - 1) / d->route.E;
+        if (d->wdt == MOE_INT8) {
+          st = launch_int8_experts(mb, xm, T, s);
+          break;
+        }
         FfnArgs a{};
         a.x = buf<void>(mb, B_XPERM);
         a.xs = d->fp8_act ? buf<uint8_t>(mb, B_XSCALE) : nullptr;
@@ -227,10 +295,16 @@ struct HipBackend {
       case sched::kCombine: {
         CombineArgs a{buf<void>(mb, B_YPERM), d->act, T, d->H, k, buf<int32_t>(mb, B_INV), buf<float>(mb, B_W),
                       d->shared_I > 0 ? buf<void>(mb, B_SHOUT) : nullptr, out + row0[mb] * d->H * as,
-                      o->comm_cu_budget, d->shared_I > 0 ? dense_down_chunks(d->act, d->shared_I, d->I) : 0,
-                      beside_ffn};
+                      o->comm_cu_budget, shared_slabs(d), beside_ffn};
         if (ctx->timing && hipEventRecord(ctx->tev[ctx->slot][mb][5], s) != hipSuccess) return MOE_ERR_HIP;
-        st = launch_combine(a, s);
+        if (d->block) {
+          moe_post_norm_params q = d->block->post;
+          if (q.gate_kind == MOE_GATE_TOKEN) q.gate = static_cast<const float*>(q.gate) + row0[mb];
+          if (q.gate_kind == MOE_GATE_FULL) q.gate = static_cast<const char*>(q.gate) + row0[mb] * d->H * as;
+          st = launch_combine_post_norm(a, d->block->residual ? x_in : nullptr, q, nullptr, nullptr, nullptr, nullptr, s);
+        } else {
+          st = launch_combine(a, s);
+        }
         if (st == MOE_OK && ctx->timing && hipEventRecord(ctx->tev[ctx->slot][mb][6], s) != hipSuccess)
           return MOE_ERR_HIP;
         break;
@@ -387,6 +461,9 @@ extern "C" moe_status dbo_moe_layer(dbo_ctx* ctx, const moe_layer_desc* d, const
       (logit_bias && !aligned16(logit_bias)))
     return MOE_ERR_MISALIGNED;
   if (T * d->route.k > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (d->select_bias && T >= (int64_t{1} << 26)) return MOE_ERR_UNSUPPORTED;      // as moe_route_balanced
+  if (d->block && T >= (int64_t{1} << 22)) return MOE_ERR_UNSUPPORTED;            // as moe_post_norm
+  if (d->wdt == MOE_INT8 && T * d->route.k > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   const HalfLayout L = half_layout(d, T);
   if (ws_bytes < 2 * L.bytes) return MOE_ERR_WORKSPACE;
 

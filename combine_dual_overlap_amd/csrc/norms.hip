@@ -13,6 +13,8 @@
 
 namespace dbomoe {
 
+static_assert(kRowMaxBytes <= kRowMaxChunks * 16, "rows in registers");
+
 struct NormOutParams {
   const u32x4_t* y;            // [T] rows, or the dispatched rows (GATHER)
   const int32_t* inv;          // GATHER: [T k]
@@ -91,97 +93,102 @@ __global__ __launch_bounds__(RowShape<W>::THREADS) void k_norm_out(NormOutParams
   using C = Chunk<BF16>;
   __shared__ float s_one[W], s_two[W];
   const int l = W == 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * RowShape<W>::ROWS + (W == 1 ? threadIdx.x >> 6 : 0);
-  if (t >= p.T) return;                                     // (a whole row's waves)
   auto at = [&](int i) { return i * 64 * W + l; };
-  float v[CH][N];
-  if constexpr (GATHER) {
-    gather_sum<BF16, W, CH>(p, t, l, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < CH; ++i)
-      C::unpack(at(i) < p.rc ? p.y[t * p.rc + at(i)] : u32x4_t{0, 0, 0, 0}, v[i]);
-  }
-  if constexpr (GATHER) {
-    if (p.y_out)
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * RowShape<W>::ROWS + (W == 1 ? threadIdx.x >> 6 : 0);
+  for (int64_t t = first; t < p.T; t += static_cast<int64_t>(gridDim.x) * RowShape<W>::ROWS) {
+    float v[CH][N];
+    if constexpr (GATHER) {
+      gather_sum<BF16, W, CH>(p, t, l, v);
+    } else {
 #pragma unroll
       for (int i = 0; i < CH; ++i)
-        if (at(i) < p.rc) p.y_out[t * p.rc + at(i)] = C::pack(v[i]);
-  }
-  // what the outputs need besides y, asked for before the sum over the row
-  u32x4_t res[CH], pw[CH], gt[CH], nw[CH];
-  const u32x4_t* gate = static_cast<const u32x4_t*>(p.gate);
+        C::unpack(at(i) < p.rc ? p.y[t * p.rc + at(i)] : u32x4_t{0, 0, 0, 0}, v[i]);
+    }
+    if constexpr (GATHER) {
+      if (p.y_out)
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    if (at(i) >= p.rc) continue;
-    if (p.res) res[i] = p.res[t * p.rc + at(i)];
-    if (p.post_w) pw[i] = p.post_w[at(i)];
-    if (p.gate_kind == MOE_GATE_CHANNEL) gt[i] = gate[at(i)];
-    if (p.gate_kind == MOE_GATE_FULL) gt[i] = gate[t * p.rc + at(i)];
-    if (p.next_w) nw[i] = p.next_w[at(i)];
-  }
-  float a = p.scale;
-  if (p.gate_kind == MOE_GATE_TOKEN) a *= static_cast<const float*>(p.gate)[t];
-  if (p.post_w) {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < CH; ++i)
-#pragma unroll
-      for (int e = 0; e < N; ++e) ss = fmaf(v[i][e], v[i][e], ss);
-    const float r = 1.0f / sqrtf(row_sum<W>(ss, s_one) * p.inv_h + p.eps);
-    if (p.rstd && l == 0) p.rstd[t] = r;
+        for (int i = 0; i < CH; ++i)
+          if (at(i) < p.rc) p.y_out[t * p.rc + at(i)] = C::pack(v[i]);
+    }
+    // what the outputs need besides y, asked for before the sum over the row
+    u32x4_t res[CH], pw[CH], gt[CH], nw[CH];
+    const u32x4_t* gate = static_cast<const u32x4_t*>(p.gate);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       if (at(i) >= p.rc) continue;
-      float w[N];
-      C::unpack(pw[i], w);
-#pragma unroll
-      for (int e = 0; e < N; ++e) v[i][e] = v[i][e] * r * w[e];
+      if (p.res) res[i] = p.res[t * p.rc + at(i)];
+      if (p.post_w) pw[i] = p.post_w[at(i)];
+      if (p.gate_kind == MOE_GATE_CHANNEL) gt[i] = gate[at(i)];
+      if (p.gate_kind == MOE_GATE_FULL) gt[i] = gate[t * p.rc + at(i)];
+      if (p.next_w) nw[i] = p.next_w[at(i)];
     }
-  }
-  float ss = 0.f;
+    float a = p.scale;
+    if (p.gate_kind == MOE_GATE_TOKEN) a *= static_cast<const float*>(p.gate)[t];
+    if (p.post_w) {
+      float ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    if (at(i) >= p.rc) continue;
-    if (p.gate_kind == MOE_GATE_CHANNEL || p.gate_kind == MOE_GATE_FULL) {
-      float g[N];
-      C::unpack(gt[i], g);
+      for (int i = 0; i < CH; ++i)
 #pragma unroll
-      for (int e = 0; e < N; ++e) v[i][e] *= g[e];
+        for (int e = 0; e < N; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+      const float r = 1.0f / sqrtf(row_sum<W>(ss, s_one) * p.inv_h + p.eps);
+      if (p.rstd && l == 0) p.rstd[t] = r;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        if (at(i) >= p.rc) continue;
+        float w[N];
+        C::unpack(pw[i], w);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[i][e] = v[i][e] * r * w[e];
+      }
     }
-    float f[N];
-    if (p.res) {
-      C::unpack(res[i], f);
-    } else {
+    float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < N; ++e) f[e] = 0.f;
+    for (int i = 0; i < CH; ++i) {
+      if (at(i) >= p.rc) continue;
+      if (p.gate_kind == MOE_GATE_CHANNEL || p.gate_kind == MOE_GATE_FULL) {
+        float g[N];
+        C::unpack(gt[i], g);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[i][e] *= g[e];
+      }
+      float f[N];
+      if (p.res) {
+        C::unpack(res[i], f);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) f[e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        v[i][e] = fmaf(a, v[i][e], f[e]);
+        ss = fmaf(v[i][e], v[i][e], ss);
+      }
+      if (p.out) p.out[t * p.rc + at(i)] = C::pack(v[i]);
     }
+    if (p.next_w) {
+      const float r = 1.0f / sqrtf(row_sum<W>(ss, s_two) * p.inv_h + p.eps);
+      if (p.next_rstd && l == 0) p.next_rstd[t] = r;
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      v[i][e] = fmaf(a, v[i][e], f[e]);
-      ss = fmaf(v[i][e], v[i][e], ss);
+      for (int i = 0; i < CH; ++i) {
+        if (at(i) >= p.rc) continue;
+        float w[N];
+        C::unpack(nw[i], w);
+#pragma unroll
+        for (int e = 0; e < N; ++e) w[e] *= v[i][e] * r;
+        p.next_n[t * p.rc + at(i)] = C::pack(w);
+      }
     }
-    if (p.out) p.out[t * p.rc + at(i)] = C::pack(v[i]);
-  }
-  if (!p.next_w) return;
-  const float r = 1.0f / sqrtf(row_sum<W>(ss, s_two) * p.inv_h + p.eps);
-  if (p.next_rstd && l == 0) p.next_rstd[t] = r;
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    if (at(i) >= p.rc) continue;
-    float w[N];
-    C::unpack(nw[i], w);
-#pragma unroll
-    for (int e = 0; e < N; ++e) w[e] *= v[i][e] * r;
-    p.next_n[t * p.rc + at(i)] = C::pack(w);
+    if constexpr (W > 1) __syncthreads();                     // the exchanges read by all before the next row's
   }
 }
 
-static moe_status launch_norm_out(const NormOutParams& p, bool bf16, bool gather, hipStream_t s) {
+static moe_status launch_norm_out(const NormOutParams& p, bool bf16, bool gather, hipStream_t s, int max_blocks = 0) {
   if (p.T == 0) return MOE_OK;
   with_row_shape(p.T, p.rc, [&](auto w, auto ch) {
     constexpr int W = decltype(w)::value, CH = decltype(ch)::value;
-    const dim3 grid(static_cast<unsigned>((p.T + RowShape<W>::ROWS - 1) / RowShape<W>::ROWS));
+    int64_t blocks = (p.T + RowShape<W>::ROWS - 1) / RowShape<W>::ROWS;
+    if (max_blocks > 0 && blocks > max_blocks) blocks = max_blocks;
+    const dim3 grid(static_cast<unsigned>(blocks));
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(RowShape<W>::THREADS), 0, s, p); };
     if (bf16)
       gather ? go(k_norm_out<true, W, CH, true>) : go(k_norm_out<true, W, CH, false>);
@@ -377,7 +384,7 @@ static moe_status norm_check_sizes(moe_dtype act, int64_t T, int32_t H) {
   if (act != MOE_F32 && act != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   const int64_t bytes = static_cast<int64_t>(H) * dtype_size(act);
   if (bytes % 16) return MOE_ERR_MISALIGNED;
-  if (bytes / 16 > kRowMaxChunks) return MOE_ERR_UNSUPPORTED;
+  if (bytes > kRowMaxBytes) return MOE_ERR_UNSUPPORTED;
   if (T >= (int64_t{1} << 22)) return MOE_ERR_UNSUPPORTED;          // 1024 threads a row, 2^32 in a grid
   return MOE_OK;
 }
@@ -434,7 +441,7 @@ moe_status launch_combine_post_norm(const CombineArgs& a, const void* res, const
   p.rstd = rstd;
   p.next_n = static_cast<u32x4_t*>(next_n);
   p.next_rstd = next_rstd;
-  return launch_norm_out(p, a.act == MOE_BF16, true, s);
+  return launch_norm_out(p, a.act == MOE_BF16, true, s, a.max_blocks);
 }
 
 }  // namespace dbomoe

@@ -11,7 +11,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
-from .device_layer import concat_shared, _dev
+from .device_layer import block_of, concat_shared, _dev
 
 
 class TrainLayer:
@@ -39,13 +39,25 @@ class TrainLayer:
     checks that a backward() came before it, and an eager backward() takes the
     tokens of the last forward() that was not a replay.
 
+    inp may hold "block", as for DeviceLayer: the layer is then x + scale * gate *
+    norm(layer(norm(x))), and pre_norm, post_norm and gate [H] are weights like the
+    others (names "pre_norm", "post_norm", "gate"; their gradients are float32 and
+    they do not decay).
+
+    Balance of the experts: inp["select_bias"] [E] float32 is added to the scores
+    when experts are chosen; bias_rate > 0: step() moves it by bias_rate towards the
+    experts that got fewer tokens than the mean since the last step (starting from
+    zeros if it was not given); balance_coef > 0: backward() adds the gradient of the
+    balance loss of its tokens, and balance_loss [1] holds that loss.  `load` [E]
+    counts the tokens of the last forward() by expert.  Not with forced ids.
+
     With a share of the experts (cfg.expert_begin, expert_end) out, dx and the
     router's gradient are this share's part, to be summed over the shares; give the
     shared experts to one share only, or their part is counted more than once.
     """
 
     def __init__(self, inp: dict, device: str = "cuda", T_max: int = None, grad_dtype=torch.float32,
-                 states: str = "f32", master: bool = True, **hyper):
+                 states: str = "f32", master: bool = True, balance_coef: float = 0.0, bias_rate: float = 0.0, **hyper):
         cfg = inp["cfg"]
         d = torch.device(device)
         if d.type == "cuda" and d.index is None:
@@ -77,6 +89,25 @@ class TrainLayer:
         if shI:
             self.weights["shared_w13"] = own("shared_w13", sh13, 2 * shI, H)[None]
             self.weights["shared_w2"] = own("shared_w2", sh2, H, shI)[None]
+        self.block = block_of(inp, act, H)
+        self.n_decay = len(self.weights)      # what follows is not decayed
+        if self.block is not None:
+            for name in ("pre_norm", "post_norm", "gate"):
+                if self.block[name] is not None:
+                    self.weights[name] = own(name, self.block[name], H)
+        if not (balance_coef >= 0.0 and bias_rate >= 0.0):
+            raise ValueError("balance_coef and bias_rate: not negative")
+        self.balance_coef, self.bias_rate = balance_coef, bias_rate
+        self.select_bias = inp.get("select_bias")
+        if self.select_bias is not None:
+            if self.select_bias.dtype != torch.float32 or self.select_bias.shape != (cfg.E,):
+                raise ValueError(f"select_bias: float32 [{cfg.E}]")
+            self.select_bias = self.select_bias.contiguous().to(d, copy=True)
+        elif bias_rate > 0:
+            self.select_bias = torch.zeros(cfg.E, device=d)
+        self.balanced = self.select_bias is not None or balance_coef > 0
+        if self.balanced and self.forced_ids is not None:
+            raise ValueError("forced_ids: not with a selection bias or a balance loss")
         self.route = B.route_params(cfg.E, cfg.k, cfg.score, cfg.renormalize, cfg.n_groups, cfg.topk_groups,
                                     cfg.group_topn, cfg.routed_scale)
 
@@ -92,11 +123,21 @@ class TrainLayer:
         self.ones = torch.ones(T, k, device=d)
         if shI:
             self.buf.update(sh_gu=new(T, 2 * shI), sh_h=new(T, shI), sh_out=new(T, H), sh_dgu=new(T, 2 * shI))
+        if self.balanced:
+            self.load, self.load_sum = (torch.zeros(E, dtype=i32, device=d) for _ in range(2))
+            self.balance_loss = torch.zeros(1, device=d)
+            self.ws_balance = new(B.moe_route_balance_loss_workspace_size(T, E), dt=torch.uint8)
+        if self.block is not None:
+            self.buf.update(xn=new(T, H), y=new(T, H), dy_block=new(T, H), rstd_pre=new(T, dt=f32), rstd_post=new(T, dt=f32),
+                            dx_block=new(T, H))
+            self.ws_norm = new(B.moe_norm_backward_workspace_size(T, H), dt=torch.uint8)
         self.ws_route = new(max(B.moe_route_workspace_size(T, H, E), 256), dt=torch.uint8)
         self.ws_dispatch = new(max(B.moe_dispatch_workspace_size(T, k, E_loc), 256), dt=torch.uint8)
         self.ws_gemm = new(B.GEMM_MAX_WORKSPACE, dt=torch.uint8)      # whatever the number of tokens
 
-        self.grads = {name: torch.zeros(w.shape, dtype=grad_dtype, device=d) for name, w in self.weights.items()}
+        names = list(self.weights)
+        self.grads = {name: torch.zeros(w.shape, dtype=grad_dtype if name in names[:self.n_decay] else f32, device=d)
+                      for name, w in self.weights.items()}
         self.fresh = True                     # the gradients are zero
         self.captured = False                 # calls were captured: `fresh` says nothing any more
         ws = list(self.weights.values())
@@ -108,9 +149,17 @@ class TrainLayer:
         else:
             self.m, self.v = ([torch.zeros(w.numel(), device=d) for w in ws] for _ in range(2))
             self.m_scale = self.v_scale = None
-        self.table = B.moe_adamw_table(ws, list(self.grads.values()), self.m, self.v, self.m_scale, self.v_scale,
-                                       self.master)
+        gs, n = list(self.grads.values()), self.n_decay
+
+        def table(part):
+            cols = (ws, gs, self.m, self.v, self.m_scale, self.v_scale, self.master)
+            return B.moe_adamw_table(*(None if c is None else c[part] for c in cols))
+
+        self.table = table(slice(0, n))
         self.hyper = B.adamw_params(**hyper)
+        self.norm_table = table(slice(n, None)) if len(ws) > n else None
+        # (another seed: the tables number their tensors from 0 each)
+        self.norm_hyper = B.adamw_params(**{**hyper, "weight_decay": 0.0, "seed": hyper.get("seed", 0) ^ 0x5bd1e995})
         self.steps = torch.zeros(1, dtype=i32, device=d)
         self.T = 0
 
@@ -121,7 +170,8 @@ class TrainLayer:
     def _rows(self, *names):
         """The parts of the buffers that a call of self.T tokens uses."""
         T, n = self.T, self.T * self.cfg.k
-        per_token = {"logits", "ids", "w", "out", "dw", "dlogits", "dx_dense", "dx", "sh_gu", "sh_h", "sh_out", "sh_dgu"}
+        per_token = {"logits", "ids", "w", "out", "dw", "dlogits", "dx_dense", "dx", "sh_gu", "sh_h", "sh_out", "sh_dgu",
+                     "xn", "y", "dy_block", "rstd_pre", "rstd_post", "dx_block"}
         return [self.buf[s][:T if s in per_token else n] for s in names]
 
     def forward(self, x, forced_ids=None):
@@ -134,6 +184,8 @@ class TrainLayer:
         if forced is not None and (forced.dtype != torch.int32 or forced.dim() != 2 or forced.shape[0] < x.shape[0] or
                                    forced.shape[1] != cfg.k or forced.device != self.device):
             raise ValueError(f"forced_ids: int32 [{x.shape[0]}, {cfg.k}] on {self.device}")
+        if forced is not None and self.balanced:
+            raise ValueError("forced_ids: not with a selection bias or a balance loss")
         self.T, self.x = x.shape[0], x
         try:
             with torch.cuda.device(self.device):
@@ -146,8 +198,16 @@ class TrainLayer:
         cfg, W = self.cfg, self.weights
         logits, ids, w, perm, inv, x_perm, gu, h, y_perm, out = self._rows(
             "logits", "ids", "w", "perm", "inv", "x_perm", "gu", "h", "y_perm", "out")
-        B.moe_route_topk(x, W["w_router"], self.route, ids, w, self.ws_route, logits_out=logits,
-                         logit_bias=self.logit_bias, forced_ids=forced)
+        x = self._normed(x, True)
+        if self.balanced:
+            self.load.zero_()
+            B.moe_route_balanced(x, W["w_router"], self.route, ids, w, self.ws_route, select_bias=self.select_bias,
+                                 load=self.load, logits_out=logits, logit_bias=self.logit_bias)
+            if self.bias_rate > 0:
+                self.load_sum.add_(self.load)
+        else:
+            B.moe_route_topk(x, W["w_router"], self.route, ids, w, self.ws_route, logits_out=logits,
+                             logit_bias=self.logit_bias, forced_ids=forced)
         B.moe_dispatch(x, ids, cfg.E, cfg.expert_begin, cfg.expert_end, self.buf["counts"], self.offsets, perm, inv,
                        x_perm, self.ws_dispatch)
         B.moe_grouped_swiglu(x_perm, W["w13"], self.offsets, h, gu=gu)
@@ -157,8 +217,23 @@ class TrainLayer:
             sh_gu, sh_h, shared = self._rows("sh_gu", "sh_h", "sh_out")
             B.moe_grouped_swiglu(x, W["shared_w13"], None, sh_h, gu=sh_gu)
             self._gemm("nt", sh_h, W["shared_w2"], None, shared)
-        B.moe_combine(y_perm, self.T, cfg.k, inv, w, out, shared_out=shared)
+        if self.block is None:
+            B.moe_combine(y_perm, self.T, cfg.k, inv, w, out, shared_out=shared)
+        else:
+            b, (y, rstd) = self.block, self._rows("y", "rstd_post")
+            B.moe_combine_post_norm(y_perm, inv, w, self.x if b["residual"] else None, out, b["eps"], W.get("post_norm"),
+                                    W.get("gate"), b["scale"], shared_out=shared, y_out=y,
+                                    rstd=rstd if "post_norm" in W else None)
         return out
+
+    def _normed(self, x, compute=False):
+        """What the layer computes from: x, or its norm."""
+        if "pre_norm" not in self.weights:
+            return x
+        xn, rstd = self._rows("xn", "rstd_pre")
+        if compute:
+            B.moe_pre_norm(x, self.weights["pre_norm"], xn, self.block["eps"], rstd=rstd)
+        return xn
 
     def backward(self, dout):
         if self.T == 0:
@@ -173,24 +248,46 @@ class TrainLayer:
         logits, ids, w, inv, x_perm, gu, h, y_perm, dy, dw, dgu, dx_perm, dlogits, dx_dense, dx = self._rows(
             "logits", "ids", "w", "inv", "x_perm", "gu", "h", "y_perm", "dy_perm", "dw", "dgu", "dx_perm", "dlogits",
             "dx_dense", "dx")
-        off = self.offsets
+        off, x, dblock = self.offsets, self._normed(self.x), dout
+        if self.block is not None:
+            y, dout, rstd = self._rows("y", "dy_block", "rstd_post")
+            B.moe_post_norm_backward(dblock, y, dout, self.ws_norm, rstd if "post_norm" in W else None, W.get("post_norm"),
+                                     G.get("post_norm"), W.get("gate"), G.get("gate"), self.block["scale"], more)
         B.moe_combine_backward(dout, y_perm, inv, w, dy, dw)
         self._gemm("tn", dy, h, off, G["w2"], more)
         B.moe_grouped_swiglu_backward(dy, W["w2"], gu, off, dgu)
         self._gemm("tn", dgu, x_perm, off, G["w13"], more)
         self._gemm("nn", dgu, W["w13"], off, dx_perm)
         B.moe_route_backward(logits, ids, dw, self.route, dlogits)
-        self._gemm("tn", dlogits, self.x, None, G["w_router"], more)
+        if self.balance_coef > 0:
+            B.moe_route_balance_loss(logits, self.load, self.route, self.balance_coef, self.balance_loss, dlogits,
+                                     self.ws_balance, accumulate=True)
+        self._gemm("tn", dlogits, x, None, G["w_router"], more)
         self._gemm("nn", dlogits, W["w_router"], None, dx_dense)
         if "shared_w13" in W:
             sh_gu, sh_h, sh_dgu = self._rows("sh_gu", "sh_h", "sh_dgu")
             self._gemm("tn", dout, sh_h, None, G["shared_w2"], more)
             B.moe_grouped_swiglu_backward(dout, W["shared_w2"], sh_gu, None, sh_dgu)
-            self._gemm("tn", sh_dgu, self.x, None, G["shared_w13"], more)
+            self._gemm("tn", sh_dgu, x, None, G["shared_w13"], more)
             self._gemm("nn", sh_dgu, W["shared_w13"], None, dx_dense, True)
         B.moe_combine(dx_perm, self.T, self.cfg.k, inv, self.ones[:self.T], dx, shared_out=dx_dense)
+        if self.block is not None:
+            dx = self._block_dx(dx, dblock if self.block["residual"] else None, more)
         self.fresh = False
         return dx
+
+    def _block_dx(self, dxn, dres, more):
+        """The gradient of x from that of what the layer computed from, and the residual's."""
+        W = self.weights
+        out, rstd = self._rows("dx_block", "rstd_pre")
+        if "pre_norm" in W:
+            B.moe_pre_norm_backward(dxn, self.x, rstd, W["pre_norm"], out, self.grads["pre_norm"], self.ws_norm, dres=dres,
+                                    accumulate=more)
+        elif dres is not None:
+            B.moe_post_norm(dxn, dres, out, self.block["eps"])       # their sum
+        else:
+            return dxn
+        return out
 
     def _captured(self):
         self.captured = self.captured or torch.cuda.is_current_stream_capturing()
@@ -210,8 +307,12 @@ class TrainLayer:
         self.steps.add_(1)
         try:
             B.moe_adamw_step(self.table, self.hyper, self.steps, lr_scale=lr_scale, grad_scale=grad_scale)
+            if self.norm_table is not None:
+                B.moe_adamw_step(self.norm_table, self.norm_hyper, self.steps, lr_scale=lr_scale, grad_scale=grad_scale)
         except Exception:
             self.steps.sub_(1)                # refused: no update has been made
             raise
+        if self.bias_rate > 0:
+            B.moe_route_bias_update(self.select_bias, self.load_sum, self.bias_rate)
         self.zero_grad()
         self.T = 0                            # the weights are no longer those of the last forward pass

@@ -589,10 +589,24 @@ moe_status moe_post_norm_backward(const void* dout, const void* y, moe_dtype act
 /* ---------------------------------------------------------------------------
  * dbo_moe_layer - the whole layer under Dual-Batch Overlap.
  * ------------------------------------------------------------------------- */
+/* The layer as a block of a model:
+ *   n = x r(x) pre_w (pre_w NULL: n = x);  y = the layer of n;
+ *   out = (residual ? x : 0) + scale * g * (y r(y) post_w)
+ * as moe_pre_norm and moe_combine_post_norm compute them; post.next_w must be NULL,
+ * post.eps is the eps of both norms. */
+typedef struct {
+  const void* pre_w;            /* [H] act or NULL */
+  moe_post_norm_params post;    /* gates per token and full ones: of all T tokens */
+  int32_t residual;             /* 0 or 1 */
+} moe_block_params;
+
 typedef struct {
   int32_t H, I;                 /* hidden size; intermediate size per routed expert */
   moe_dtype act;                /* activations and router weights: MOE_F32 or MOE_BF16 */
-  moe_dtype wdt;                /* routed expert weights (see moe_grouped_ffn) */
+  moe_dtype wdt;                /* routed expert weights (see moe_grouped_ffn), or MOE_INT8
+                                   (act MOE_BF16, w13_scale [E_loc, 2I], w2_scale [E_loc, H]:
+                                   moe_dispatch_int8 and moe_grouped_ffn_int8; ffn_tile_m is
+                                   not used; the shared experts keep act) */
   moe_route_params route;
   int32_t expert_begin;         /* local experts [expert_begin, expert_end) */
   int32_t expert_end;
@@ -615,6 +629,9 @@ typedef struct {
                                    moe_grouped_ffn_fp8 (row tiles 64 or 128: ffn_tile_m
                                    0, 64 or 128, else MOE_ERR_UNSUPPORTED).  The shared
                                    experts keep act. */
+  const float* select_bias;     /* [E] fp32 or NULL.  Given: experts are chosen as
+                                   moe_route_balanced does (forced ids come first, as ever) */
+  const moe_block_params* block; /* NULL: the layer by itself */
 } moe_layer_desc;
 
 typedef enum {

@@ -239,3 +239,48 @@ def test_binding_refuses_what_does_not_belong_together():
         with pytest.raises(ValueError):
             c()
             print("accepted:", n)
+
+
+def test_layer_description_refusals():
+    """dbo_moe_layer's integer experts, selection bias and block."""
+    B = _B()
+
+    def size(block=None, post=None, **kw):
+        d = B.moe_layer_desc(2048, 1408, B.MOE_BF16, B.MOE_INT8, B.route_params(64, 6), 0, 64, 256, 512, 768, 1024, 1280, 0, None, None)
+        for k, v in kw.items():
+            setattr(d, k, v)
+        if block is not None or post is not None:
+            q = B.moe_post_norm_params(256, 256, 1, 1.0, 1e-6, None)
+            for k, v in (post or {}).items():
+                setattr(q, k, v)
+            b = B.moe_block_params(256, q, 1)
+            for k, v in (block or {}).items():
+                setattr(b, k, v)
+            d.block = ctypes.pointer(b)
+        return B.moe_layer_workspace_size(d, 64)
+
+    n = size()
+    assert n > 0 and size(select_bias=256) == n
+    assert size(block={}) == n + 2 * 64 * 2048 * 2                     # the norm of each microbatch's tokens
+    assert size(block=dict(pre_w=None)) == n
+    for kw in (dict(act=B.MOE_F32), dict(H=2048 + 64), dict(I=1400), dict(w13_scale=None), dict(w2_scale=None), dict(fp8_act=1),
+               dict(select_bias=260), dict(w13_scale=1028)):
+        assert size(**kw) == 0, kw
+    for kw in (dict(block=dict(pre_w=260)), dict(block=dict(residual=2)), dict(post=dict(eps=0.0)), dict(post=dict(next_w=256)),
+               dict(post=dict(gate=None)), dict(post=dict(gate_kind=0)), dict(post=dict(gate_kind=4)), dict(post=dict(post_w=264))):
+        assert size(**kw) == 0, kw
+
+
+def test_block_entries_are_checked():
+    from combine_dual_overlap_amd.device_layer import block_of
+    from workloads import get_config
+    cfg = get_config(2, small=True)
+    w = torch.ones(cfg.H)
+    ok = block_of(dict(cfg=cfg, block=dict(pre_norm=w)), torch.float32, cfg.H)
+    assert ok["residual"] and ok["scale"] == 1.0 and ok["pre_norm"] is w and block_of(dict(cfg=cfg), torch.float32, cfg.H) is None
+    share = cfg.replace(expert_end=8)
+    for c, b in ((cfg, dict(norm=w)), (cfg, dict(pre_norm=w[:-1])), (cfg, dict(post_norm=w.bfloat16())), (cfg, dict(gate=w[None])),
+                 (share, dict(pre_norm=w)), (share, dict(post_norm=w, residual=False))):
+        with pytest.raises(ValueError):
+            block_of(dict(cfg=c, block=b), torch.float32, cfg.H)
+    assert block_of(dict(cfg=share, block=dict(pre_norm=w, residual=False)), torch.float32, cfg.H)
