@@ -164,230 +164,302 @@ struct I8Params {
   const float* bs;     // [E, N] (SwiGLU: [E, 2N])
 };
 
-// C = product (c_f32, or bf16), or with SwiGLU h = silu(gate) * up.  The tile of
-// the bf16 product (grouped_gemm.hip) for one reduction part: BM x BN, BK pairs
-// per stage, WAVES_M x WAVES_N (x WAVES_K halves of a stage) waves, a ring of
-// NBUF stages.
-template <int EPI, int BM, int BN, int BK, int WAVES_M, int WAVES_N, int WAVES_K, int NBUF, int TM>
-__device__ __forceinline__ void i8_tile(const I8Params& ip, const GgTile& t, uint8_t* lds) {
+// C = product (c_f32, or bf16), or with SwiGLU h = silu(gate) * up.
+//
+// A workgroup walks tiles BM x BN of its XCD's contiguous run of them, BK pairs of
+// integers per stage, in a ring of NBUF stages that runs on from one tile into the
+// next: the next tile's first stages are on their way while this one's results are
+// scaled and stored.
+//  - Every wave keeps the whole tile map (experts' rows and first tiles) in LDS.
+//  - The tile's scales come to LDS as its first stage does.
+//  - The second operand's rows are dealt to the MFMA's positions so that a lane ends
+//    up with 16 bytes of consecutive columns of its row and stores them as they are
+//    (64 bytes of a row by four lanes): position q of TG neighbouring subtiles is row
+//    (q / 4) 4 TG + 4 j + q % 4 of theirs, TG = 1 for fp32 and 2 for bf16.
+template <int EPI, bool F32, int BM, int BN, int WAVES_M, int WAVES_N, int NBUF>
+struct I8Shape {
+  static constexpr int BK = 64;                                 // pairs: 128 bytes of a row
+  static constexpr int NW = WAVES_M * WAVES_N;
+  static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 16, TN = WN / 16;
+  static constexpr int TH = EPI == EPI_SWIGLU ? TN / 2 : TN;    // subtiles of output columns
+  static constexpr int TG = F32 || TH == 1 ? 1 : 2;
+  static constexpr int STAGE = (BM + BN) * BK * 2;
+  static constexpr int NQA = BM / (8 * NW), NQB = BN / (8 * NW);  // DMAs per wave and stage: 8 rows each
+  static constexpr int NDMA = NQA + NQB;
+  static constexpr int SLOTS = 4;                               // tiles whose scales are in LDS: NBUF + 1 at most
+  static_assert(NQA * 8 * NW == BM && NQB * 8 * NW == BN && NW % 4 == 0, "DMA split");
+  static_assert((BM + 63) / 64 + BN / 64 <= NW && NBUF < SLOTS && (NBUF - 1) * NDMA < 64, "scales, ring, vmcnt");
+  // the XORs that rows put on their 16-byte chunks: the eight lanes that read together
+  // hit rows of both parities and four keys
+  static __device__ __forceinline__ int key_a(int r) { return r & 7; }
+  static __device__ __forceinline__ int key_b(int r) { return (r >> 1 & 1) | (r / (4 * TG) & 3) << 1; }
+};
+
+// The reciprocal is the hardware's, one unit in the last place off: an IEEE division
+// made the SwiGLU epilogue 4 % of the whole product longer.
+__device__ __forceinline__ float silu(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+
+struct I8Tile {
+  int e, m_n, nt, tm;
+  int64_t row;             // first row of the tile
+};
+
+template <int EPI, bool F32, int BM, int BN, int WAVES_M, int WAVES_N, int NBUF>
+__global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Params ip) {
+  using S = I8Shape<EPI, F32, BM, BN, WAVES_M, WAVES_N, NBUF>;
+  constexpr int BK = S::BK, NW = S::NW, WM = S::WM, WN = S::WN, TM = S::TM, TN = S::TN, TH = S::TH, TG = S::TG;
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[NBUF * S::STAGE];
+  __shared__ float s_scale[S::SLOTS][BM + BN];
+  __shared__ __attribute__((aligned(16))) int s_first[256];     // the expert's first tile
+  __shared__ int s_row0[256], s_rows[256];
   const GgParams& p = ip.g;
-  constexpr int NW = WAVES_M * WAVES_N * WAVES_K;
-  constexpr int WM = TM * 16, WN = BN / WAVES_N, TN = WN / 16;
-  using OpA = Operand<true, BM, BK, NW, TM * 16 * WAVES_M>;
-  using OpB = Operand<true, BN, BK, NW>;
-  constexpr int NDMA = OpA::NQ + OpB::NQ, STAGE = OpA::BYTES + OpB::BYTES;
-  static_assert((NBUF - 1) * NDMA < 64, "vmcnt");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wk = wave / (WAVES_M * WAVES_N), wm = wave / WAVES_N % WAVES_M, wn = wave % WAVES_N;
-  const int KT = (p.K + BK - 1) / BK;
+  const int wm = wave / WAVES_N, wn = wave % WAVES_N;
 
-  OpA a;
-  OpB b;
-  a.init(static_cast<const bf16_t*>(p.A) + (t.row0 + t.m_off) * p.K, p.K, 0, 0,
-         [&](int r) { return min(r, t.rows - 1 - t.m_off); });
+  if (threadIdx.x < kWave) {
+    int t4[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int o = 0, n = 0;
+      if (lane * 4 + i < p.E) gg_rows(p, lane * 4 + i, o, n);
+      s_row0[lane * 4 + i] = o;
+      s_rows[lane * 4 + i] = n;
+      t4[i] = (n + BM - 1) / BM * p.n_tiles;
+      sum += t4[i];
+    }
+    int at = wave_incl_scan(sum) - sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s_first[lane * 4 + i] = at;
+      at += t4[i];
+    }
+    if (lane == 63) s_scale[0][0] = __int_as_float(at);         // all tiles
+  }
+  __syncthreads();
+  const int R = __builtin_amdgcn_readfirstlane(__float_as_int(s_scale[0][0]));
+  __syncthreads();
+  // Workgroup b runs on XCD b % 8, which walks a contiguous run of tiles.
+  const int per = (R + 7) / 8, xcd = blockIdx.x & 7, step = gridDim.x >> 3;
+  const int stop = min((xcd + 1) * per, R);
+  const int L0 = xcd * per + (blockIdx.x >> 3);
+  if (L0 >= stop) return;
+  auto locate = [&](int L) {
+    const int4 f = reinterpret_cast<const int4*>(s_first)[lane];
+    const int e = __popcll(__ballot(f.x <= L)) + __popcll(__ballot(f.y <= L)) + __popcll(__ballot(f.z <= L)) +
+                  __popcll(__ballot(f.w <= L)) - 1;             // the last expert that starts at L or before
+    const int rows = __builtin_amdgcn_readfirstlane(s_rows[e]);
+    const int l = L - __builtin_amdgcn_readfirstlane(s_first[e]);
+    const int tiles = (rows + BM - 1) / BM;
+    // bands of eight row tiles: what runs together on an XCD is about as high as wide
+    const int band = l / (8 * p.n_tiles), r = l - band * 8 * p.n_tiles, high = min(8, tiles - 8 * band);
+    // the expert's rows in tiles of equal height (a multiple of 32 where tiles are higher than that)
+    const int height = BM <= 32 ? BM : ((rows + tiles - 1) / tiles + 31) / 32 * 32;
+    const int m_off = (8 * band + r % high) * height;
+    I8Tile t;
+    t.e = __builtin_amdgcn_readfirstlane(e);
+    t.nt = __builtin_amdgcn_readfirstlane(r / high);
+    t.m_n = __builtin_amdgcn_readfirstlane(min(height, rows - m_off));
+    t.row = __builtin_amdgcn_readfirstlane(s_row0[e] + m_off);
+    t.tm = __builtin_amdgcn_readfirstlane(min(TM, max(0, (t.m_n - wm * WM + 15) / 16)));
+    return t;
+  };
+
+  // ---- loads: the tile whose stages are being asked for runs ahead of the one computed
+  const int KT = (p.K + BK - 1) / BK;
   const int brows = EPI == EPI_SWIGLU ? 2 * p.N : p.N;
-  const bf16_t* B = static_cast<const bf16_t*>(p.B) + static_cast<int64_t>(t.e) * brows * p.K;
-  if constexpr (EPI == EPI_SWIGLU)       // half a tile of gate rows, then the matching up rows
-    b.init(B + static_cast<int64_t>(t.nt * (BN / 2)) * p.K, p.K, 0, 0, [&](int r) {
-      return min(r % (BN / 2), p.N - 1 - t.nt * (BN / 2)) + (r < BN / 2 ? 0 : p.N);
-    });
-  else
-    b.init(B + static_cast<int64_t>(t.nt * BN) * p.K, p.K, 0, 0, [&](int r) { return min(r, p.N - 1 - t.nt * BN); });
   const uint32_t lds0 = static_cast<uint32_t>(
-      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)(lds)));
-  __builtin_amdgcn_s_waitcnt(0);           // from here on only counted DMAs are in flight
-  auto issue = [&](int kt) {
-    const uint32_t at = lds0 + (kt % NBUF) * STAGE;
-    const int left = p.K - kt * BK;
-    if (left >= BK) {
-      a.issue(at, kt);
-      b.issue(at + OpA::BYTES, kt);
-    } else {
-      a.issue_tail(at, kt, left);
-      b.issue_tail(at + OpA::BYTES, kt, left);
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)(ring)));
+  const uint32_t lds_scale = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) float*)(&s_scale[0][0])));
+  const int64_t row_bytes = static_cast<int64_t>(p.K) * 2;
+  const uint8_t *a_base, *b_base;                    // uniform
+  uint32_t a_off[S::NQA], b_off[S::NQB];             // this lane's chunks
+  int L_in = L0, kt_in = 0, issued = 0, tile_in = 0;
+  // A DMA takes eight rows: lane l the row l / 8 of them and chunk (l % 8) ^ key, a key
+  // that does not depend on which of the wave's DMAs it is.
+  const int lr = lane >> 3, pos = lane & 7;
+  const int chunk_a = pos ^ S::key_a(lr), chunk_b = pos ^ S::key_b(8 * wave + lr);
+  auto open_tile = [&](int L) {
+    const I8Tile t = locate(L);
+    a_base = static_cast<const uint8_t*>(p.A) + t.row * row_bytes;
+    const int m_last = t.m_n - 1;                    // rows and columns behind the last are its copies
+#pragma unroll
+    for (int i = 0; i < S::NQA; ++i)
+      a_off[i] = min(8 * (i * NW + wave) + lr, m_last) * static_cast<uint32_t>(row_bytes) + chunk_a * 16;
+    const int col0 = t.nt * (EPI == EPI_SWIGLU ? BN / 2 : BN);
+    const int n_last = p.N - 1 - col0;
+    // row of b of row x of the tile (SwiGLU: half a tile of gate rows, then the matching up rows)
+    auto row_of = [&](int x) {
+      return EPI == EPI_SWIGLU ? min(x & (BN / 2 - 1), n_last) + (x < BN / 2 ? 0 : p.N) : min(x, n_last);
+    };
+#pragma unroll
+    for (int i = 0; i < S::NQB; ++i)
+      b_off[i] = row_of(8 * (i * NW + wave) + lr) * static_cast<uint32_t>(row_bytes) + chunk_b * 16;
+    b_base = static_cast<const uint8_t*>(p.B) + (static_cast<int64_t>(t.e) * brows + col0) * row_bytes;
+    // the scales: 64 rows or columns by each wave
+    constexpr int WA = (BM + 63) / 64;
+    const uint32_t at = lds_scale + (tile_in % S::SLOTS) * (BM + BN) * 4;
+    if (wave < WA) {
+      const int r = wave * 64 + lane;
+      if (r < BM) lds_dma4(at + wave * 256, ip.as + t.row + min(r, m_last));
+    } else if (wave < WA + BN / 64) {
+      const int c = (wave - WA) * 64;
+      lds_dma4(at + BM * 4 + c * 4, ip.bs + static_cast<int64_t>(t.e) * brows + col0 + row_of(c + lane));
     }
   };
+  auto issue = [&]() {
+    if (kt_in == KT) {
+      L_in += step;
+      kt_in = 0;
+      ++tile_in;
+    }
+    if (L_in >= stop) return;
+    if (kt_in == 0) open_tile(L_in);
+    const uint32_t at = lds0 + (issued % NBUF) * S::STAGE + wave * 1024;
+    const int left = p.K - kt_in * BK;
+    const uint8_t *as = a_base + kt_in * (BK * 2), *bs = b_base + kt_in * (BK * 2);
+    if (left >= BK) {
+#pragma unroll
+      for (int i = 0; i < S::NQA; ++i) lds_dma16_at(at + i * NW * 1024, as, a_off[i]);
+#pragma unroll
+      for (int i = 0; i < S::NQB; ++i) lds_dma16_at(at + BM * 128 + i * NW * 1024, bs, b_off[i]);
+    } else {                                         // the reduction ends inside the stage: zeros behind it
+#pragma unroll
+      for (int i = 0; i < S::NQA; ++i)
+        lds_dma16(at + i * NW * 1024, chunk_a * 8 < left ? static_cast<const void*>(as + a_off[i]) : g_zero16);
+#pragma unroll
+      for (int i = 0; i < S::NQB; ++i)
+        lds_dma16(at + BM * 128 + i * NW * 1024, chunk_b * 8 < left ? static_cast<const void*>(bs + b_off[i]) : g_zero16);
+    }
+    ++kt_in;
+    ++issued;
+  };
 
-  // Accumulators hold C transposed: lane l has row l & 15 and the four columns
-  // 4 * (l >> 4) .. + 3 of each 16 x 16 tile.
-  i32x4_t acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
-  auto b_pos = [&](int tn) {
-    if constexpr (EPI == EPI_SWIGLU)
-      return tn < TN / 2 ? wn * (WN / 2) + tn * 16 : BN / 2 + wn * (WN / 2) + (tn - TN / 2) * 16;
-    else
-      return wn * WN + tn * 16;
+  // ---- products.  Accumulators hold C transposed: lane l has row l & 15 and four
+  // positions 4 (l >> 4) .. + 3 of each 16 x 16 subtile.
+  i32x4_t acc[TM][TN], af[TM], bfr[2][TN];
+  const int l15 = lane & 15, g = lane >> 4;
+  const int rb = (l15 >> 2) * (4 * TG) + (l15 & 3);
+  // first column of subtile j in the lane's own of the wave's, but for the lane's place among them
+  auto sub = [](int j) { return j / TG * (16 * TG) + j % TG * 4; };
+  auto frag = [&](const uint8_t* tile, int r, int key, int kk) {
+    return *reinterpret_cast<const i32x4_t*>(tile + r * (BK * 2) + (((kk * 4 + g) ^ key) << 4));
   };
-  constexpr int KK = BK / 32 / WAVES_K;              // steps of a stage that this wave takes
-  static_assert(KK % 2 == 0, "the second operand's sets in turn");
-  i32x4_t af[TM], bfr[2][TN];
-  auto at_a = [&](int kt) { return lds + (kt % NBUF) * STAGE; };
-  auto read_a = [&](int kt, int kk, int i) {
-    af[i] = __builtin_bit_cast(i32x4_t, OpA::frag(at_a(kt), wm * WM + i * 16, wk * KK + kk));
+  auto read_a = [&](int s, int kk, int i) {
+    const int r = wm * WM + i * 16 + l15;
+    af[i] = frag(ring + (s % NBUF) * S::STAGE, r, S::key_a(r), kk);
   };
-  auto read_b = [&](int kt, int kk, int set) {
+  auto read_b = [&](int s, int kk, int set) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-      bfr[set][j] = __builtin_bit_cast(i32x4_t, OpB::frag(at_a(kt) + OpA::BYTES, b_pos(j), wk * KK + kk));
+    for (int j = 0; j < TN; ++j) {
+      const int r = EPI == EPI_SWIGLU ? (j / TH) * (BN / 2) + wn * (WN / 2) + rb + sub(j % TH) : wn * WN + rb + sub(j);
+      bfr[set][j] = frag(ring + (s % NBUF) * S::STAGE + BM * BK * 2, r, S::key_b(r), kk);
+    }
   };
+  int tm = TM;
   auto mfmas = [&](int i, int set) {
+    if (i < tm) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bfr[set][j], af[i], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < TN; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bfr[set][j], af[i], acc[i][j], 0, 0, 0);
+    }
     __builtin_amdgcn_sched_barrier(0);
   };
-  // (The last stage reads a stage that does not exist: bytes of the ring that
-  // nothing uses.)
-  auto stage = [&](int kt) {
+  // The reduction advances in two steps of 32 pairs a stage.  A fragment of the first
+  // operand is read again, for the next step, as soon as this step's MFMAs have taken
+  // it, and the second operand's of the next step are read ahead into a second set.
+  // Half of the second step's MFMAs run before the barrier that hands the stage's
+  // buffer back; the DMAs that fill it again follow at once.  (Spread between the MFMAs
+  // behind it, they come late: 4 % slower.  After the last stage of all, bytes are read
+  // that nothing uses.)
+  auto stage = [&](int s) {
+    read_b(s, 1, 1);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int kk = 0; kk < KK; ++kk) {
-      const int set = kk & 1;
-      if (kk + 1 < KK) {
-        read_b(kt, kk + 1, set ^ 1);
-        __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < TM; ++i) {
+      mfmas(i, 0);
+      read_a(s, 1, i);
+    }
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          mfmas(i, set);
-          read_a(kt, kk + 1, i);
-        }
+    for (int i = 0; i < TM / 2; ++i) mfmas(i, 1);
+    // this wave's reads of the stage are done, and its DMAs of the next
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    wait_stages<S::NDMA, NBUF - 2>(issued - s - 2);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    issue();
+    read_b(s + 1, 0, 0);
+#pragma unroll
+    for (int i = 0; i < TM / 2; ++i) read_a(s + 1, 0, i);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = TM / 2; i < TM; ++i) {
+      mfmas(i, 1);
+      read_a(s + 1, 0, i);
+    }
+  };
+
+  __builtin_amdgcn_s_waitcnt(0);           // from here on only counted DMAs are in flight (and stores, which are younger)
+  for (int s = 0; s < NBUF; ++s) issue();
+  wait_stages<S::NDMA, NBUF - 1>(issued - 1);
+  __syncthreads();
+  read_b(0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < TM; ++i) read_a(0, 0, i);
+  int s = 0, tile = 0;
+#pragma unroll 1
+  for (int L = L0; L < stop; L += step, ++tile) {
+    const I8Tile t = locate(L);
+    tm = t.tm;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+#pragma unroll 1
+    for (int kt = 0; kt < KT; ++kt, ++s) stage(s);
+
+    // The sums become fp32 (a rounding of 2^-24), times the row's scale, times the channel's.
+    const float* sc = s_scale[tile % S::SLOTS];
+    const int c0 = (EPI == EPI_SWIGLU ? wn * (WN / 2) : wn * WN) + g * (4 * TG);
+    const int col = t.nt * (EPI == EPI_SWIGLU ? BN / 2 : BN) + c0;
+    f32x4_t bs[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      bs[j] = *reinterpret_cast<const f32x4_t*>(sc + BM + c0 + (EPI == EPI_SWIGLU ? (j / TH) * (BN / 2) : 0) + sub(j % TH));
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      if (i >= tm) break;
+      const int in = wm * WM + i * 16 + l15;
+      if (in >= t.m_n) continue;
+      const float as = sc[in];
+      f32x4_t v[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) v[j] = __builtin_convertvector(acc[i][j], f32x4_t) * as * bs[j];
+      if constexpr (EPI == EPI_SWIGLU) {
+#pragma unroll
+        for (int j = 0; j < TH; ++j)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) v[j][x] = silu(v[j][x]) * v[j + TH][x];
+      }
+      const int64_t at = (t.row + in) * p.N + col;
+      if constexpr (F32) {
+#pragma unroll
+        for (int j = 0; j < TH; ++j)
+          if (col + sub(j) < p.N) *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.C) + at + sub(j)) = v[j];
+      } else if constexpr (TG == 1) {
+        if (col < p.N)
+          *reinterpret_cast<uint2*>(static_cast<bf16_t*>(p.C) + at) = make_uint2(cvt_bf16x2(v[0][0], v[0][1]), cvt_bf16x2(v[0][2], v[0][3]));
       } else {
 #pragma unroll
-        for (int i = 0; i < TM / 2; ++i) mfmas(i, set);
-        // this wave's reads of the stage are done, and its DMAs of the next
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        wait_stages<NDMA, NBUF - 2>(min(KT - 1, kt + NBUF - 1) - (kt + 1));
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (kt + NBUF < KT) issue(kt + NBUF);
-        read_b(kt + 1, 0, set ^ 1);
-#pragma unroll
-        for (int i = 0; i < TM / 2; ++i) read_a(kt + 1, 0, i);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = TM / 2; i < TM; ++i) {
-          mfmas(i, set);
-          read_a(kt + 1, 0, i);
-        }
+        for (int j = 0; j < TH; j += 2)
+          if (col + sub(j) < p.N)
+            *reinterpret_cast<u32x4_t*>(static_cast<bf16_t*>(p.C) + at + sub(j)) =
+                u32x4_t{cvt_bf16x2(v[j][0], v[j][1]), cvt_bf16x2(v[j][2], v[j][3]), cvt_bf16x2(v[j + 1][0], v[j + 1][1]),
+                        cvt_bf16x2(v[j + 1][2], v[j + 1][3])};
       }
     }
-  };
-  {
-    const int pre = min(NBUF, KT);
-    for (int s = 0; s < pre; ++s) issue(s);
-    wait_stages<NDMA, NBUF - 1>(pre - 1);
-    __syncthreads();
-    read_b(0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) read_a(0, 0, i);
-#pragma unroll 1
-    for (int kt = 0; kt < KT; ++kt) stage(kt);
   }
-
-  // Epilogue: the wave turns 16 rows at a time through LDS so that each lane has
-  // eight columns of a row; the sums become fp32 there (a rounding of 2^-24) and
-  // take the row's scale, then the channel's.
-  constexpr int CH = WN / 4;                         // 16-byte chunks of a row
-  constexpr int OUT = EPI == EPI_SWIGLU ? WN / 16 : WN / 8;   // lanes per row
-  constexpr int HN = (16 * OUT + 63) / 64;           // passes of the wave over 16 rows
-  const int q = lane % OUT;
-  const int col = EPI == EPI_SWIGLU ? t.nt * (BN / 2) + wn * (WN / 2) + q * 8 : t.nt * BN + wn * WN + q * 8;
-  const bool col_ok = col < p.N;
-  f32x4_t s0{0.f, 0.f, 0.f, 0.f}, s1 = s0, u0 = s0, u1 = s0;
-  if (col_ok) {
-    const f32x4_t* bs = reinterpret_cast<const f32x4_t*>(ip.bs + static_cast<int64_t>(t.e) * brows + col);
-    s0 = bs[0];
-    s1 = bs[1];
-    if constexpr (EPI == EPI_SWIGLU) {
-      const f32x4_t* us = reinterpret_cast<const f32x4_t*>(ip.bs + static_cast<int64_t>(t.e) * brows + p.N + col);
-      u0 = us[0];
-      u1 = us[1];
-    }
-  }
-  __syncthreads();                                   // the ring is free
-  constexpr int JOIN = WAVES_K == 1 ? 0 : NW * TM * TN * 1024;
-  static_assert(JOIN + NW * 16 * WN * 4 <= NBUF * STAGE, "epilogue scratch");
-  auto mine = [&](int i) { return WAVES_K == 1 || (i & 1) == wk; };
-  if constexpr (WAVES_K == 2) {
-    i32x4_t* slot = reinterpret_cast<i32x4_t*>(lds);
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-      if (!mine(i))
-#pragma unroll
-        for (int j = 0; j < TN; ++j) slot[((wave * TM + i) * TN + j) * 64 + lane] = acc[i][j];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-      if (mine(i))
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] += slot[(((wave ^ (NW / 2)) * TM + i) * TN + j) * 64 + lane];
-  }
-  float* turn = reinterpret_cast<float*>(lds + JOIN) + wave * 16 * WN;
-  auto chunk = [&](int r, int c) { return reinterpret_cast<f32x4_t*>(turn + r * WN + ((c ^ (r & (CH - 1))) << 2)); };
-  auto store8_f32 = [&](int64_t at, const f32x4_t& v0, const f32x4_t& v1) {
-    f32x4_t* c = reinterpret_cast<f32x4_t*>(static_cast<float*>(p.C) + at);
-    c[0] = v0;
-    c[1] = v1;
-  };
-  auto store8_bf16 = [&](int64_t at, const f32x4_t& v0, const f32x4_t& v1) {
-    *reinterpret_cast<u32x4_t*>(static_cast<bf16_t*>(p.C) + at) =
-        u32x4_t{cvt_bf16x2(v0[0], v0[1]), cvt_bf16x2(v0[2], v0[3]), cvt_bf16x2(v1[0], v1[1]), cvt_bf16x2(v1[2], v1[3])};
-  };
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    if (!mine(i)) continue;
-#pragma unroll
-    for (int j = 0; j < TN; ++j) *chunk(lane & 15, j * 4 + (lane >> 4)) = __builtin_convertvector(acc[i][j], f32x4_t);
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
-    for (int h = 0; h < HN; ++h) {
-      const int r = (h * 64 + lane) / OUT, in = wm * WM + i * 16 + r;
-      if (r >= 16 || in >= t.m_n || !col_ok) continue;
-      const int64_t row = t.row0 + t.m_off + in;
-      const float as = ip.as[row];
-      f32x4_t v0 = *chunk(r, 2 * q) * as * s0, v1 = *chunk(r, 2 * q + 1) * as * s1;
-      if constexpr (EPI == EPI_SWIGLU) {
-        const f32x4_t w0 = *chunk(r, CH / 2 + 2 * q) * as * u0, w1 = *chunk(r, CH / 2 + 2 * q + 1) * as * u1;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          v0[x] = silu_f32(v0[x]) * w0[x];
-          v1[x] = silu_f32(v1[x]) * w1[x];
-        }
-      }
-      const int64_t at = row * p.N + col;
-      if (p.c_f32)
-        store8_f32(at, v0, v1);
-      else
-        store8_bf16(at, v0, v1);
-    }
-    __builtin_amdgcn_wave_barrier();
-  }
-}
-
-template <int EPI, int BM, int BN, int BK, int WAVES_M, int WAVES_N, int WAVES_K, int NBUF, int TM>
-__device__ __forceinline__ void i8_tile_of(int tm, const I8Params& p, const GgTile& t, uint8_t* lds) {
-  if constexpr (TM == 1) {
-    i8_tile<EPI, BM, BN, BK, WAVES_M, WAVES_N, WAVES_K, NBUF, 1>(p, t, lds);
-  } else {
-    if (tm == TM)
-      i8_tile<EPI, BM, BN, BK, WAVES_M, WAVES_N, WAVES_K, NBUF, TM>(p, t, lds);
-    else
-      i8_tile_of<EPI, BM, BN, BK, WAVES_M, WAVES_N, WAVES_K, NBUF, TM - 1>(tm, p, t, lds);
-  }
-}
-
-template <int EPI, int BM, int BN, int BK, int WAVES_M, int WAVES_N, int WAVES_K, int NBUF>
-__global__ __launch_bounds__(WAVES_M * WAVES_N * WAVES_K * 64, 2) void k_grouped_int8(I8Params p) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[NBUF * (BM + BN) * BK * 2];
-  GgTile t;
-  if (!gg_locate<MOE_GEMM_NT, BM>(p.g, reinterpret_cast<int*>(lds), t)) return;
-  i8_tile_of<EPI, BM, BN, BK, WAVES_M, WAVES_N, WAVES_K, NBUF, BM / WAVES_M / 16>(
-      (t.m_n + 16 * WAVES_M - 1) / (16 * WAVES_M), p, t, lds);
 }
 
 // ---- host -----------------------------------------------------------------------
@@ -405,22 +477,29 @@ static moe_status launch_int8(I8Params& p, hipStream_t s) {
     BM = 32;
   else if (rows > 128 && tiles(256, 256) >= 256)
     BM = BN = 256;
-  else if (tiles(64, 128) <= 128)
-    BM = 64;
   const int width = EPI == EPI_SWIGLU ? BN / 2 : BN;
   p.g.n_tiles = (p.g.N + width - 1) / width;
   p.g.splits = 1;
   const int64_t n = gemm_grid(tiles(BM, BN));
   if (n >= (1 << 23)) return MOE_ERR_UNSUPPORTED;      // at most 512 threads each, 2^32 in a grid
   const dim3 grid(static_cast<unsigned>(n));
-  if (BM == 256)
-    hipLaunchKernelGGL((k_grouped_int8<EPI, 256, 256, 64, 2, 4, 1, 2>), grid, dim3(512), 0, s, p);
-  else if (BM == 128)
-    hipLaunchKernelGGL((k_grouped_int8<EPI, 128, 128, 64, 2, 2, 1, 2>), grid, dim3(256), 0, s, p);
-  else if (BM == 64)
-    hipLaunchKernelGGL((k_grouped_int8<EPI, 64, 128, 128, 2, 2, 2, 3>), grid, dim3(512), 0, s, p);
+  auto go = [&](auto kernel, int threads, int per_cu) {
+    const int64_t most = 256 * per_cu;               // what runs at once
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(n < most ? n : most)), dim3(threads), 0, s, p);
+  };
+  auto pick = [&](auto f32) {
+    constexpr bool F32 = decltype(f32)::value;
+    if (BM == 256)
+      go(k_grouped_int8<EPI, F32, 256, 256, 2, 4, 2>, 512, 1);
+    else if (BM == 128)
+      go(k_grouped_int8<EPI, F32, 128, 128, 2, 2, 2>, 256, 2);
+    else
+      go(k_grouped_int8<EPI, F32, 32, 128, 1, 4, 3>, 256, 2);
+  };
+  if (p.g.c_f32)
+    pick(std::true_type{});
   else
-    hipLaunchKernelGGL((k_grouped_int8<EPI, 32, 128, 64, 1, 4, 1, 3>), grid, dim3(256), 0, s, p);
+    pick(std::false_type{});
   DBOMOE_CHECK_LAUNCH();
   return MOE_OK;
 }
