@@ -143,7 +143,8 @@ moe_status launch_quant_int8(const QuantInt8Args& a, hipStream_t s) {
       go(k_quant_int8<BF16, 16, 0>, 1, 1024);
       return;
     }
-    with_row_shape(a.T, rc, [&](auto w, auto ch) {
+    // (65536 rows of 256 bf16 chunks: 85 us with one wave each, 104 with four)
+    with_row_shape(a.T, rc, 256, [&](auto w, auto ch) {
       constexpr int W = decltype(w)::value;
       go(k_quant_int8<BF16, W, decltype(ch)::value>, RowShape<W>::ROWS, RowShape<W>::THREADS);
     });

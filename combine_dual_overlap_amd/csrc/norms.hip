@@ -37,7 +37,7 @@ struct NormOutParams {
 };
 
 // The sum of a token's expert rows and shared rows, four rows' loads in flight.
-template <bool BF16, int W, int CH>
+template <bool BF16, int W, int CH, bool STREAM>
 __device__ __forceinline__ void gather_sum(const NormOutParams& p, int64_t t, int l,
                                            float (&v)[CH][Chunk<BF16>::N]) {
   constexpr int N = Chunk<BF16>::N, G = CH == 1 ? 8 : 4;
@@ -69,7 +69,7 @@ __device__ __forceinline__ void gather_sum(const NormOutParams& p, int64_t t, in
         used |= 1u << g;
 #pragma unroll
         for (int i = 0; i < CH; ++i)
-          if (i * 64 * W + l < p.rc) c[g][i] = src[i * 64 * W + l];
+          if (i * 64 * W + l < p.rc) c[g][i] = load_chunk<STREAM>(src + i * 64 * W + l);
       }
     }
 #pragma unroll
@@ -87,7 +87,7 @@ __device__ __forceinline__ void gather_sum(const NormOutParams& p, int64_t t, in
   }
 }
 
-template <bool BF16, int W, int CH, bool GATHER>
+template <bool BF16, int W, int CH, bool GATHER, bool STREAM>
 __global__ __launch_bounds__(RowShape<W>::THREADS) void k_norm_out(NormOutParams p) {
   constexpr int N = Chunk<BF16>::N;
   using C = Chunk<BF16>;
@@ -98,11 +98,11 @@ __global__ __launch_bounds__(RowShape<W>::THREADS) void k_norm_out(NormOutParams
   for (int64_t t = first; t < p.T; t += static_cast<int64_t>(gridDim.x) * RowShape<W>::ROWS) {
     float v[CH][N];
     if constexpr (GATHER) {
-      gather_sum<BF16, W, CH>(p, t, l, v);
+      gather_sum<BF16, W, CH, STREAM>(p, t, l, v);
     } else {
 #pragma unroll
       for (int i = 0; i < CH; ++i)
-        C::unpack(at(i) < p.rc ? p.y[t * p.rc + at(i)] : u32x4_t{0, 0, 0, 0}, v[i]);
+        C::unpack(at(i) < p.rc ? load_chunk<STREAM>(p.y + t * p.rc + at(i)) : u32x4_t{0, 0, 0, 0}, v[i]);
     }
     if constexpr (GATHER) {
       if (p.y_out)
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(RowShape<W>::THREADS) void k_norm_out(NormOutParams
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       if (at(i) >= p.rc) continue;
-      if (p.res) res[i] = p.res[t * p.rc + at(i)];
+      if (p.res) res[i] = load_chunk<STREAM>(p.res + t * p.rc + at(i));
       if (p.post_w) pw[i] = p.post_w[at(i)];
       if (p.gate_kind == MOE_GATE_CHANNEL) gt[i] = gate[at(i)];
       if (p.gate_kind == MOE_GATE_FULL) gt[i] = gate[t * p.rc + at(i)];
@@ -182,18 +182,30 @@ __global__ __launch_bounds__(RowShape<W>::THREADS) void k_norm_out(NormOutParams
   }
 }
 
+// Rows are read past the caches where there are more than kStreamBytes of them: k = 8,
+// 8192 x 2048 76 -> 70 us, 2048 x 7168 80 -> 65; 2048 x 2048 (67 MB) 19 either way.
+constexpr int64_t kStreamBytes = int64_t{64} << 20;
+
+// Rows of 256 chunks are spread over four waves: 8192 x 2048, k = 8, with one wave
+// (217 registers) 89 us, with four 76; without a combine 31 and 26.  Rows of 128 the
+// other way round: 4096 x 1024, k = 8, 18 and 21.
 static moe_status launch_norm_out(const NormOutParams& p, bool bf16, bool gather, hipStream_t s, int max_blocks = 0) {
   if (p.T == 0) return MOE_OK;
-  with_row_shape(p.T, p.rc, [&](auto w, auto ch) {
+  const bool stream = p.T * (gather ? p.k + p.n_shared : 1) * p.rc * 16 > kStreamBytes;
+  with_row_shape(p.T, p.rc, 128, [&](auto w, auto ch) {
     constexpr int W = decltype(w)::value, CH = decltype(ch)::value;
     int64_t blocks = (p.T + RowShape<W>::ROWS - 1) / RowShape<W>::ROWS;
     if (max_blocks > 0 && blocks > max_blocks) blocks = max_blocks;
     const dim3 grid(static_cast<unsigned>(blocks));
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(RowShape<W>::THREADS), 0, s, p); };
+    auto of = [&](auto b, auto g) {
+      constexpr bool B = decltype(b)::value, G = decltype(g)::value;
+      stream ? go(k_norm_out<B, W, CH, G, true>) : go(k_norm_out<B, W, CH, G, false>);
+    };
     if (bf16)
-      gather ? go(k_norm_out<true, W, CH, true>) : go(k_norm_out<true, W, CH, false>);
+      gather ? of(std::true_type{}, std::true_type{}) : of(std::true_type{}, std::false_type{});
     else
-      gather ? go(k_norm_out<false, W, CH, true>) : go(k_norm_out<false, W, CH, false>);
+      gather ? of(std::false_type{}, std::true_type{}) : of(std::false_type{}, std::false_type{});
   });
   DBOMOE_CHECK_LAUNCH();
   return MOE_OK;
@@ -224,7 +236,10 @@ struct NormBwdParams {
   float* part;                 // [gridDim.x][H] or NULL
 };
 
-template <bool BF16, int W, int CH>
+// Rows and weights stay packed as they were loaded and are taken apart twice (for
+// the sums over the row, then for dy): fp32 copies of them would leave two waves to a
+// SIMD.
+template <bool BF16, int W, int CH, int GATE, bool STREAM>
 __global__ __launch_bounds__(RowShape<W>::THREADS) void k_norm_bwd(NormBwdParams p) {
   constexpr int N = Chunk<BF16>::N, ROWS = RowShape<W>::ROWS;
   using C = Chunk<BF16>;
@@ -233,76 +248,87 @@ __global__ __launch_bounds__(RowShape<W>::THREADS) void k_norm_bwd(NormBwdParams
   const int l = W == 1 ? threadIdx.x & 63 : threadIdx.x;
   const int sub = W == 1 ? threadIdx.x >> 6 : 0;
   auto at = [&](int i) { return i * 64 * W + l; };
-  float w[CH][N], g[CH][N], col[CH][N];
+  const u32x4_t* gate = static_cast<const u32x4_t*>(p.gate);
+  const uint32_t one = BF16 ? 0x3f803f80u : 0x3f800000u;
+  u32x4_t w[CH], g[GATE == MOE_GATE_CHANNEL ? CH : 1];
+  float col[CH][N];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const bool in = at(i) < p.rc;
+    w[i] = in && p.w ? p.w[at(i)] : u32x4_t{one, one, one, one};
+    if constexpr (GATE == MOE_GATE_CHANNEL) g[i] = in ? gate[at(i)] : u32x4_t{0, 0, 0, 0};
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      w[i][e] = g[i][e] = 1.f;
-      col[i][e] = 0.f;
-    }
-    if (in && p.w) C::unpack(p.w[at(i)], w[i]);
-    if (in && p.gate_kind == MOE_GATE_CHANNEL) C::unpack(static_cast<const u32x4_t*>(p.gate)[at(i)], g[i]);
+    for (int e = 0; e < N; ++e) col[i][e] = 0.f;
   }
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * ROWS + sub; t < p.T; t += static_cast<int64_t>(gridDim.x) * ROWS) {
-    u32x4_t dv[CH], yv[CH], rv[CH], gv[CH];
+    u32x4_t dv[CH], yv[CH], rv[CH], gv[GATE == MOE_GATE_FULL ? CH : 1];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      if (at(i) >= p.rc) {
-        dv[i] = yv[i] = u32x4_t{0, 0, 0, 0};
-        continue;
-      }
-      dv[i] = p.d[t * p.rc + at(i)];
-      yv[i] = p.y[t * p.rc + at(i)];
-      if (p.dres) rv[i] = p.dres[t * p.rc + at(i)];
-      if (p.gate_kind == MOE_GATE_FULL) gv[i] = static_cast<const u32x4_t*>(p.gate)[t * p.rc + at(i)];
+      dv[i] = yv[i] = rv[i] = u32x4_t{0, 0, 0, 0};
+      if constexpr (GATE == MOE_GATE_FULL) gv[i] = u32x4_t{0, 0, 0, 0};
+      if (at(i) >= p.rc) continue;
+      dv[i] = load_chunk<STREAM>(p.d + t * p.rc + at(i));
+      yv[i] = load_chunk<STREAM>(p.y + t * p.rc + at(i));
+      if (p.dres) rv[i] = load_chunk<STREAM>(p.dres + t * p.rc + at(i));
+      if constexpr (GATE == MOE_GATE_FULL) gv[i] = gate[t * p.rc + at(i)];
     }
     const float r = p.rstd ? p.rstd[t] : 1.f;
-    const float gt = p.gate_kind == MOE_GATE_TOKEN ? static_cast<const float*>(p.gate)[t] : 1.f;
-    float q[CH][N], yh[CH][N], dot = 0.f, tok = 0.f;
+    const float gt = GATE == MOE_GATE_TOKEN ? static_cast<const float*>(p.gate)[t] : 1.f;
+    // of chunk i: a = scale d, yh, the weights and the gate
+    auto take = [&](int i, float (&a)[N], float (&yh)[N], float (&wf)[N], float (&gf)[N]) {
+      C::unpack(dv[i], a);
+      C::unpack(yv[i], yh);
+      C::unpack(w[i], wf);
+      if constexpr (GATE == MOE_GATE_CHANNEL) C::unpack(g[i], gf);
+      if constexpr (GATE == MOE_GATE_FULL) C::unpack(gv[i], gf);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        a[e] *= p.scale;
+        yh[e] *= r;
+        if constexpr (GATE == MOE_GATE_NONE || GATE == MOE_GATE_TOKEN) gf[e] = gt;
+      }
+    };
+    float dot = 0.f, tok = 0.f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      C::unpack(dv[i], q[i]);
-      C::unpack(yv[i], yh[i]);
-      float gf[N];
-      if (p.gate_kind == MOE_GATE_FULL && at(i) < p.rc) {
-        C::unpack(gv[i], gf);
+      float a[N], yh[N], wf[N], gf[N];
+      take(i, a, yh, wf, gf);
+      if constexpr (GATE == MOE_GATE_FULL) {
         float dg[N];
 #pragma unroll
-        for (int e = 0; e < N; ++e) dg[e] = p.scale * q[i][e] * (yh[i][e] * r) * w[i][e];
-        if (p.dgate) static_cast<u32x4_t*>(p.dgate)[t * p.rc + at(i)] = C::pack(dg);
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) gf[e] = g[i][e];
+        for (int e = 0; e < N; ++e) dg[e] = a[e] * yh[e] * wf[e];
+        if (p.dgate && at(i) < p.rc) static_cast<u32x4_t*>(p.dgate)[t * p.rc + at(i)] = C::pack(dg);
       }
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const float a = p.scale * q[i][e];
-        yh[i][e] *= r;
-        const float ay = a * yh[i][e];
+        const float ay = a[e] * yh[e];
         // the column sums leave a channel's gate out
-        col[i][e] = fmaf(p.gate_kind == MOE_GATE_FULL ? gf[e] : gt, ay, col[i][e]);
-        tok = fmaf(ay, w[i][e], tok);
-        q[i][e] = a * gt * gf[e] * w[i][e];
-        dot = fmaf(q[i][e], yh[i][e], dot);
+        col[i][e] = GATE == MOE_GATE_CHANNEL || GATE == MOE_GATE_NONE ? col[i][e] + ay : fmaf(gf[e], ay, col[i][e]);
+        if constexpr (GATE == MOE_GATE_TOKEN) tok = fmaf(ay, wf[e], tok);
+        dot = fmaf(ay, gf[e] * wf[e], dot);
       }
     }
-    if (p.gate_kind == MOE_GATE_TOKEN) {
+    if constexpr (GATE == MOE_GATE_TOKEN) {
       tok = row_sum<W>(tok, s_one);
       if (p.dgate && l == 0) static_cast<float*>(p.dgate)[t] = tok;
     }
     float mean = 0.f;
     if (p.rstd) mean = row_sum<W>(dot, s_two) * p.inv_h;
+    // (nothing that was taken apart above is kept)
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      asm volatile("" : "+v"(dv[i]), "+v"(yv[i]), "+v"(w[i]));
+      if constexpr (GATE == MOE_GATE_CHANNEL) asm volatile("" : "+v"(g[i]));
+      if constexpr (GATE == MOE_GATE_FULL) asm volatile("" : "+v"(gv[i]));
+    }
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       if (at(i) >= p.rc) continue;
-      float f[N];
+      float a[N], yh[N], wf[N], gf[N], f[N];
+      take(i, a, yh, wf, gf);
+      C::unpack(rv[i], f);
 #pragma unroll
-      for (int e = 0; e < N; ++e) f[e] = 0.f;
-      if (p.dres) C::unpack(rv[i], f);
-#pragma unroll
-      for (int e = 0; e < N; ++e) f[e] = fmaf(r, q[i][e] - yh[i][e] * mean, f[e]);
+      for (int e = 0; e < N; ++e) f[e] = fmaf(r, a[e] * gf[e] * wf[e] - yh[e] * mean, f[e]);
       p.dy[t * p.rc + at(i)] = C::pack(f);
     }
     if constexpr (W > 1) __syncthreads();                   // the exchanges read by all before the next row's
@@ -328,21 +354,37 @@ __global__ __launch_bounds__(RowShape<W>::THREADS) void k_norm_bwd(NormBwdParams
 }
 
 // Column sums of the partial rows: S_h; dw = S g (g per channel, else 1), dgate = S w.
-// 32 columns by 16 parts of the rows in a workgroup.
+// 16 columns by 64 parts of the rows in a workgroup, eight rows' loads in flight.
+constexpr int kColWidth = 16, kColParts = 64;
 template <bool BF16>
-__global__ __launch_bounds__(512) void k_norm_cols(const float* __restrict__ part, int rows, int H,
-                                                   const void* __restrict__ w, const void* __restrict__ gate,
-                                                   float* __restrict__ dw, float* __restrict__ dgate, int accumulate) {
-  __shared__ float s[16][33];
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, h = blockIdx.x * 32 + x;
+__global__ __launch_bounds__(kColWidth * kColParts) void k_norm_cols(const float* __restrict__ part, int rows, int H,
+                                                                     const void* __restrict__ w,
+                                                                     const void* __restrict__ gate,
+                                                                     float* __restrict__ dw, float* __restrict__ dgate,
+                                                                     int accumulate) {
+  __shared__ float s[kColParts][kColWidth + 1];
+  const int x = threadIdx.x % kColWidth, y = threadIdx.x / kColWidth, h = blockIdx.x * kColWidth + x;
   float v = 0.f;
-  if (h < H)
-    for (int r = y; r < rows; r += 16) v += part[static_cast<int64_t>(r) * H + h];
+  if (h < H) {
+    for (int r0 = y; r0 < rows; r0 += 8 * kColParts) {
+      float f[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int r = r0 + u * kColParts;
+        f[u] = r < rows ? part[static_cast<int64_t>(r) * H + h] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v += f[u];
+    }
+  }
   s[y][x] = v;
   __syncthreads();
+  for (int n = kColParts / 2; n > 0; n /= 2) {
+    if (y < n) s[y][x] += s[y + n][x];
+    __syncthreads();
+  }
   if (y != 0 || h >= H) return;
-#pragma unroll
-  for (int i = 1; i < 16; ++i) v += s[i][x];
+  v = s[0][x];
   auto get = [&](const void* p) {
     return p == nullptr ? 1.f : BF16 ? bf16_to_f32(static_cast<const bf16_t*>(p)[h]) : static_cast<const float*>(p)[h];
   };
@@ -358,17 +400,34 @@ static moe_status launch_norm_bwd(NormBwdParams& p, bool bf16, int32_t H, float*
   const int blocks = static_cast<int>(norm_bwd_blocks(p.T));
   p.part = cols ? static_cast<float*>(ws) : nullptr;
   if (p.T > 0) {
-    with_row_shape(p.T, p.rc, [&](auto w, auto ch) {
+    // past the caches (see kStreamBytes) from 24 MB an operand on: 16384 x 2048 41 -> 37 us,
+    // 2047 x 7168 with a residual 26.9 -> 24.7; 4096 x 2048 (17 MB) 13.5 -> 14.0
+    const bool stream = p.T * p.rc * 16 > (int64_t{24} << 20);
+    // (8192 rows of 256 chunks: 22.5 us with one wave each, 27.6 with four)
+    with_row_shape(p.T, p.rc, 256, [&](auto w, auto ch) {
       constexpr int W = decltype(w)::value, CH = decltype(ch)::value;
       auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(blocks), dim3(RowShape<W>::THREADS), 0, s, p); };
-      bf16 ? go(k_norm_bwd<true, W, CH>) : go(k_norm_bwd<false, W, CH>);
+      auto of_gate = [&](auto gate) {
+        constexpr int GATE = decltype(gate)::value;
+        if (bf16)
+          stream ? go(k_norm_bwd<true, W, CH, GATE, true>) : go(k_norm_bwd<true, W, CH, GATE, false>);
+        else
+          stream ? go(k_norm_bwd<false, W, CH, GATE, true>) : go(k_norm_bwd<false, W, CH, GATE, false>);
+      };
+      switch (p.gate_kind) {
+        case MOE_GATE_CHANNEL: of_gate(std::integral_constant<int, MOE_GATE_CHANNEL>{}); break;
+        case MOE_GATE_TOKEN: of_gate(std::integral_constant<int, MOE_GATE_TOKEN>{}); break;
+        case MOE_GATE_FULL: of_gate(std::integral_constant<int, MOE_GATE_FULL>{}); break;
+        default: of_gate(std::integral_constant<int, MOE_GATE_NONE>{});
+      }
     });
     DBOMOE_CHECK_LAUNCH();
   }
   if (cols && !(p.T == 0 && accumulate)) {
     const void* gate = p.gate_kind == MOE_GATE_CHANNEL ? p.gate : nullptr;
     auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((H + 31) / 32)), dim3(512), 0, s, p.part,
+      hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((H + kColWidth - 1) / kColWidth)),
+                         dim3(kColWidth * kColParts), 0, s, p.part,
                          p.T > 0 ? blocks : 0, H, static_cast<const void*>(p.w), gate, dw, dgate_cols, accumulate ? 1 : 0);
     };
     bf16 ? go(k_norm_cols<true>) : go(k_norm_cols<false>);

@@ -15,6 +15,13 @@ struct RowShape {
   static constexpr int ROWS = W == 1 ? 4 : 1;
 };
 
+// A chunk that the caches need not keep (STREAM), or as ever.
+template <bool STREAM>
+__device__ __forceinline__ u32x4_t load_chunk(const u32x4_t* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(p);
+  return *p;
+}
+
 // The values of a chunk as floats and back.
 template <bool BF16>
 struct Chunk {
@@ -48,12 +55,29 @@ struct Chunk {
   }
 };
 
+// Sum over a wave, the same in every lane, by cross-lane adds in registers (six
+// dependent adds; through LDS permutes the same takes six round trips).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  const int o = __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, false);
+  return v + __int_as_float(o);
+}
+__device__ __forceinline__ float wave_sum_dpp(float v) {
+  v = dpp_add<0x111, 0xf>(v);          // row_shr 1, 2, 4, 8: lane 15 of each 16 has their sum
+  v = dpp_add<0x112, 0xf>(v);
+  v = dpp_add<0x114, 0xf>(v);
+  v = dpp_add<0x118, 0xf>(v);
+  v = dpp_add<0x142, 0xa>(v);          // lane 15 of a row to the next, lane 31 to the upper half
+  v = dpp_add<0x143, 0xc>(v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
 // Sum (or maximum of bit patterns) over the W waves of a row, the same in every
 // lane; always added in the same order.  s: W words of LDS that no earlier
 // exchange still reads (two exchanges in a row need two arrays, or a barrier).
 template <int W>
 __device__ __forceinline__ float row_sum(float v, float* s) {
-  v = wave_sum_f(v);
+  v = wave_sum_dpp(v);
   if constexpr (W > 1) {
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -78,12 +102,14 @@ __device__ __forceinline__ uint32_t row_max_bits(uint32_t v, uint32_t* s) {
   return v;
 }
 
-// Calls f(W, CH) with the shape for rows of rc chunks (at most kRowMaxChunks):
-// one wave while that holds the row in four chunks per lane and there are rows
-// enough to fill the GPU with one wave each, else four, else sixteen.
+// Calls f(W, CH) with the shape for rows of rc chunks (at most kRowMaxChunks): one
+// wave for rows of up to `narrow` chunks (64, 128 or 256; short rows of few tokens
+// excepted), else four, else sixteen.  Sixteen waves for a row of 256 chunks took
+// twice the time of one or four in every kernel; of rows of 896 chunks they are on par
+// with four.
 constexpr int kRowMaxChunks = 4096;
 template <typename F>
-inline void with_row_shape(int64_t rows, int rc, F f) {
+inline void with_row_shape(int64_t rows, int rc, int narrow, F f) {
   auto with_ch = [&](auto w) {
     constexpr int W = decltype(w)::value;
     const int ch = (rc + 64 * W - 1) / (64 * W);
@@ -94,7 +120,8 @@ inline void with_row_shape(int64_t rows, int rc, F f) {
     else
       f(w, std::integral_constant<int, 4>{});
   };
-  if (rc <= 64 || (rc <= 256 && rows >= 2048))
+  // (256 rows of 256 chunks: 5.5 us with four waves each, 9.9 us with one)
+  if (rc <= 64 || (rc <= narrow && rows >= 2048))
     with_ch(std::integral_constant<int, 1>{});
   else if (rc <= 1024)
     with_ch(std::integral_constant<int, 4>{});
