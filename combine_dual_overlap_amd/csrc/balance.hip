@@ -2,6 +2,7 @@
 // the weights do not see, the bias's update from the experts' load, and the
 // balance loss with its gradient.
 #include "gemm_mfma.h"
+#include "rows.h"
 
 namespace dbomoe {
 
@@ -25,32 +26,108 @@ struct SelectParams {
   int32_t* ids;
   float* w;
   int32_t* load;           // [E] or NULL: what each expert got is added
+  int count_here;          // k_select adds it all; else only takes off what k_count will add too much
 };
 
-__device__ __forceinline__ double wave_sum_d(double v) {
-#pragma unroll
-  for (int d = kWave / 2; d > 0; d >>= 1) v += __shfl_xor(v, d, kWave);
+// Cross-lane moves in registers (the lane permutes through LDS that __shfl makes are
+// a round trip each, and the steps here depend on one another).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_move(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false));
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add_d(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t lo = dpp_move<CTRL, ROWS>(static_cast<uint32_t>(b)), hi = dpp_move<CTRL, ROWS>(static_cast<uint32_t>(b >> 32));
+  return v + __builtin_bit_cast(double, hi << 32 | lo);
+}
+
+__device__ __forceinline__ double lane_of(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(b), lane));
+  const uint64_t hi = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(b >> 32), lane));
+  return __builtin_bit_cast(double, hi << 32 | lo);
+}
+
+// Sum of the first 16 lanes, of the wave; the largest of the wave: the same in every lane.
+__device__ __forceinline__ double row_sum_d(double v) {
+  v = dpp_add_d<0x111, 0xf>(v);          // row_shr 1, 2, 4, 8: lane 15 of each 16 has their sum
+  v = dpp_add_d<0x112, 0xf>(v);
+  v = dpp_add_d<0x114, 0xf>(v);
+  v = dpp_add_d<0x118, 0xf>(v);
   return v;
 }
 
-// (value descending, index ascending): the best of the wave, in every lane.
-__device__ __forceinline__ void wave_best(double& v, int& e) {
-#pragma unroll
-  for (int d = kWave / 2; d > 0; d >>= 1) {
-    const double ov = __shfl_xor(v, d, kWave);
-    const int oe = __shfl_xor(e, d, kWave);
-    if (ov > v || (ov == v && oe < e)) {
-      v = ov;
-      e = oe;
-    }
-  }
+__device__ __forceinline__ double wave_sum_d(double v) {
+  v = row_sum_d(v);
+  v = dpp_add_d<0x142, 0xa>(v);          // lane 15 of a row to the next, lane 31 to the upper half
+  v = dpp_add_d<0x143, 0xc>(v);
+  return lane_of(v, 63);
+}
+
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = max(v, dpp_move<0x111, 0xf>(v));
+  v = max(v, dpp_move<0x112, 0xf>(v));
+  v = max(v, dpp_move<0x114, 0xf>(v));
+  v = max(v, dpp_move<0x118, 0xf>(v));
+  v = max(v, dpp_move<0x142, 0xa>(v));
+  v = max(v, dpp_move<0x143, 0xc>(v));
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+
+// Bits whose order as whole numbers is that of the floats; 0 is below all of them.
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u ^ (u >> 31 ? 0x80000000u : 0xffffffffu));
+}
+
+// e^x for x <= 0, and 1 / x for x >= 1, to a few units in the last place of 64 bits:
+// x = n ln 2 + r with |r| <= ln 2 / 2, the Taylor sum of e^r to r^13 (the next term is
+// below 2^-57), times 2^n; Newton steps from the hardware's reciprocal.  (The general
+// functions are several times as long, and what a token's wave waits for here is
+// instructions.)
+__device__ __forceinline__ double exp_neg(double x) {
+  x = fmax(x, -800.0);                                   // e^-800 is 0
+  const double n = rint(x * 1.4426950408889634);
+  double r = fma(n, -0x1.62e42fefa0000p-1, x);           // ln 2 in two parts, the first exact times n
+  r = fma(n, -0x1.cf79abc9e3b3ap-40, r);
+  double s = 1.0 / 6227020800.0;
+  s = fma(s, r, 1.0 / 479001600.0);
+  s = fma(s, r, 1.0 / 39916800.0);
+  s = fma(s, r, 1.0 / 3628800.0);
+  s = fma(s, r, 1.0 / 362880.0);
+  s = fma(s, r, 1.0 / 40320.0);
+  s = fma(s, r, 1.0 / 5040.0);
+  s = fma(s, r, 1.0 / 720.0);
+  s = fma(s, r, 1.0 / 120.0);
+  s = fma(s, r, 1.0 / 24.0);
+  s = fma(s, r, 1.0 / 6.0);
+  s = fma(s, r, 0.5);
+  s = fma(s, r, 1.0);
+  s = fma(s, r, 1.0);
+  return __builtin_amdgcn_ldexp(s, static_cast<int>(n));
+}
+
+__device__ __forceinline__ double inverse(double x) {
+  double r = __builtin_amdgcn_rcp(x);
+  r = fma(fma(-x, r, 1.0), r, r);
+  return fma(fma(-x, r, 1.0), r, r);
 }
 
 constexpr int kSelTokens = 4;      // tokens of a workgroup, one wave each
 
+// One wave per token, NE experts in a lane: expert lane + 64 i.
+// A slot's expert is found by the keys rounded to fp32 (which keeps their order):
+// the wave's largest, then a ballot for who has it; only where several do, the keys
+// themselves are compared.
+template <int NE>
 __global__ __launch_bounds__(64 * kSelTokens) void k_select(SelectParams p) {
-  __shared__ double s_key[kSelTokens][256];
-  __shared__ int s_load[256];
+  __shared__ double s_val[kSelTokens][64 * NE];
+  __shared__ int s_load[64 * NE];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int E = p.rp.E, k = p.rp.k;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kSelTokens + wave;
@@ -59,148 +136,252 @@ __global__ __launch_bounds__(64 * kSelTokens) void k_select(SelectParams p) {
     __syncthreads();
   }
   if (t < p.T) {
-    float l[4];
-    unsigned cand = 0;                         // bit i: expert lane + 64 i may be chosen
-    float lmax = -INFINITY;
+    const double NEG = -INFINITY;
+    double* val = s_val[wave];
+    float l[NE], bias[NE];
+    bool cand[NE];                             // may be chosen
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NE; ++i) {
       const int e = lane + 64 * i;
       l[i] = -INFINITY;
+      bias[i] = 0.f;
       if (e >= E) continue;
+      if (p.bias) bias[i] = p.bias[e];
       float s = 0.f;
       for (int s0 = 0; s0 < p.S; ++s0) s += p.part[(s0 * p.T + t) * E + e];     // in split order
       if (p.logit_bias) s += p.logit_bias[e];
       if (p.logits) p.logits[t * E + e] = s;
-      if (s > -INFINITY) {
-        l[i] = fminf(s, 3.402823466e38f);
-        cand |= 1u << i;
-        lmax = fmaxf(lmax, l[i]);
-      }
+      if (s > -INFINITY) l[i] = fminf(s, 3.402823466e38f);
     }
-    const bool softmax = p.rp.score == MOE_SCORE_SOFTMAX;
-    double pr[4], key[4];
-    if (softmax) {
-      lmax = wave_max_f(lmax);
+    double pr[NE], key[NE];
+    if (p.rp.score == MOE_SCORE_SOFTMAX) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) top = max(top, ordered(l[i]));
+      const double lmax = unordered(wave_max_u32(top));
       double sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        pr[i] = (cand >> i) & 1u ? exp(static_cast<double>(l[i]) - static_cast<double>(lmax)) : 0.0;
+      for (int i = 0; i < NE; ++i) {
+        pr[i] = l[i] > -INFINITY ? exp_neg(static_cast<double>(l[i]) - lmax) : 0.0;
         sum += pr[i];
       }
       sum = wave_sum_d(sum);
+      const double inv = sum > 0.0 ? inverse(sum) : 0.0;     // (a sum is at least 1)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pr[i] = (cand >> i) & 1u ? pr[i] / sum : 0.0;
+      for (int i = 0; i < NE; ++i) pr[i] *= inv;
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pr[i] = (cand >> i) & 1u ? 1.0 / (1.0 + exp(-static_cast<double>(l[i]))) : 0.0;
+      for (int i = 0; i < NE; ++i) {
+        const double e = exp_neg(-fabs(static_cast<double>(l[i])));      // (0 for a masked one)
+        pr[i] = (l[i] < 0.f ? e : 1.0) * inverse(1.0 + e);
+        if (!(l[i] > -INFINITY)) pr[i] = 0.0;
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      key[i] = pr[i] + (p.bias && lane + 64 * i < E ? static_cast<double>(p.bias[lane + 64 * i]) : 0.0);
-    const double NEG = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (!(key[i] > NEG)) cand &= ~(1u << i);         // a bias of -inf or NaN masks too
-    if (p.rp.n_groups > 1) {
-      const int G = p.rp.n_groups, per = E / G, n = p.rp.group_topn;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (lane + 64 * i < E) s_key[wave][lane + 64 * i] = (cand >> i) & 1u ? key[i] : NEG;
-      __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      double gs = NEG;
-      if (lane < G) {
-        double top[4] = {NEG, NEG, NEG, NEG};
-        for (int j = 0; j < per; ++j) {
-          double x = s_key[wave][lane * per + j];
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (q < n && x > top[q]) {
-              const double tmp = top[q];
-              top[q] = x;
-              x = tmp;
-            }
-        }
-        gs = top[0];
-#pragma unroll
-        for (int q = 1; q < 4; ++q)
-          if (q < n && top[q] > NEG) gs += top[q];
-      }
-      uint64_t kept = 0;
-      for (int r = 0; r < p.rp.topk_groups; ++r) {
-        const bool open = lane < G && !((kept >> lane) & 1ull);
-        double bv = open ? gs : NEG;
-        int be = open ? lane : 1 << 30;
-        wave_best(bv, be);
-        kept |= 1ull << be;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = lane + 64 * i;
-        if (e < E && !((kept >> (e / per)) & 1ull)) cand &= ~(1u << i);
-      }
+    for (int i = 0; i < NE; ++i) {
+      key[i] = pr[i] + static_cast<double>(bias[i]);
+      cand[i] = l[i] > -INFINITY && key[i] > NEG;        // a bias of -inf or NaN masks too
     }
 
-    unsigned left = 0;                         // not chosen yet
+    if (p.rp.n_groups > 1) {
+      // A group's members are read by a team of lanes, as many as fit into the wave;
+      // each keeps its group_topn best in order, and the team's lists are merged.
+      const int G = p.rp.n_groups, per = E / G, n = p.rp.group_topn;
+      const int team = 64 >> (32 - __clz(G - 1));        // a power of two
+      const int grp = lane / team, at = lane & (team - 1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 64 * i < E) left |= 1u << i;
-    int my_e = 0;
-    double my_p = 0.0, sum = 0.0;
-#pragma unroll 1
-    for (int j = 0; j < k; ++j) {
-      double bv = NEG;
-      int be = 1 << 30;
+      for (int i = 0; i < NE; ++i)
+        if (lane + 64 * i < E) val[lane + 64 * i] = cand[i] ? key[i] : NEG;
+      __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      double best[4] = {NEG, NEG, NEG, NEG};
+      auto insert = [&](double x) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+        for (int q = 0; q < 4; ++q) {
+          if (q >= n) break;
+          const double more = fmax(best[q], x);
+          x = fmin(best[q], x);
+          best[q] = more;
+        }
+      };
+      if (grp < G)
+        for (int j0 = at; j0 < per; j0 += 4 * team) {    // four reads in flight
+          double x[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x[q] = j0 + q * team < per ? val[grp * per + j0 + q * team] : NEG;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) insert(x[q]);
+        }
+      for (int d = 1; d < team; d <<= 1) {
+        double other[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < n) other[q] = __shfl_xor(best[q], d, kWave);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < n) insert(other[q]);
+      }
+      double score = best[0];
+#pragma unroll
+      for (int q = 1; q < 4; ++q)
+        if (q < n && best[q] > NEG) score += best[q];
+      // its place among the groups
+      int place = 0;
+      for (int o = 0; o < G; ++o) {
+        const double so = lane_of(score, o * team);
+        place += so > score || (so == score && o < grp);
+      }
+      const uint64_t kept = __ballot(grp < G && place < p.rp.topk_groups);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
         const int e = lane + 64 * i;
-        if (((cand >> i) & 1u) && (key[i] > bv || be == 1 << 30)) {
-          bv = key[i];
-          be = e;
+        if (e < E) cand[i] = cand[i] && (kept >> (e / per * team) & 1ull);
+      }
+      __builtin_amdgcn_wave_barrier();                   // val is read by all before it is written again
+    }
+
+    uint32_t u[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      u[i] = cand[i] ? ordered(static_cast<float>(key[i])) : 0;
+      if (lane + 64 * i < E) val[lane + 64 * i] = pr[i];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    int my_e = 0, real = 0;                    // slot j is kept by lane j
+#pragma unroll 1
+    for (; real < k; ++real) {
+      uint32_t m = u[0];
+#pragma unroll
+      for (int i = 1; i < NE; ++i) m = max(m, u[i]);
+      m = wave_max_u32(m);
+      if (m == 0) break;                       // no candidate is left
+      uint64_t who[NE];
+      int have = 0;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        who[i] = __ballot(u[i] == m);
+        have += __popcll(who[i]);
+      }
+      auto lowest = [&](double* its) {         // the lowest expert of who, and its key
+        int be = 0;
+#pragma unroll
+        for (int i = NE - 1; i >= 0; --i)
+          if (who[i]) {
+            const int src = __ffsll(static_cast<unsigned long long>(who[i])) - 1;
+            be = src + 64 * i;
+            if (its) *its = lane_of(key[i], src);
+          }
+        return be;
+      };
+      int be;
+      if (have == 1) {
+        be = lowest(nullptr);
+      } else {
+        // those above the lowest one's key, until there are none
+        bool more = true;
+        while (more) {
+          double its = 0.0;
+          be = lowest(&its);
+          more = false;
+          uint64_t above[NE];
+#pragma unroll
+          for (int i = 0; i < NE; ++i) {
+            above[i] = __ballot(u[i] == m && key[i] > its);
+            more |= above[i] != 0;
+          }
+          if (more)
+#pragma unroll
+            for (int i = 0; i < NE; ++i) who[i] = above[i];
         }
       }
-      wave_best(bv, be);
-      bool real = be < E;
-      if (!real) {                             // no candidate is left: the first expert not chosen, weight 0
-        bv = 0.0;
-        be = 1 << 30;
 #pragma unroll
-        for (int i = 3; i >= 0; --i)
-          if ((left >> i) & 1u) be = lane + 64 * i;
-        wave_best(bv, be);
+      for (int i = 0; i < NE; ++i)
+        if (lane + 64 * i == be) u[i] = 0;
+      if (lane == real) my_e = be;
+    }
+    // the slots without a candidate: the first experts not chosen, weight 0
+    if (real < k) {
+      uint64_t taken[NE];
+#pragma unroll
+      for (int i = 0; i < NE; ++i) taken[i] = 0;
+      for (int j = 0; j < real; ++j) {
+        const int e = __builtin_amdgcn_readlane(my_e, j);
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+          if (e >> 6 == i) taken[i] |= 1ull << (e & 63);
       }
-      const int i = be >> 6;
-      if ((be & 63) == lane) {
-        cand &= ~(1u << i);
-        left &= ~(1u << i);
-      }
-      const double mine = i == 0 ? pr[0] : i == 1 ? pr[1] : i == 2 ? pr[2] : pr[3];
-      const double pj = real ? __shfl(mine, be & 63, kWave) : 0.0;
-      sum += pj;
-      if (lane == j) {
-        my_e = be;
-        my_p = pj;
-        if (p.load && real) atomicAdd(&s_load[be], 1);
+      for (int j = real; j < k; ++j) {
+        int e = 0;
+#pragma unroll
+        for (int i = NE - 1; i >= 0; --i)
+          if (~taken[i]) e = 64 * i + __ffsll(static_cast<unsigned long long>(~taken[i])) - 1;
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+          if (e >> 6 == i) taken[i] |= 1ull << (e & 63);
+        if (lane == j) my_e = e;
       }
     }
+    const double my_p = lane < real ? val[my_e] : 0.0;
+    const double sum = lane_of(row_sum_d(my_p), 15);     // (at most 16 slots)
     if (lane < k) {
       const double w = p.rp.renormalize && sum > 0.0 ? my_p / sum : my_p;
       p.ids[t * k + lane] = my_e;
       p.w[t * k + lane] = static_cast<float>(w * static_cast<double>(p.rp.routed_scale));
+      if (p.load && (lane < real) == (p.count_here != 0)) atomicAdd(&s_load[my_e], 1);
     }
   }
   if (p.load) {
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x)
-      if (s_load[e]) atomicAdd(&p.load[e], s_load[e]);        // whole numbers: any order
+      if (s_load[e]) atomicAdd(&p.load[e], p.count_here ? s_load[e] : -s_load[e]);      // whole numbers: any order
   }
 }
 
-moe_status launch_select(const SelectParams& p, hipStream_t s) {
+// Up to this many tokens k_select adds up the load itself.  512 tokens x 8 of 256: 1.3 us
+// for it, where k_count takes 3.5; 4096 x 8: 13 us, and k_count 4.
+constexpr int64_t kCountHere = 512;
+
+// load[e] += how often e is among the n ids.  Few workgroups: it is the additions to the
+// same few cache lines from all over the GPU that take the time.
+__global__ __launch_bounds__(1024) void k_count(const int32_t* __restrict__ ids, int64_t n, int E,
+                                                int32_t* __restrict__ load) {
+  __shared__ int s_load[4][256];
+  s_load[threadIdx.x >> 8][threadIdx.x & 255] = 0;
+  __syncthreads();
+  int* mine = s_load[threadIdx.x & 3];
+  const int4* ids4 = reinterpret_cast<const int4*>(ids);
+  const int64_t n4 = n / 4, stride = static_cast<int64_t>(gridDim.x) * 1024;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 1024 + threadIdx.x; i < n4; i += stride) {
+    const int4 v = ids4[i];
+    atomicAdd(&mine[v.x], 1);
+    atomicAdd(&mine[v.y], 1);
+    atomicAdd(&mine[v.z], 1);
+    atomicAdd(&mine[v.w], 1);
+  }
+  if (blockIdx.x == 0 && threadIdx.x < (n & 3)) atomicAdd(&mine[ids[n4 * 4 + threadIdx.x]], 1);
+  __syncthreads();
+  const int e = threadIdx.x;
+  if (e >= E) return;
+  const int sum = s_load[0][e] + s_load[1][e] + s_load[2][e] + s_load[3][e];
+  if (sum) atomicAdd(&load[e], sum);
+}
+
+moe_status launch_select(SelectParams p, hipStream_t s) {
   if (p.T == 0) return MOE_OK;
-  hipLaunchKernelGGL(k_select, dim3(static_cast<unsigned>((p.T + kSelTokens - 1) / kSelTokens)), dim3(64 * kSelTokens), 0,
-                     s, p);
+  const int64_t n = p.T * p.rp.k;
+  p.count_here = p.T <= kCountHere;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((p.T + kSelTokens - 1) / kSelTokens)), dim3(64 * kSelTokens), 0,
+                       s, p);
+  };
+  p.rp.E <= 64 ? go(k_select<1>) : p.rp.E <= 128 ? go(k_select<2>) : go(k_select<4>);
   DBOMOE_CHECK_LAUNCH();
+  if (p.load && !p.count_here) {
+    const int64_t blocks = std::min<int64_t>(std::max<int64_t>(n / 2048, 1), 16);
+    hipLaunchKernelGGL(k_count, dim3(static_cast<unsigned>(blocks)), dim3(1024), 0, s, p.ids, n, p.rp.E, p.load);
+    DBOMOE_CHECK_LAUNCH();
+  }
   return MOE_OK;
 }
 
@@ -208,7 +389,7 @@ moe_status launch_route_balanced(const RouteArgs& a, const float* select_bias, i
   if (a.T == 0) return MOE_OK;
   const moe_status st = launch_route_logits(a, s);
   if (st != MOE_OK) return st;
-  SelectParams p{a.part, route_splits(a.T, a.H, a.p.E), a.T, a.bias, select_bias, a.p, a.logits, a.ids, a.w, load};
+  SelectParams p{a.part, route_splits(a.T, a.H, a.p.E), a.T, a.bias, select_bias, a.p, a.logits, a.ids, a.w, load, 0};
   return launch_select(p, s);
 }
 
@@ -242,73 +423,79 @@ __global__ __launch_bounds__(256) void k_bias_update(float* __restrict__ bias, i
 // inner sums, and k_loss_sum adds these in order.
 constexpr int kLossBlocks = 1024;      // at most; four waves each
 
-template <typename Out, bool ADD>
+template <typename Out, bool ADD, int NE>
 __global__ __launch_bounds__(256) void k_balance_loss(const float* __restrict__ logits, int64_t T,
                                                       const int32_t* __restrict__ load, int E, int softmax, float scale,
                                                       Out* __restrict__ dl, double* __restrict__ part) {
   __shared__ double s_part[4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float f1[4];                          // f - 1
-  long long n[4], sum = 0;
+  float f1[NE];                         // f - 1
+  double n[NE], sum = 0.0;              // (whole numbers below 2^53: exact)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < NE; ++i) {
     n[i] = lane + 64 * i < E ? load[lane + 64 * i] : 0;
     sum += n[i];
   }
+  sum = wave_sum_d(sum);
+  const bool any = sum > 0.0;           // no load: f = 0, no loss
 #pragma unroll
-  for (int d = kWave / 2; d > 0; d >>= 1) sum += __shfl_xor(sum, d, kWave);
-  const float none = sum > 0 ? 0.f : -1.f;        // no load: f = 0, no loss
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    f1[i] = sum > 0 ? static_cast<float>(static_cast<double>(n[i] * E - sum) / static_cast<double>(sum)) : 0.f;
+  for (int i = 0; i < NE; ++i) f1[i] = any ? static_cast<float>((n[i] * E - sum) / sum) : 0.f;
   double total = 0.0;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave; t < T; t += static_cast<int64_t>(gridDim.x) * 4) {
     const float* row = logits + t * E;
-    float l[4], q[4], c[4] = {1.f, 1.f, 1.f, 1.f};
-    bool in[4];
+    float l[NE], q[NE], c[NE], was[NE];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float v = lane + 64 * i < E ? row[lane + 64 * i] : -INFINITY;
-      in[i] = v > -INFINITY;                      // masked experts (-inf, NaN): q = 0, no gradient
-      l[i] = in[i] ? fminf(v, 3.402823466e38f) : -INFINITY;
+    for (int i = 0; i < NE; ++i) {
+      const int e = lane + 64 * i;
+      l[i] = -INFINITY;
+      was[i] = 0.f;
+      if (e >= E) continue;
+      if constexpr (ADD && sizeof(Out) == 2) was[i] = bf16_to_f32(dl[t * E + e]);
+      if constexpr (ADD && sizeof(Out) == 4) was[i] = dl[t * E + e];
+      const float v = row[e];
+      if (v > -INFINITY) l[i] = fminf(v, 3.402823466e38f);       // masked experts (-inf, NaN): q = 0, no gradient
     }
     float norm = 0.f;
     if (softmax) {
-      const float lmax = wave_max_f(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
+      uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = in[i] ? expf(l[i] - lmax) : 0.f;
+      for (int i = 0; i < NE; ++i) top = max(top, ordered(l[i]));
+      const float lmax = unordered(wave_max_u32(top));
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        q[i] = l[i] > -INFINITY ? expf(l[i] - lmax) : 0.f;
+        c[i] = 1.f;
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        q[i] = in[i] ? 1.0f / (1.0f + expf(-l[i])) : 0.f;
-        c[i] = in[i] ? 1.0f / (1.0f + expf(l[i])) : 0.f;      // 1 - p, without cancellation
+      for (int i = 0; i < NE; ++i) {
+        const float e = expf(-fabsf(l[i])), r = 1.0f / (1.0f + e);
+        const bool in = l[i] > -INFINITY;
+        q[i] = in ? (l[i] < 0.f ? e * r : r) : 0.f;
+        c[i] = l[i] < 0.f ? r : e * r;                           // 1 - p, without cancellation
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) norm += q[i];
-    norm = wave_sum_f(norm);
+    for (int i = 0; i < NE; ++i) norm += q[i];
+    norm = wave_sum_dpp(norm);
     const float inv = norm > 0.f ? 1.0f / norm : 0.f;
     float dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NE; ++i) {
       q[i] *= inv;
       dot += q[i] * f1[i];
     }
-    dot = wave_sum_f(dot);
-    if (norm > 0.f) total += static_cast<double>(dot) + 1.0 + none;
+    dot = wave_sum_dpp(dot);
+    if (norm > 0.f && any) total += static_cast<double>(dot) + 1.0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NE; ++i) {
       const int e = lane + 64 * i;
       if (e >= E) continue;
-      float g = scale * (q[i] * c[i]) * (f1[i] - dot);
-      Out* at = dl + t * E + e;
-      if constexpr (sizeof(Out) == 2) {
-        if (ADD) g += bf16_to_f32(*at);
-        *at = f32_to_bf16(g);
-      } else {
-        if (ADD) g += *at;
-        *at = g;
-      }
+      const float g = was[i] + scale * (q[i] * c[i]) * (f1[i] - dot);
+      if constexpr (sizeof(Out) == 2)
+        dl[t * E + e] = f32_to_bf16(g);
+      else
+        dl[t * E + e] = g;
     }
   }
   if (lane == 0) s_part[wave] = total;
@@ -348,7 +535,7 @@ extern "C" moe_status moe_route_select(const float* logits, int64_t T, const flo
   if (!aligned16(logits) || (select_bias && !aligned16(select_bias)) || !aligned16(topk_ids) || !aligned16(topk_w) ||
       (load && !aligned16(load)))
     return MOE_ERR_MISALIGNED;
-  SelectParams p{logits, 1, T, nullptr, select_bias, *params, nullptr, topk_ids, topk_w, load};
+  SelectParams p{logits, 1, T, nullptr, select_bias, *params, nullptr, topk_ids, topk_w, load, 0};
   return launch_select(p, as_stream(stream));
 }
 
@@ -420,12 +607,21 @@ extern "C" moe_status moe_route_balance_loss(const float* logits, int64_t T, con
     hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), 0, s, logits, T, load, params->E, softmax,
                        static_cast<float>(over_t), out, part);
   };
-  if (dl == MOE_BF16)
-    accumulate ? go(k_balance_loss<bf16_t, true>, static_cast<bf16_t*>(dlogits))
-               : go(k_balance_loss<bf16_t, false>, static_cast<bf16_t*>(dlogits));
+  auto of = [&](auto ne) {
+    constexpr int NE = decltype(ne)::value;
+    if (dl == MOE_BF16)
+      accumulate ? go(k_balance_loss<bf16_t, true, NE>, static_cast<bf16_t*>(dlogits))
+                 : go(k_balance_loss<bf16_t, false, NE>, static_cast<bf16_t*>(dlogits));
+    else
+      accumulate ? go(k_balance_loss<float, true, NE>, static_cast<float*>(dlogits))
+                 : go(k_balance_loss<float, false, NE>, static_cast<float*>(dlogits));
+  };
+  if (params->E <= 64)
+    of(std::integral_constant<int, 1>{});
+  else if (params->E <= 128)
+    of(std::integral_constant<int, 2>{});
   else
-    accumulate ? go(k_balance_loss<float, true>, static_cast<float*>(dlogits))
-               : go(k_balance_loss<float, false>, static_cast<float*>(dlogits));
+    of(std::integral_constant<int, 4>{});
   DBOMOE_CHECK_LAUNCH();
   hipLaunchKernelGGL(k_loss_sum, dim3(1), dim3(256), 0, s, part, blocks, over_t, loss);
   DBOMOE_CHECK_LAUNCH();
