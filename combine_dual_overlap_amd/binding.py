@@ -597,21 +597,24 @@ def _typed(t, dtype, shape, what: str):
 
 
 def _check_select(E, T, params, topk_ids, topk_w, select_bias, load):
+    k = params.k
     if E != params.E:
         raise ValueError("logits of params.E experts")
-    _typed(topk_ids, torch.int32, (T, params.k), "topk_ids")
-    _typed(topk_w, torch.float32, (T, params.k), "topk_w")
-    if select_bias is not None:
-        _typed(select_bias, torch.float32, (E,), "select_bias")
-    if load is not None:
-        _typed(load, torch.int32, (E,), "load")
+    if (topk_ids.dtype != torch.int32 or topk_ids.shape != (T, k) or topk_w.dtype != torch.float32 or
+            topk_w.shape != (T, k)):
+        raise ValueError(f"topk_ids int32, topk_w float32 [{T}, {k}]")
+    if select_bias is not None and (select_bias.dtype != torch.float32 or select_bias.shape != (E,)):
+        raise ValueError(f"select_bias: float32 [{E}]")
+    if load is not None and (load.dtype != torch.int32 or load.shape != (E,)):
+        raise ValueError(f"load: int32 [{E}]")
 
 
 def moe_route_select(logits, params: moe_route_params, topk_ids, topk_w, select_bias=None, load=None, stream=None):
     """topk_ids and topk_w [T, k] of logits [T, E] float32: chosen by score + select_bias [E], weighted by the score.
     load [E] int32 (optional): the number of tokens of each expert is added."""
     T, E = logits.shape
-    _typed(logits, torch.float32, (T, E), "logits")
+    if logits.dtype != torch.float32:
+        raise ValueError("logits: float32")
     _check_select(E, T, params, topk_ids, topk_w, select_bias, load)
     d = _device(logits)
     pl, pb, pi, pw, po = _ptrs(d, logits, select_bias, topk_ids, topk_w, load)
@@ -748,56 +751,44 @@ def moe_grouped_ffn_int8(xq, xq_scale, offsets, w13, w13_scale, w2, w2_scale, y,
 
 # ------------------------------------------------------------------ norms before and after the layer
 
-def _rows_typed(t, like, what: str):
-    if t is not None and (t.dtype != like.dtype or t.shape != like.shape):
-        raise ValueError(f"{what}: {like.dtype} {list(like.shape)}")
+# (Each check is one expression: a decode-sized call takes the GPU 5 us, and a function
+# call for every tensor took the host as long.)
 
-
-def _channel(t, like, what: str):
-    if t is not None:
-        _typed(t, like.dtype, like.shape[1:], what)
-
-
-def _token(t, T: int, what: str):
-    if t is not None:
-        _typed(t, torch.float32, (T,), what)
-
-
-def _gate_kind(gate, like) -> int:
+def _gate_kind(gate, T: int, H: int, dtype) -> int:
     """By shape: [H] and [T, H] of the rows' type, or [T, 1] float32."""
-    if gate is None:
-        return MOE_GATE_NONE
-    T, H = like.shape
-    if gate.dtype == like.dtype and gate.shape == (H,):
+    s, t = gate.shape, gate.dtype
+    if t == dtype and s == (H,):
         return MOE_GATE_CHANNEL
-    if gate.dtype == torch.float32 and gate.shape == (T, 1) and H != 1:
+    if t == torch.float32 and s == (T, 1) and H != 1:
         return MOE_GATE_TOKEN
-    if gate.dtype == like.dtype and gate.shape == (T, H):
+    if t == dtype and s == (T, H):
         return MOE_GATE_FULL
-    raise ValueError(f"gate: {like.dtype} [{H}] or [{T}, {H}], or float32 [{T}, 1]")
+    raise ValueError(f"gate: {dtype} [{H}] or [{T}, {H}], or float32 [{T}, 1]")
 
 
 def moe_pre_norm(x, w, n, eps: float, rstd=None, stream=None):
     """n [T, H] = x / rms(x) * w; rstd [T] float32 (optional): 1 / rms, for the backward pass.  n may be x."""
-    T, H = x.shape
-    _rows_typed(n, x, "n")
-    _channel(w, x, "w")
-    _token(rstd, T, "rstd")
+    t, s = x.dtype, x.shape
+    T, H = s
+    if n.dtype != t or n.shape != s or w.dtype != t or w.shape != (H,):
+        raise ValueError(f"n: {t} [{T}, {H}], w: {t} [{H}]")
+    if rstd is not None and (rstd.dtype != torch.float32 or rstd.shape != (T,)):
+        raise ValueError(f"rstd: float32 [{T}]")
     d = _device(x)
     px, pw, pn, pr = _ptrs(d, x, w, n, rstd)
-    _call("moe_pre_norm", d, stream, px, _code(x.dtype), T, H, pw, eps, pn, pr)
+    _call("moe_pre_norm", d, stream, px, _code(t), T, H, pw, eps, pn, pr)
 
 
-def _post_params(d, like, eps, post_w, gate, scale, next_w, next_n, rstd, next_rstd) -> moe_post_norm_params:
-    T = like.shape[0]
-    _channel(post_w, like, "post_w")
-    _channel(next_w, like, "next_w")
-    _rows_typed(next_n, like, "next_n")
-    _token(rstd, T, "rstd")
-    _token(next_rstd, T, "next_rstd")
-    kind = _gate_kind(gate, like)
-    pw, pg, pn = _ptrs(d, post_w, gate, next_w)
-    return moe_post_norm_params(pw, pg, kind, scale, eps, pn)
+def _check_post(t, s, post_w, next_w, next_n, rstd, next_rstd):
+    T, H = s
+    if ((post_w is not None and (post_w.dtype != t or post_w.shape != (H,))) or
+            (next_w is not None and (next_w.dtype != t or next_w.shape != (H,)))):
+        raise ValueError(f"post_w, next_w: {t} [{H}]")
+    if next_n is not None and (next_n.dtype != t or next_n.shape != s):
+        raise ValueError(f"next_n: {t} [{T}, {H}]")
+    if ((rstd is not None and (rstd.dtype != torch.float32 or rstd.shape != (T,))) or
+            (next_rstd is not None and (next_rstd.dtype != torch.float32 or next_rstd.shape != (T,)))):
+        raise ValueError(f"rstd, next_rstd: float32 [{T}]")
 
 
 def moe_post_norm(y, res, out, eps: float, post_w=None, gate=None, scale: float = 1.0, rstd=None, next_w=None,
@@ -805,31 +796,39 @@ def moe_post_norm(y, res, out, eps: float, post_w=None, gate=None, scale: float 
     """out [T, H] = res + scale * gate * (y / rms(y) * post_w), and next_n = out / rms(out) * next_w.
 
     res None: no residual; post_w None: no norm; gate [H] or [T, H] of y's type, or float32 [T, 1].  out may be res."""
-    T, H = y.shape
-    _rows_typed(res, y, "res")
-    _rows_typed(out, y, "out")
+    t, s = y.dtype, y.shape
+    T, H = s
+    if out.dtype != t or out.shape != s or (res is not None and (res.dtype != t or res.shape != s)):
+        raise ValueError(f"res, out: {t} [{T}, {H}]")
+    _check_post(t, s, post_w, next_w, next_n, rstd, next_rstd)
+    kind = MOE_GATE_NONE if gate is None else _gate_kind(gate, T, H, t)
     d = _device(y)
-    q = _post_params(d, y, eps, post_w, gate, scale, next_w, next_n, rstd, next_rstd)
-    py, pe, po, pr, pn, ps = _ptrs(d, y, res, out, rstd, next_n, next_rstd)
-    _call("moe_post_norm", d, stream, py, _code(y.dtype), T, H, pe, q, po, pr, pn, ps)
+    py, pe, po, pr, pn, ps, pw, pg, px = _ptrs(d, y, res, out, rstd, next_n, next_rstd, post_w, gate, next_w)
+    _call("moe_post_norm", d, stream, py, _code(t), T, H, pe, moe_post_norm_params(pw, pg, kind, scale, eps, px), po, pr,
+          pn, ps)
 
 
 def moe_combine_post_norm(y_perm, inv, topk_w, res, out, eps: float, post_w=None, gate=None, scale: float = 1.0,
                           shared_out=None, y_out=None, rstd=None, next_w=None, next_n=None, next_rstd=None, stream=None):
     """moe_post_norm of moe_combine's sum of y_perm, inv [T*k], topk_w [T, k] (+ shared_out [T, H]); y_out: that sum."""
-    T, H = out.shape
+    t, s = out.dtype, out.shape
+    T, H = s
     k = topk_w.shape[1]
-    if y_perm.dtype != out.dtype or y_perm.dim() != 2 or y_perm.shape[1] != H:
-        raise ValueError(f"y_perm: {out.dtype} [rows, {H}]")
+    if y_perm.dtype != t or y_perm.dim() != 2 or y_perm.shape[1] != H:
+        raise ValueError(f"y_perm: {t} [rows, {H}]")
     if topk_w.dtype != torch.float32 or topk_w.shape != (T, k) or inv.dtype != torch.int32 or inv.numel() != T * k:
         raise ValueError("topk_w float32 [T, k], inv int32 [T * k]")
-    for t, what in ((res, "res"), (shared_out, "shared_out"), (y_out, "y_out")):
-        _rows_typed(t, out, what)
+    if ((res is not None and (res.dtype != t or res.shape != s)) or
+            (shared_out is not None and (shared_out.dtype != t or shared_out.shape != s)) or
+            (y_out is not None and (y_out.dtype != t or y_out.shape != s))):
+        raise ValueError(f"res, shared_out, y_out: {t} [{T}, {H}]")
+    _check_post(t, s, post_w, next_w, next_n, rstd, next_rstd)
+    kind = MOE_GATE_NONE if gate is None else _gate_kind(gate, T, H, t)
     d = _device(out)
-    q = _post_params(d, out, eps, post_w, gate, scale, next_w, next_n, rstd, next_rstd)
-    pp, pi, pk, ph, pe, po, py, pr, pn, ps = _ptrs(d, y_perm, inv, topk_w, shared_out, res, out, y_out, rstd, next_n,
-                                                   next_rstd)
-    _call("moe_combine_post_norm", d, stream, pp, _code(out.dtype), T, H, k, pi, pk, ph, pe, q, po, py, pr, pn, ps)
+    pp, pi, pk, ph, pe, po, py, pr, pn, ps, pw, pg, px = _ptrs(d, y_perm, inv, topk_w, shared_out, res, out, y_out, rstd,
+                                                               next_n, next_rstd, post_w, gate, next_w)
+    _call("moe_combine_post_norm", d, stream, pp, _code(t), T, H, k, pi, pk, ph, pe,
+          moe_post_norm_params(pw, pg, kind, scale, eps, px), po, py, pr, pn, ps)
 
 
 def moe_norm_backward_workspace_size(T: int, H: int) -> int:
@@ -838,40 +837,40 @@ def moe_norm_backward_workspace_size(T: int, H: int) -> int:
 
 def moe_pre_norm_backward(dn, x, rstd, w, dx, dw, ws, dres=None, accumulate=False, stream=None):
     """dx [T, H] = dres + the gradient of moe_pre_norm's x; dw [H] float32 (or None).  dx may be dn or dres."""
-    T, H = x.shape
-    for t, what in ((dn, "dn"), (dx, "dx"), (dres, "dres")):
-        _rows_typed(t, x, what)
-    _channel(w, x, "w")
-    _token(rstd, T, "rstd")
-    if dw is not None:
-        _typed(dw, torch.float32, (H,), "dw")
+    t, s = x.dtype, x.shape
+    T, H = s
+    if (dn.dtype != t or dn.shape != s or dx.dtype != t or dx.shape != s or
+            (dres is not None and (dres.dtype != t or dres.shape != s))):
+        raise ValueError(f"dn, dx, dres: {t} [{T}, {H}]")
+    if w.dtype != t or w.shape != (H,) or rstd.dtype != torch.float32 or rstd.shape != (T,):
+        raise ValueError(f"w: {t} [{H}], rstd: float32 [{T}]")
+    if dw is not None and (dw.dtype != torch.float32 or dw.shape != (H,)):
+        raise ValueError(f"dw: float32 [{H}]")
     d = _device(x)
     pd, px, pr, pw, pe, po, pg, ps = _ptrs(d, dn, x, rstd, w, dres, dx, dw, ws)
-    _call("moe_pre_norm_backward", d, stream, pd, px, _code(x.dtype), T, H, pr, pw, pe, po, pg, 1 if accumulate else 0,
-          ps, _nbytes(ws))
+    _call("moe_pre_norm_backward", d, stream, pd, px, _code(t), T, H, pr, pw, pe, po, pg, 1 if accumulate else 0, ps,
+          _nbytes(ws))
 
 
 def moe_post_norm_backward(dout, y, dy, ws, rstd=None, post_w=None, dpost_w=None, gate=None, dgate=None,
                            scale: float = 1.0, accumulate=False, stream=None):
     """Gradients of moe_post_norm's out: dy [T, H], dpost_w [H] float32 (or None), dgate (or None): float32 [H] or
     [T, 1], or [T, H] of y's type, as the gate.  The residual's gradient is dout."""
-    T, H = y.shape
-    _rows_typed(dout, y, "dout")
-    _rows_typed(dy, y, "dy")
-    _channel(post_w, y, "post_w")
-    _token(rstd, T, "rstd")
-    kind = _gate_kind(gate, y)
-    if dpost_w is not None:
-        _typed(dpost_w, torch.float32, (H,), "dpost_w")
-    if dgate is not None:
-        if gate is None:
-            raise ValueError("dgate goes with gate")
-        _typed(dgate, y.dtype if kind == MOE_GATE_FULL else torch.float32, gate.shape, "dgate")
+    t, s = y.dtype, y.shape
+    T, H = s
+    if dout.dtype != t or dout.shape != s or dy.dtype != t or dy.shape != s:
+        raise ValueError(f"dout, dy: {t} [{T}, {H}]")
+    _check_post(t, s, post_w, None, None, rstd, None)
+    kind = MOE_GATE_NONE if gate is None else _gate_kind(gate, T, H, t)
+    if dpost_w is not None and (dpost_w.dtype != torch.float32 or dpost_w.shape != (H,)):
+        raise ValueError(f"dpost_w: float32 [{H}]")
+    if dgate is not None and (gate is None or dgate.dtype != (t if kind == MOE_GATE_FULL else torch.float32) or
+                              dgate.shape != gate.shape):
+        raise ValueError("dgate: of the gate's shape, float32 (a full gate's: of its type)")
     d = _device(y)
     pd, py, po, ps, pr, pw, pc, pg, pt = _ptrs(d, dout, y, dy, ws, rstd, post_w, dpost_w, gate, dgate)
-    q = moe_post_norm_params(pw, pg, kind, scale, 1.0, None)
-    _call("moe_post_norm_backward", d, stream, pd, py, _code(y.dtype), T, H, pr, q, po, pc, pt, 1 if accumulate else 0,
-          ps, _nbytes(ws))
+    _call("moe_post_norm_backward", d, stream, pd, py, _code(t), T, H, pr,
+          moe_post_norm_params(pw, pg, kind, scale, 1.0, None), po, pc, pt, 1 if accumulate else 0, ps, _nbytes(ws))
 
 
 class DboContext:
