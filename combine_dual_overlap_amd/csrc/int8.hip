@@ -186,10 +186,10 @@ struct I8Shape {
   static constexpr int TG = F32 || TH == 1 ? 1 : 2;
   static constexpr int STAGE = (BM + BN) * BK * 2;
   static constexpr int NQA = BM / (8 * NW), NQB = BN / (8 * NW);  // DMAs per wave and stage: 8 rows each
-  static constexpr int NDMA = NQA + NQB;
+  static constexpr int NDMA = NQB + 1;                          // at least: rows of a that do not exist are not loaded
   static constexpr int SLOTS = 4;                               // tiles whose scales are in LDS: NBUF + 1 at most
   static_assert(NQA * 8 * NW == BM && NQB * 8 * NW == BN && NW % 4 == 0, "DMA split");
-  static_assert((BM + 63) / 64 + BN / 64 <= NW && NBUF < SLOTS && (NBUF - 1) * NDMA < 64, "scales, ring, vmcnt");
+  static_assert((BM + 63) / 64 + BN / 64 <= NW && NBUF < SLOTS && (NBUF - 1) * (NQA + NQB) < 64, "scales, ring, vmcnt");
   // the XORs that rows put on their 16-byte chunks: the eight lanes that read together
   // hit rows of both parities and four keys
   static __device__ __forceinline__ int key_a(int r) { return r & 7; }
@@ -208,7 +208,7 @@ struct I8Tile {
 template <int EPI, bool F32, int BM, int BN, int WAVES_M, int WAVES_N, int NBUF>
 __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Params ip) {
   using S = I8Shape<EPI, F32, BM, BN, WAVES_M, WAVES_N, NBUF>;
-  constexpr int BK = S::BK, NW = S::NW, WM = S::WM, WN = S::WN, TM = S::TM, TN = S::TN, TH = S::TH, TG = S::TG;
+  constexpr int BK = S::BK, NW = S::NW, WN = S::WN, TM = S::TM, TN = S::TN, TH = S::TH, TG = S::TG;
   __shared__ __attribute__((aligned(1024))) uint8_t ring[NBUF * S::STAGE];
   __shared__ float s_scale[S::SLOTS][BM + BN];
   __shared__ __attribute__((aligned(16))) int s_first[256];     // the expert's first tile
@@ -262,7 +262,8 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Pa
     t.nt = __builtin_amdgcn_readfirstlane(r / high);
     t.m_n = __builtin_amdgcn_readfirstlane(min(height, rows - m_off));
     t.row = __builtin_amdgcn_readfirstlane(s_row0[e] + m_off);
-    t.tm = __builtin_amdgcn_readfirstlane(min(TM, max(0, (t.m_n - wm * WM + 15) / 16)));
+    // subtiles of 16 rows go to the waves in turn: a tile that is not full keeps them all busy
+    t.tm = __builtin_amdgcn_readfirstlane(((t.m_n + 15) / 16 - wm + WAVES_M - 1) / WAVES_M);
     return t;
   };
 
@@ -276,6 +277,7 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Pa
   const int64_t row_bytes = static_cast<int64_t>(p.K) * 2;
   const uint8_t *a_base, *b_base;                    // uniform
   uint32_t a_off[S::NQA], b_off[S::NQB];             // this lane's chunks
+  int a_dmas = 0;                                    // of this wave and stage: those with rows of the tile
   int L_in = L0, kt_in = 0, issued = 0, tile_in = 0;
   // A DMA takes eight rows: lane l the row l / 8 of them and chunk (l % 8) ^ key, a key
   // that does not depend on which of the wave's DMAs it is.
@@ -285,6 +287,7 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Pa
     const I8Tile t = locate(L);
     a_base = static_cast<const uint8_t*>(p.A) + t.row * row_bytes;
     const int m_last = t.m_n - 1;                    // rows and columns behind the last are its copies
+    a_dmas = (t.m_n + 8 * NW - 1) / (8 * NW);
 #pragma unroll
     for (int i = 0; i < S::NQA; ++i)
       a_off[i] = min(8 * (i * NW + wave) + lr, m_last) * static_cast<uint32_t>(row_bytes) + chunk_a * 16;
@@ -322,13 +325,15 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Pa
     const uint8_t *as = a_base + kt_in * (BK * 2), *bs = b_base + kt_in * (BK * 2);
     if (left >= BK) {
 #pragma unroll
-      for (int i = 0; i < S::NQA; ++i) lds_dma16_at(at + i * NW * 1024, as, a_off[i]);
+      for (int i = 0; i < S::NQA; ++i)
+        if (i < a_dmas) lds_dma16_at(at + i * NW * 1024, as, a_off[i]);
 #pragma unroll
       for (int i = 0; i < S::NQB; ++i) lds_dma16_at(at + BM * 128 + i * NW * 1024, bs, b_off[i]);
     } else {                                         // the reduction ends inside the stage: zeros behind it
 #pragma unroll
       for (int i = 0; i < S::NQA; ++i)
-        lds_dma16(at + i * NW * 1024, chunk_a * 8 < left ? static_cast<const void*>(as + a_off[i]) : g_zero16);
+        if (i < a_dmas)
+          lds_dma16(at + i * NW * 1024, chunk_a * 8 < left ? static_cast<const void*>(as + a_off[i]) : g_zero16);
 #pragma unroll
       for (int i = 0; i < S::NQB; ++i)
         lds_dma16(at + BM * 128 + i * NW * 1024, chunk_b * 8 < left ? static_cast<const void*>(bs + b_off[i]) : g_zero16);
@@ -348,7 +353,7 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Pa
     return *reinterpret_cast<const i32x4_t*>(tile + r * (BK * 2) + (((kk * 4 + g) ^ key) << 4));
   };
   auto read_a = [&](int s, int kk, int i) {
-    const int r = wm * WM + i * 16 + l15;
+    const int r = (i * WAVES_M + wm) * 16 + l15;
     af[i] = frag(ring + (s % NBUF) * S::STAGE, r, S::key_a(r), kk);
   };
   auto read_b = [&](int s, int kk, int set) {
@@ -431,7 +436,7 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Pa
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       if (i >= tm) break;
-      const int in = wm * WM + i * 16 + l15;
+      const int in = (i * WAVES_M + wm) * 16 + l15;
       if (in >= t.m_n) continue;
       const float as = sc[in];
       f32x4_t v[TN];
@@ -465,6 +470,16 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Pa
 
 // ---- host -----------------------------------------------------------------------
 
+// Tiles, from the sizes alone; us on both sides of each border (N x K, uniform rows):
+//   32 x 128 for up to 32 rows an expert, and while their grid is no more than what
+//   runs at once: 512 rows x 2048 x 2048 9.8 against 14.9 with 128 x 128, 1024 rows
+//   12.7 / 15.5, 2048 rows 22.4 / 16.8; 451 rows of 8 experts x 784 x 1504 8.4 / 12.0.
+//   256 x 256 where there are 256 of them, from 129 rows an expert on: 64 experts x 2048
+//   x 1408, 156 rows 47 against 52, 192 rows 51 / 55, 375 rows 101 / 111, 512 rows 131 /
+//   148; but 256 rows 89 / 73 and 312 rows 92 / 91 (1408 x 2048 gate/up: 161 / 148):
+//   about half of such experts need a second, short tile.
+//   (64 x 128 lies between its neighbours; 256 x 256 and 128 x 128 in four half stages
+//   are 5 to 15 % slower.)
 template <int EPI>
 static moe_status launch_int8(I8Params& p, hipStream_t s) {
   const int64_t cap = p.g.cap, rows = cap / p.g.E;
@@ -474,9 +489,9 @@ static moe_status launch_int8(I8Params& p, hipStream_t s) {
     return max_row_tiles(cap, p.g.E, BM, dense) * ((p.g.N + width - 1) / width);
   };
   int BM = 128, BN = 128;
-  if (rows <= 32)
+  if (rows <= 32 || tiles(32, 128) <= 512)
     BM = 32;
-  else if (rows > 128 && tiles(256, 256) >= 256)
+  else if (rows > 128 && !(rows > 224 && rows <= 320) && tiles(256, 256) >= 256)
     BM = BN = 256;
   const int width = EPI == EPI_SWIGLU ? BN / 2 : BN;
   p.g.n_tiles = (p.g.N + width - 1) / width;
