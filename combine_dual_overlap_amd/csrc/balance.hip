@@ -11,8 +11,9 @@ namespace dbomoe {
 // bias: experts are chosen by p + b (groups by the sum of their group_topn best),
 // and weighted by p alone.  Scores and sums are kept in 64 bits: the bias brings
 // experts close to each other on purpose, and what is chosen must not hang on the
-// rounding of a score.  (Logits that the caller already has: 4096 x 256 of them
-// are 4 MB, under 1 us of HBM time; the steps of the selection bound it.)
+// rounding of a score.  4096 x 256 logits are 4 MB, under 1 us of HBM time: the steps
+// of the selection bound it.  One wave takes a token, so that a maximum is six DPP
+// instructions; 256 tokens x 6 of 64 3.9 us, 4096 x 8 of 256 in 4 of 8 groups 12.
 // An expert whose logit is -inf or NaN has score 0 and is chosen only when no
 // other is left; a logit of +inf counts as the largest finite one.
 struct SelectParams {

@@ -460,7 +460,7 @@ moe_status moe_adamw_step(const void* table_host, const void* table_dev, const m
  *   loss [1] fp32 out   = coef / T * sum_t sum_e f_e q_te
  *   dlogits [T, E], fp32 or bf16 (dl): coef / T q_te (f_e - sum_j f_j q_tj), times
  *                1 - p_te (sigmoid); accumulate 1: added to what is there, rounded once
- *   ws           moe_route_balance_loss_workspace_size(T, E) bytes
+ *   ws           moe_route_balance_loss_workspace_size(T, E) bytes (calls that may overlap: one each)
  * Of params only E and score are used.  Masked logits (-inf, NaN) have q = 0 and no
  * gradient.  T == 0: loss = 0.
  * ------------------------------------------------------------------------- */
@@ -503,7 +503,7 @@ moe_status moe_route_balance_loss(const float* logits, int64_t T, const int32_t*
  * moe_grouped_ffn_int8 - a whole expert: moe_grouped_swiglu_int8 with h in fp32,
  *   h quantised as moe_quant_int8_rows does, and the product with w2 [E_loc, H, I],
  *   w2_scale [E_loc, H]; y [cap_rows, H] bf16.
- *   ws  moe_ffn_int8_workspace_size(cap_rows, I) bytes
+ *   ws  moe_ffn_int8_workspace_size(cap_rows, I) bytes (calls that may overlap: one each)
  * Rows outside the experts' ranges are left as they are.  N % 8 == 0 and K % 16 == 0
  * (the FFN: H and I both multiples of 16), else MOE_ERR_MISALIGNED; K <= 2^17 (the sums
  * stay in int32) and N <= 2^22; E_loc <= 256.  Integers are -127 .. 127 (-128 is
@@ -556,7 +556,8 @@ moe_status moe_grouped_ffn_int8(const int8_t* xq, const float* xq_scale, int32_t
  *   the forward pass (next_w is not used).
  * accumulate 1: dw, dpost_w and a channel gate's dgate are added to (dx, dy and the other
  * gates' are written).  Column sums are added in a fixed order.
- *   ws  moe_norm_backward_workspace_size(T, H) bytes (for dw, dpost_w or a channel's dgate)
+ *   ws  moe_norm_backward_workspace_size(T, H) bytes (for dw, dpost_w or a channel's dgate; calls
+ *       that may overlap: one each)
  * A row is at most 64 KB; H * sizeof(act) % 16 == 0; T < 2^22; eps > 0.
  * ------------------------------------------------------------------------- */
 typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 } moe_gate_kind;
