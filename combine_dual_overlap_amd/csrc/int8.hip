@@ -227,6 +227,10 @@ struct I8Params {
 // scaled and stored.
 //  - Every wave keeps the whole tile map (experts' rows and first tiles) in LDS.
 //  - The tile's scales come to LDS as its first stage does.
+//  - Of eight waves four load, one on each SIMD: while a stage's DMAs queue up (64 of
+//    16 clocks), the SIMD's other wave goes on with its MFMAs.  All eight loading
+//    against four: prefill gate/up 284 / 266 us, down 170 / 165, 8192^3 of zeros 423 /
+//    395 (of random integers 545 / 538: the clock gives way to the power).
 //  - The second operand's rows are dealt to the MFMA's positions so that a lane ends
 //    up with 16 bytes of consecutive columns of its row and stores them as they are
 //    (64 bytes of a row by four lanes): position q of TG neighbouring subtiles is row
@@ -239,10 +243,11 @@ struct I8Shape {
   static constexpr int TH = EPI == EPI_SWIGLU ? TN / 2 : TN;    // subtiles of output columns
   static constexpr int TG = F32 || TH == 1 ? 1 : 2;
   static constexpr int STAGE = (BM + BN) * BK * 2;
-  static constexpr int NQA = BM / (8 * NW), NQB = BN / (8 * NW);  // DMAs per wave and stage: 8 rows each
+  static constexpr int NI = NW == 8 ? 4 : NW;                   // waves that load
+  static constexpr int NQA = BM / (8 * NI), NQB = BN / (8 * NI);  // their DMAs per stage: 8 rows each
   static constexpr int NDMA = NQB + 1;                          // at least: rows of a that do not exist are not loaded
   static constexpr int SLOTS = 4;                               // tiles whose scales are in LDS: NBUF + 1 at most
-  static_assert(NQA * 8 * NW == BM && NQB * 8 * NW == BN && NW % 4 == 0, "DMA split");
+  static_assert(NQA * 8 * NI == BM && NQB * 8 * NI == BN && NI % 4 == 0, "DMA split");
   static_assert((BM + 63) / 64 + BN / 64 <= NW && NBUF < SLOTS && (NBUF - 1) * (NQA + NQB) < 64, "scales, ring, vmcnt");
   // the XORs that rows put on their 16-byte chunks: the eight lanes that read together
   // hit rows of both parities and four keys
@@ -262,7 +267,7 @@ struct I8Tile {
 template <int EPI, bool F32, int BM, int BN, int WAVES_M, int WAVES_N, int NBUF>
 __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Params ip) {
   using S = I8Shape<EPI, F32, BM, BN, WAVES_M, WAVES_N, NBUF>;
-  constexpr int BK = S::BK, NW = S::NW, WN = S::WN, TM = S::TM, TN = S::TN, TH = S::TH, TG = S::TG;
+  constexpr int BK = S::BK, NW = S::NW, NI = S::NI, WN = S::WN, TM = S::TM, TN = S::TN, TH = S::TH, TG = S::TG;
   __shared__ __attribute__((aligned(1024))) uint8_t ring[NBUF * S::STAGE];
   __shared__ float s_scale[S::SLOTS][BM + BN];
   __shared__ __attribute__((aligned(16))) int s_first[256];     // the expert's first tile
@@ -295,7 +300,7 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Pa
   const int R = __builtin_amdgcn_readfirstlane(__float_as_int(s_scale[0][0]));
   __syncthreads();
   // Workgroup b runs on XCD b % 8, which walks a contiguous run of tiles.
-  const int per = (R + 7) / 8, xcd = blockIdx.x & 7, step = gridDim.x >> 3;
+  const int per = (R + 7) / 8, xcd = blockIdx.x & 7, stride = gridDim.x >> 3;
   const int stop = min((xcd + 1) * per, R);
   const int L0 = xcd * per + (blockIdx.x >> 3);
   if (L0 >= stop) return;
@@ -330,30 +335,31 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Pa
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) float*)(&s_scale[0][0])));
   const int64_t row_bytes = static_cast<int64_t>(p.K) * 2;
   const uint8_t *a_base, *b_base;                    // uniform
-  uint32_t a_off[S::NQA], b_off[S::NQB];             // this lane's chunks
   int a_dmas = 0;                                    // of this wave and stage: those with rows of the tile
+  uint32_t a_last, b_most;                           // the lane's chunk of the last of them; the last columns' rows
   int L_in = L0, kt_in = 0, issued = 0, tile_in = 0;
   // A DMA takes eight rows: lane l the row l / 8 of them and chunk (l % 8) ^ key, a key
-  // that does not depend on which of the wave's DMAs it is.
+  // that does not depend on which of the wave's DMAs it is.  So a lane's offsets are the
+  // same in all of them, from bases that stay in scalar registers, but for the last rows
+  // of a.
   const int lr = lane >> 3, pos = lane & 7;
   const int chunk_a = pos ^ S::key_a(lr), chunk_b = pos ^ S::key_b(8 * wave + lr);
+  const uint32_t step8 = static_cast<uint32_t>(row_bytes) * 8, step = step8 * NI;
+  const uint32_t a_off = (8 * wave + lr) * static_cast<uint32_t>(row_bytes) + chunk_a * 16;
+  const uint32_t b_off = lr * static_cast<uint32_t>(row_bytes) + chunk_b * 16;
   auto open_tile = [&](int L) {
     const I8Tile t = locate(L);
     a_base = static_cast<const uint8_t*>(p.A) + t.row * row_bytes;
     const int m_last = t.m_n - 1;                    // rows and columns behind the last are its copies
-    a_dmas = (t.m_n + 8 * NW - 1) / (8 * NW);
-#pragma unroll
-    for (int i = 0; i < S::NQA; ++i)
-      a_off[i] = min(8 * (i * NW + wave) + lr, m_last) * static_cast<uint32_t>(row_bytes) + chunk_a * 16;
+    a_dmas = (t.m_n + 8 * NI - 1) / (8 * NI);
+    a_last = min(8 * ((a_dmas - 1) * NI + wave) + lr, m_last) * static_cast<uint32_t>(row_bytes) + chunk_a * 16;
     const int col0 = t.nt * (EPI == EPI_SWIGLU ? BN / 2 : BN);
     const int n_last = p.N - 1 - col0;
     // row of b of row x of the tile (SwiGLU: half a tile of gate rows, then the matching up rows)
     auto row_of = [&](int x) {
       return EPI == EPI_SWIGLU ? min(x & (BN / 2 - 1), n_last) + (x < BN / 2 ? 0 : p.N) : min(x, n_last);
     };
-#pragma unroll
-    for (int i = 0; i < S::NQB; ++i)
-      b_off[i] = row_of(8 * (i * NW + wave) + lr) * static_cast<uint32_t>(row_bytes) + chunk_b * 16;
+    b_most = (min(n_last, BN - 1) - 7) * static_cast<uint32_t>(row_bytes);   // (columns come in eights)
     b_base = static_cast<const uint8_t*>(p.B) + (static_cast<int64_t>(t.e) * brows + col0) * row_bytes;
     // the scales: 64 rows or columns by each wave
     constexpr int WA = (BM + 63) / 64;
@@ -368,7 +374,7 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Pa
   };
   auto issue = [&]() {
     if (kt_in == KT) {
-      L_in += step;
+      L_in += stride;
       kt_in = 0;
       ++tile_in;
     }
@@ -377,20 +383,33 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Pa
     const uint32_t at = lds0 + (issued % NBUF) * S::STAGE + wave * 1024;
     const int left = p.K - kt_in * BK;
     const uint8_t *as = a_base + kt_in * (BK * 2), *bs = b_base + kt_in * (BK * 2);
-    if (left >= BK) {
+    if (NI == NW || wave < NI) {
+      // rows of b of DMA i (SwiGLU: gate rows, then up rows)
+      constexpr int HALF = EPI == EPI_SWIGLU ? S::NQB / 2 : S::NQB;
+      auto b_at = [&](int i) {
+        const uint32_t up = i < HALF ? 0 : static_cast<uint32_t>(p.N) * static_cast<uint32_t>(row_bytes);
+        return bs + min(wave * step8 + i % HALF * step, b_most) + up;
+      };
+      if (left >= BK) {
 #pragma unroll
-      for (int i = 0; i < S::NQA; ++i)
-        if (i < a_dmas) lds_dma16_at(at + i * NW * 1024, as, a_off[i]);
+        for (int i = 0; i < S::NQA; ++i) {
+          if (i < a_dmas - 1)
+            lds_dma16_at(at + i * NI * 1024, as + i * step, a_off);
+          else if (i == a_dmas - 1)
+            lds_dma16_at(at + i * NI * 1024, as, a_last);
+        }
 #pragma unroll
-      for (int i = 0; i < S::NQB; ++i) lds_dma16_at(at + BM * 128 + i * NW * 1024, bs, b_off[i]);
-    } else {                                         // the reduction ends inside the stage: zeros behind it
+        for (int i = 0; i < S::NQB; ++i) lds_dma16_at(at + BM * 128 + i * NI * 1024, b_at(i), b_off);
+      } else {                                       // the reduction ends inside the stage: zeros behind it
 #pragma unroll
-      for (int i = 0; i < S::NQA; ++i)
-        if (i < a_dmas)
-          lds_dma16(at + i * NW * 1024, chunk_a * 8 < left ? static_cast<const void*>(as + a_off[i]) : g_zero16);
+        for (int i = 0; i < S::NQA; ++i) {
+          const uint8_t* src = as + (i < a_dmas - 1 ? i * step + a_off : a_last);
+          if (i < a_dmas) lds_dma16(at + i * NI * 1024, chunk_a * 8 < left ? static_cast<const void*>(src) : g_zero16);
+        }
 #pragma unroll
-      for (int i = 0; i < S::NQB; ++i)
-        lds_dma16(at + BM * 128 + i * NW * 1024, chunk_b * 8 < left ? static_cast<const void*>(bs + b_off[i]) : g_zero16);
+        for (int i = 0; i < S::NQB; ++i)
+          lds_dma16(at + BM * 128 + i * NI * 1024, chunk_b * 8 < left ? static_cast<const void*>(b_at(i) + b_off) : g_zero16);
+      }
     }
     ++kt_in;
     ++issued;
@@ -469,7 +488,7 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Pa
   for (int i = 0; i < TM; ++i) read_a(0, 0, i);
   int s = 0, tile = 0;
 #pragma unroll 1
-  for (int L = L0; L < stop; L += step, ++tile) {
+  for (int L = L0; L < stop; L += stride, ++tile) {
     const I8Tile t = locate(L);
     tm = t.tm;
 #pragma unroll
