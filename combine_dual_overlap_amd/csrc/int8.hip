@@ -541,9 +541,98 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_grouped_int8(I8Pa
   }
 }
 
+// Few tiles: one workgroup per 32 x 32 outputs (SwiGLU: 16 gate and 16 up columns), its
+// eight waves each with every eighth 128 bytes of the reduction, fragments loaded straight
+// from memory, the eight sums joined through LDS.  No barrier until then: where the tiled
+// kernel takes 0.42 us a stage whatever is in it, a short call is two or three memory
+// round trips.  One row x 2048 x 2048 9.2 -> 5.2 us, x 1024 x 7168 23 -> 10; 64 rows of 4
+// experts x 2048 x 1408 7.9 -> 5.9.  (256 bytes or more at a time: 3 to 30 % slower.)
+template <int EPI, bool F32>
+__global__ __launch_bounds__(512) void k_grouped_int8_few(I8Params ip) {
+  constexpr int BM = 32, NW = 8;
+  __shared__ i32x4_t red[NW][4][64];
+  __shared__ int s_loc[8];
+  const GgParams& p = ip.g;
+  GgTile t;
+  if (!gg_locate<MOE_GEMM_NT, BM>(p, s_loc, t)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l15 = lane & 15, g = lane >> 4;                   // fragment: position l15, bytes 16 g .. 16 g + 15 of 64
+  const int c0 = t.nt * (EPI == EPI_SWIGLU ? 16 : 32);
+  const int brows = EPI == EPI_SWIGLU ? 2 * p.N : p.N;
+  const int64_t row_bytes = static_cast<int64_t>(p.K) * 2;
+  const int64_t row0 = t.row0 + t.m_off;
+  const bool two = t.m_n > 16;
+  const uint8_t *a[2], *b[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    a[i] = static_cast<const uint8_t*>(p.A) + (row0 + min(i * 16 + l15, t.m_n - 1)) * row_bytes + g * 16;
+    const int col = EPI == EPI_SWIGLU ? min(c0 + l15, p.N - 1) + i * p.N : min(c0 + i * 16 + l15, p.N - 1);
+    b[i] = static_cast<const uint8_t*>(p.B) + (static_cast<int64_t>(t.e) * brows + col) * row_bytes + g * 16;
+  }
+  // the scales of what this wave will finish: subtile (wave >> 1, wave & 1)
+  const int fi = wave >> 1 & 1, fj = wave & 1, in = fi * 16 + l15;
+  const int col = c0 + (EPI == EPI_SWIGLU ? 0 : fj * 16) + g * 4;
+  const float as = ip.as[row0 + min(in, t.m_n - 1)];
+  const float* bs = ip.bs + static_cast<int64_t>(t.e) * brows + min(col, p.N - 4);
+  const f32x4_t bs0 = *reinterpret_cast<const f32x4_t*>(bs);
+  const f32x4_t bs1 = EPI == EPI_SWIGLU ? *reinterpret_cast<const f32x4_t*>(bs + p.N) : bs0;
+  const i32x4_t zero = {0, 0, 0, 0};
+  i32x4_t acc[2][2] = {{zero, zero}, {zero, zero}};
+  const int lines = (static_cast<int>(row_bytes) + 127) / 128;
+  for (int c = wave; c < lines; c += NW) {
+    i32x4_t av[2][2], bv[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = c * 128 + h * 64;
+      const bool there = k + g * 16 < row_bytes;              // K is a multiple of 16: a chunk or none
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        av[h][i] = there && (i == 0 || two) ? *reinterpret_cast<const i32x4_t*>(a[i] + k) : zero;
+        bv[h][i] = there ? *reinterpret_cast<const i32x4_t*>(b[i] + k) : zero;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (i == 0 || two) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bv[h][j], av[h][i], acc[i][j], 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) red[wave][i * 2 + j][lane] = acc[i][j];
+  __syncthreads();
+  auto sum = [&](int q) {
+    i32x4_t v = red[0][q][lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) v += red[w][q][lane];
+    return __builtin_convertvector(v, f32x4_t);
+  };
+  if (wave >= 4 || in >= t.m_n || col >= p.N) return;
+  f32x4_t v;
+  if constexpr (EPI == EPI_SWIGLU) {
+    if (fj) return;
+    const f32x4_t gate = sum(fi * 2) * as * bs0, up = sum(fi * 2 + 1) * as * bs1;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = silu(gate[x]) * up[x];
+  } else {
+    v = sum(wave) * as * bs0;
+  }
+  const int64_t at = (row0 + in) * p.N + col;
+  if constexpr (F32)
+    *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.C) + at) = v;
+  else
+    *reinterpret_cast<uint2*>(static_cast<bf16_t*>(p.C) + at) = make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
+}
+
 // ---- host -----------------------------------------------------------------------
 
 // Tiles, from the sizes alone; us on both sides of each border (N x K, uniform rows):
+//   32 x 32 outputs a workgroup up to 384 of them: 8 rows of 4 experts, 2048 -> 2 x 1408
+//   (352) 8.7 against 9.6, 128 dense rows x 2048 x 2048 (256) 7.0 / 9.8; 192 rows (384)
+//   10.6 / 9.9, 256 rows (512) 10.7 / 10.0, 400 rows 17.9 / 10.1.
 //   32 x 128 for up to 32 rows an expert, and while their grid is no more than what
 //   runs at once: 512 rows x 2048 x 2048 9.8 against 14.9 with 128 x 128, 1024 rows
 //   12.7 / 15.5, 2048 rows 22.4 / 16.8; 451 rows of 8 experts x 784 x 1504 8.4 / 12.0.
@@ -557,12 +646,15 @@ template <int EPI>
 static moe_status launch_int8(I8Params& p, hipStream_t s) {
   const int64_t cap = p.g.cap, rows = cap / p.g.E;
   const bool dense = !p.g.offsets;
-  auto tiles = [&](int BM, int BN) {
+  auto tiles = [&](int BM, int BN) {                 // at most, whatever the experts' rows
     const int64_t width = EPI == EPI_SWIGLU ? BN / 2 : BN;
-    return max_row_tiles(cap, p.g.E, BM, dense) * ((p.g.N + width - 1) / width);
+    const int64_t some = dense ? 0 : std::min<int64_t>(p.g.E, cap);    // experts with rows, at most
+    return (some + (cap - some + (dense ? BM - 1 : 0)) / BM) * ((p.g.N + width - 1) / width);
   };
   int BM = 128, BN = 128;
-  if (rows <= 32 || tiles(32, 128) <= 512)
+  if (tiles(32, 32) <= 384)
+    BM = BN = 32;
+  else if (rows <= 32 || tiles(32, 128) <= 512)
     BM = 32;
   else if (rows > 128 && !(rows > 224 && rows <= 320) && tiles(256, 256) >= 256)
     BM = BN = 256;
@@ -580,6 +672,8 @@ static moe_status launch_int8(I8Params& p, hipStream_t s) {
     constexpr bool F32 = decltype(f32)::value;
     if (BM == 256)
       go(k_grouped_int8<EPI, F32, 256, 256, 2, 4, 2>, 512, 1);
+    else if (BN == 32)
+      go(k_grouped_int8_few<EPI, F32>, 512, 1 << 20);
     else if (BM == 128)
       go(k_grouped_int8<EPI, F32, 128, 128, 2, 2, 2>, 256, 2);
     else

@@ -106,7 +106,11 @@ def test_dispatch(T, H, k, E, lo, hi, dt):
 
 PRODUCTS = [([1], 8, 16), ([5], 24, 48), ([0, 3, 0], 128, 128), ([31, 1, 33], 136, 272), ([64, 0, 65, 200], 264, 144),
             ([129, 300], 512, 256), ([1000], 72, 2048), ([700, 300, 257], 1024, 400), ([2], 2816, 2048),
-            ([260] * 40, 520, 128), ([3000], 2048, 64), ([128, 5, 0, 77], 384, 16)]
+            ([260] * 40, 520, 128), ([3000], 2048, 64), ([128, 5, 0, 77], 384, 16),
+            # tiles of 32 x 128 with few rows, 128 x 128 and 256 x 256 with ragged ones
+            ([1, 2] * 12, 1032, 272), ([0, 1, 31, 32, 33, 64, 5] + [2] * 8, 1416, 400), ([17] * 30, 520, 1040),
+            ([1] * 64, 264, 16), ([129, 500, 1, 127, 260], 4104, 80), ([600, 333, 511, 257, 513], 8200, 272),
+            ([513, 0, 1, 900], 12296, 64)]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
@@ -153,7 +157,8 @@ def test_product_extremes():
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("counts,I,H", [([1], 8, 16), ([0, 40, 3], 72, 48), ([33, 130], 136, 256), ([600, 300], 264, 128), ([300] * 9, 1032, 64)])
+@pytest.mark.parametrize("counts,I,H", [([1], 8, 16), ([0, 40, 3], 72, 48), ([33, 130], 136, 256), ([600, 300], 264, 128), ([300] * 9, 1032, 64),
+                                        ([1, 0, 17, 16] * 6, 392, 208), ([33, 300, 1] * 2, 2056, 144), ([600, 333, 511, 257, 513], 4104, 272)])
 def test_swiglu(counts, I, H, out):
     B = _B()
     g = torch.Generator().manual_seed(sum(counts) + I)
@@ -172,7 +177,7 @@ def test_swiglu(counts, I, H, out):
 
 
 @pytest.mark.parametrize("counts,H,I", [([1], 16, 16), ([3, 0, 50], 64, 48), ([130, 0, 257, 1], 256, 208), ([700], 144, 512),
-                                        ([280] * 10, 512, 96)])
+                                        ([280] * 10, 512, 96), ([1, 2, 0, 3] * 10, 528, 272), ([1, 1], 16, 8208)])
 def test_ffn(counts, H, I):
     B = _B()
     g = torch.Generator().manual_seed(sum(counts) + H)
