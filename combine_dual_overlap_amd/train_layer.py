@@ -52,8 +52,9 @@ class TrainLayer:
     counts the tokens of the last forward() by expert.  Not with forced ids.
 
     With a share of the experts (cfg.expert_begin, expert_end) out, dx and the
-    router's gradient are this share's part, to be summed over the shares; give the
-    shared experts to one share only, or their part is counted more than once.
+    router's gradient are this share's part, to be summed over the shares (and those
+    of the norm before the layer and of the gate); give the shared experts and the
+    balance loss to one share only, or their part is counted more than once.
     """
 
     def __init__(self, inp: dict, device: str = "cuda", T_max: int = None, grad_dtype=torch.float32,

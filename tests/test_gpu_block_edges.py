@@ -1,0 +1,203 @@
+"""What the balanced gate, the integer experts, the norms and the layer made of them allow beyond the ordinary call:
+gates per token in split layers, shares of the experts, single tokens, calls side by side on two streams."""
+import pytest
+import torch
+
+import block_oracle as O
+from test_gpu_block_layer import _inputs
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.mark.parametrize("kind", ["token", "full"])
+@pytest.mark.parametrize("cid,int8", [(5, True), (5, False), (1, False)])
+def test_gates_of_all_tokens_in_a_split_layer(kind, cid, int8):
+    """Each microbatch takes its own part of a gate per token or a full one."""
+    from combine_dual_overlap_amd import DeviceLayer, binding as B
+    cfg, inp = _inputs(cid, "f32" if cid == 1 else "bf16")
+    inp["block"].update(gate=None)
+    layer, T = DeviceLayer(inp, int8=int8), cfg.T
+    x = inp["x"].to(DEV)
+    g = torch.Generator().manual_seed(3)
+    gate = torch.randn(T, 1, generator=g).to(DEV) if kind == "token" else torch.randn(T, cfg.H, generator=g).to(x.dtype).to(DEV)
+    b = layer.block
+    layer.block_params.post.gate = gate.data_ptr()
+    layer.block_params.post.gate_kind = B.MOE_GATE_TOKEN if kind == "token" else B.MOE_GATE_FULL
+    for schedule, kw in (("unsplit", {}), ("dbo", {}), ("serial", dict(split_at=1)), ("dbo_recv_hook", dict(split_at=T - 3))):
+        layer.out.fill_(9)
+        got = layer.run(schedule, **kw).clone()
+        # by halves, each an unsplit layer of its tokens with its part of the gate
+        T0 = T if schedule == "unsplit" else kw.get("split_at", (T + 1) // 2)
+        want = []
+        for lo, hi in ((0, T0), (T0, T)):
+            if lo == hi:
+                continue
+            part = gate[lo:hi].clone()
+            layer.block_params.post.gate = part.data_ptr()
+            forced = None if layer.forced_ids is None else layer.forced_ids[lo:hi].clone()
+            want.append(layer.run("unsplit", x=x[lo:hi].clone(), out=torch.empty_like(x[lo:hi]), forced_ids=forced).clone())
+            torch.cuda.synchronize()
+        layer.block_params.post.gate = gate.data_ptr()
+        if int8 or cid == 1:
+            assert torch.equal(got, torch.cat(want)), schedule
+        else:
+            # the bf16 experts' tiles follow the number of tokens, and with them the order of fp32 sums: a rounding of
+            # h (half a step, 2^-8) moves y by up to that, three roundings (h, y_perm, out) of either side
+            w = torch.cat(want).double()
+            assert float((got.double() - w).norm() / w.norm()) < 6 * 2.0 ** -8, schedule
+    # and the gate is applied: against the layer's sum without norm and residual
+    layer.block_params.post.gate_kind, layer.block_params.post.gate = B.MOE_GATE_NONE, None
+    assert not torch.equal(layer.run("unsplit"), want[0][:T] if len(want) == 1 else torch.cat(want))
+
+
+@pytest.mark.parametrize("T", [1, 2, 3])
+@pytest.mark.parametrize("cid", [2, 5])
+def test_few_tokens(cid, T):
+    """A block of one, two and three tokens: every schedule gives the bits of its parts."""
+    from combine_dual_overlap_amd import DeviceLayer
+    cfg, inp = _inputs(cid, shared=False)
+    layer = DeviceLayer(inp, int8=True)
+    x = inp["x"][:T].clone().to(DEV)
+    rows = [layer.run("unsplit", x=x[t:t + 1].clone(), out=torch.empty_like(x[:1])).clone() for t in range(T)]
+    for schedule in ("unsplit", "serial", "dbo", "dbo_recv_hook"):
+        out = torch.full_like(x, 9)
+        layer.run(schedule, x=x, out=out)
+        torch.cuda.synchronize()
+        # (the router's product has the same split for one token as for three)
+        assert torch.equal(out, torch.cat(rows)), schedule
+
+
+def test_shares_of_the_experts_add_up():
+    """Two shares of a layer with a norm before it, a gate and a selection bias; the balance loss with one of them."""
+    from combine_dual_overlap_amd import TrainLayer
+    cfg, inp = _inputs(1, "f32")
+    inp["block"].update(post_norm=None, residual=False)
+    half = cfg.E // 2
+    whole = TrainLayer(inp, balance_coef=0.5, bias_rate=0.25)
+    shares = []
+    for lo, hi, coef in ((0, half, 0.5), (half, cfg.E, 0.0)):
+        part = dict(inp, cfg=cfg.replace(expert_begin=lo, expert_end=hi), w13=inp["w13"][lo:hi], w2=inp["w2"][lo:hi])
+        shares.append(TrainLayer(part, balance_coef=coef, bias_rate=0.25))
+    x = inp["x"].to(DEV)
+    dout = torch.randn(x.shape, generator=torch.Generator().manual_seed(8)).to(DEV)
+    out, outs = whole.forward(x), [s.forward(x) for s in shares]
+    dx, dxs = whole.backward(dout), [s.backward(dout) for s in shares]
+    # chains of six sums of at most 4096 terms, in another order: sqrt(4096) * 2^-24 of the value each
+    near = lambda a, b: float((a - b).norm() / b.norm()) < 6 * 64 * 2.0 ** -24
+    assert near(outs[0] + outs[1], out) and near(dxs[0] + dxs[1], dx)
+    assert torch.equal(shares[0].balance_loss, whole.balance_loss)
+    for name in ("pre_norm", "gate", "w_router"):
+        assert near(shares[0].grads[name] + shares[1].grads[name], whole.grads[name]), name
+    for name in ("w13", "w2"):
+        assert near(torch.cat([s.grads[name] for s in shares]), whole.grads[name]), name
+    for s in shares:
+        assert torch.equal(s.load, whole.load)
+
+
+def _tasks():
+    """Each operator's call on buffers of its own: (run, outputs)."""
+    from combine_dual_overlap_amd import binding as B
+    T, H, E, k, I = 700, 512, 64, 6, 320
+    g = torch.Generator(device=DEV).manual_seed(5)
+    rand = lambda *s: torch.randn(*s, device=DEV, generator=g)
+    new = lambda *s, dt=torch.float32: torch.empty(s, dtype=dt, device=DEV)
+    u8, bf, i8 = torch.uint8, torch.bfloat16, torch.int8
+    rp = B.route_params(E, k, "softmax", True)
+    logits, bias, load = rand(T, E), 0.01 * rand(E), torch.zeros(E, dtype=torch.int32, device=DEV)
+    ids, w = new(T, k, dt=torch.int32), new(T, k)
+    loss, dl, ws = new(1), new(T, E), new(B.moe_route_balance_loss_workspace_size(T, E), dt=u8)
+
+    def gate(s):
+        load.zero_()
+        B.moe_route_select(logits, rp, ids, w, select_bias=bias, load=load, stream=s)
+        B.moe_route_balance_loss(logits, load, rp, 0.5, loss, dl, ws, stream=s)
+
+    x, n = rand(T, H).to(bf), T * k
+    cnt, off = new(E, dt=torch.int32), new(E + 1, dt=torch.int32)
+    perm, inv, xq, xs = new(n, dt=torch.int32), new(n, dt=torch.int32), new(n, H, dt=i8), new(n)
+    wsd = new(max(256, B.moe_dispatch_workspace_size(T, k, E)), dt=u8)
+    w13, w2 = new(E, 2 * I, H, dt=i8), new(E, H, I, dt=i8)
+    s13, s2 = new(E, 2 * I), new(E, H)
+    B.moe_quant_int8_rows(0.05 * rand(E, 2 * I, H), w13, s13)
+    B.moe_quant_int8_rows(0.05 * rand(E, H, I), w2, s2)
+    y, wsf = torch.zeros(n, H, dtype=bf, device=DEV), new(B.moe_ffn_int8_workspace_size(n, I), dt=u8)
+    nw, out, nn, r1, r2 = rand(H).to(bf), new(T, H, dt=bf), new(T, H, dt=bf), new(T), new(T)
+    yo, dy, dw, dg, dx = new(T, H, dt=bf), new(T, H, dt=bf), new(H), new(H), new(T, H, dt=bf)
+    wsn = new(B.moe_norm_backward_workspace_size(T, H), dt=u8)
+
+    def experts(s):
+        B.moe_dispatch_int8(x, ids, E, 0, E, cnt, off, perm, inv, xq, xs, wsd, stream=s)
+        B.moe_grouped_ffn_int8(xq, xs, off, w13, s13, w2, s2, y, wsf, stream=s)
+        B.moe_combine_post_norm(y, inv, w, x, out, 1e-6, nw, nw, 0.5, y_out=yo, rstd=r1, next_w=nw, next_n=nn, next_rstd=r2, stream=s)
+        B.moe_post_norm_backward(out, yo, dy, wsn, r1, nw, dw, nw, dg, 0.5, stream=s)
+        B.moe_pre_norm_backward(nn, out, r2, nw, dx, dw, wsn, dres=dy, accumulate=True, stream=s)
+
+    def run(s):
+        with torch.cuda.stream(s):
+            gate(s)
+            experts(s)
+
+    return run, [ids, w, load, loss, dl, inv, xq, xs, y, out, nn, yo, dy, dw, dg, dx]
+
+
+def test_two_streams_at_once():
+    """The whole chain on two streams at once, eager and captured, each with its own buffers: the bits of one alone."""
+    (run_a, out_a), (run_b, out_b) = _tasks(), _tasks()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    run_a(sa)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in out_a]
+    for _ in range(10):
+        run_a(sa)
+        run_b(sb)
+    torch.cuda.synchronize()
+    for a, b, t in zip(out_a, out_b, want):
+        assert torch.equal(a, t) and torch.equal(b, t)
+    graphs = []
+    for run, s in ((run_a, sa), (run_b, sb)):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            run(s)
+        graphs.append(graph)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for t in out_a + out_b:
+            t.zero_()
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, (sa, sb)):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for a, b, t in zip(out_a, out_b, want):
+            assert torch.equal(a, t) and torch.equal(b, t)
+
+
+def test_gate_of_as_many_slots_as_experts():
+    """k = E = 16, and rows whose masks leave fewer or none."""
+    from combine_dual_overlap_amd import binding as B
+    T, E = 33, 16
+    g = torch.Generator().manual_seed(2)
+    logits, bias = torch.randn(T, E, generator=g), 0.1 * torch.randn(E, generator=g)
+    logits[1, 3:] = -float("inf")
+    logits[2] = -float("inf")
+    logits[3] = float("nan")
+    logits[4] = torch.finfo(torch.float32).min
+    logits[5] = float("inf")
+    rp = B.route_params(E, E, "softmax", True)
+    ids, w = torch.empty(T, E, dtype=torch.int32, device=DEV), torch.empty(T, E, device=DEV)
+    load = torch.zeros(E, dtype=torch.int32, device=DEV)
+    B.moe_route_select(logits.to(DEV), rp, ids, w, select_bias=bias.to(DEV), load=load)
+    ids, w = ids.cpu(), w.cpu()
+    assert torch.equal(ids.sort(1).values, torch.arange(E, dtype=torch.int32).repeat(T, 1))      # every expert once
+    order = torch.argsort(bias.double(), descending=True, stable=True).int()
+    assert torch.equal(ids[1, 3:], torch.arange(3, E, dtype=torch.int32)) and (w[1, 3:] == 0).all()
+    assert abs(float(w[1, :3].double().sum()) - 1) <= 3 * 2.0 ** -24
+    for t in (2, 3):                          # nothing left: the lowest indices, weight 0, not in the load
+        assert torch.equal(ids[t], torch.arange(E, dtype=torch.int32)) and (w[t] == 0).all()
+    for t in (4, 5):                          # all the same: the bias decides
+        assert torch.equal(ids[t], order) and ((w[t].double() - 1 / E).abs() <= 2.0 ** -24 / E).all()
+    want = torch.full((E,), T - 3)
+    want[:3] += 1
+    assert torch.equal(load.cpu(), want.int())
