@@ -201,3 +201,32 @@ def test_gate_of_as_many_slots_as_experts():
     want = torch.full((E,), T - 3)
     want[:3] += 1
     assert torch.equal(load.cpu(), want.int())
+
+
+@pytest.mark.parametrize("T,H,dt", [(5, 64, torch.float32), (300, 2048, torch.bfloat16), (9, 16384, torch.float32), (4100, 1024, torch.bfloat16)])
+@pytest.mark.parametrize("kind", ["none", "channel", "token", "full"])
+def test_norms_in_the_place_of_their_operands(T, H, dt, kind):
+    """out in res's place, dy in dout's, dx in dres's: the bits of separate tensors."""
+    from combine_dual_overlap_amd import binding as B
+    g = torch.Generator(device=DEV).manual_seed(T)
+    rand = lambda *s: torch.randn(*s, device=DEV, generator=g)
+    y, res, d = (rand(T, H).to(dt) for _ in range(3))
+    w = rand(H).to(dt)
+    gate = {"none": None, "channel": rand(H).to(dt), "token": rand(T, 1), "full": rand(T, H).to(dt)}[kind]
+    out, rstd = torch.empty_like(y), torch.empty(T, device=DEV)
+    B.moe_post_norm(y, res, out, 1e-6, w, gate, 0.5, rstd)
+    there = res.clone()
+    B.moe_post_norm(y, there, there, 1e-6, w, gate, 0.5)
+    assert torch.equal(there, out)
+    ws = torch.empty(B.moe_norm_backward_workspace_size(T, H), dtype=torch.uint8, device=DEV)
+    dgate = lambda: None if gate is None else torch.empty(gate.shape, dtype=torch.float32 if kind == "channel" else gate.dtype, device=DEV)
+    dy, dw, dg = torch.empty_like(y), torch.empty(H, device=DEV), dgate()
+    B.moe_post_norm_backward(d, y, dy, ws, rstd, w, dw, gate, dg, 0.5)
+    there, dw2, dg2 = d.clone(), torch.empty(H, device=DEV), dgate()
+    B.moe_post_norm_backward(there, y, there, ws, rstd, w, dw2, gate, dg2, 0.5)
+    assert torch.equal(there, dy) and torch.equal(dw, dw2) and (gate is None or torch.equal(dg, dg2))
+    dx = torch.empty_like(y)
+    B.moe_pre_norm_backward(d, y, rstd, w, dx, dw, ws, dres=res)
+    there = res.clone()
+    B.moe_pre_norm_backward(d, y, rstd, w, there, dw2, ws, dres=there)
+    assert torch.equal(there, dx) and torch.equal(dw, dw2)
