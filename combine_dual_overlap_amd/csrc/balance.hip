@@ -13,7 +13,8 @@ namespace dbomoe {
 // experts close to each other on purpose, and what is chosen must not hang on the
 // rounding of a score.  4096 x 256 logits are 4 MB, under 1 us of HBM time: the steps
 // of the selection bound it.  One wave takes a token, so that a maximum is six DPP
-// instructions; 256 tokens x 6 of 64 3.9 us, 4096 x 8 of 256 in 4 of 8 groups 12.
+// instructions; 256 tokens x 6 of 64 3 us, 4096 x 8 of 256 in 4 of 8 groups 9.2 (a lane
+// has neighbouring experts, so that a group is a team of lanes; by way of LDS 11.2).
 // An expert whose logit is -inf or NaN has score 0 and is chosen only when no
 // other is left; a logit of +inf counts as the largest finite one.
 struct SelectParams {
@@ -37,12 +38,15 @@ __device__ __forceinline__ uint32_t dpp_move(uint32_t v) {
   return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false));
 }
 
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double dpp_add_d(double v) {
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ double dpp_d(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
   const uint64_t lo = dpp_move<CTRL, ROWS>(static_cast<uint32_t>(b)), hi = dpp_move<CTRL, ROWS>(static_cast<uint32_t>(b >> 32));
-  return v + __builtin_bit_cast(double, hi << 32 | lo);
+  return __builtin_bit_cast(double, hi << 32 | lo);
 }
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add_d(double v) { return v + dpp_d<CTRL, ROWS>(v); }
 
 __device__ __forceinline__ double lane_of(double v, int lane) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
@@ -139,20 +143,30 @@ __global__ __launch_bounds__(64 * kSelTokens) void k_select(SelectParams p) {
   if (t < p.T) {
     const double NEG = -INFINITY;
     double* val = s_val[wave];
-    float l[NE], bias[NE];
+    // Lane l has experts l NE .. l NE + NE - 1.
+    typedef float some_t __attribute__((ext_vector_type(NE), aligned(4)));
+    const int e0 = lane * NE, have = min(max(E - e0, 0), NE);
+    auto get = [&](const float* row) {
+      some_t v = 0.f;
+      if (have == NE) {
+        v = *reinterpret_cast<const some_t*>(row + e0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+          if (i < have) v[i] = row[e0 + i];
+      }
+      return v;
+    };
+    float l[NE];
     bool cand[NE];                             // may be chosen
+    some_t sum_l = 0.f, bias = 0.f;
+    if (p.bias) bias = get(p.bias);
+    for (int s0 = 0; s0 < p.S; ++s0) sum_l += get(p.part + (s0 * p.T + t) * E);      // in split order
+    if (p.logit_bias) sum_l += get(p.logit_bias);
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      const int e = lane + 64 * i;
-      l[i] = -INFINITY;
-      bias[i] = 0.f;
-      if (e >= E) continue;
-      if (p.bias) bias[i] = p.bias[e];
-      float s = 0.f;
-      for (int s0 = 0; s0 < p.S; ++s0) s += p.part[(s0 * p.T + t) * E + e];     // in split order
-      if (p.logit_bias) s += p.logit_bias[e];
-      if (p.logits) p.logits[t * E + e] = s;
-      if (s > -INFINITY) l[i] = fminf(s, 3.402823466e38f);
+      if (p.logits && i < have) p.logits[t * E + e0 + i] = sum_l[i];
+      l[i] = i < have && sum_l[i] > -INFINITY ? fminf(sum_l[i], 3.402823466e38f) : -INFINITY;
     }
     double pr[NE], key[NE];
     if (p.rp.score == MOE_SCORE_SOFTMAX) {
@@ -185,47 +199,68 @@ __global__ __launch_bounds__(64 * kSelTokens) void k_select(SelectParams p) {
     }
 
     if (p.rp.n_groups > 1) {
-      // A group's members are read by a team of lanes, as many as fit into the wave;
-      // each keeps its group_topn best in order, and the team's lists are merged.
+      // A group's members are with a team of lanes: those that have them, or, where a
+      // group is not a power of two of lanes, as many as fit into the wave, through LDS.
+      // Each keeps its group_topn best in order, and the team's lists are merged.
       const int G = p.rp.n_groups, per = E / G, n = p.rp.group_topn;
-      const int team = 64 >> (32 - __clz(G - 1));        // a power of two
+      const bool own = per % NE == 0 && (per / NE & (per / NE - 1)) == 0;
+      const int team = own ? per / NE : 64 >> (32 - __clz(G - 1));     // a power of two
       const int grp = lane / team, at = lane & (team - 1);
+      auto score_of = [&](auto length) {                 // lists of two or four, at least n
+        constexpr int N = decltype(length)::value;
+        double best[N];
 #pragma unroll
-      for (int i = 0; i < NE; ++i)
-        if (lane + 64 * i < E) val[lane + 64 * i] = cand[i] ? key[i] : NEG;
-      __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      double best[4] = {NEG, NEG, NEG, NEG};
-      auto insert = [&](double x) {
+        for (int q = 0; q < N; ++q) best[q] = NEG;
+        auto insert = [&](double x) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (q >= n) break;
-          const double more = fmax(best[q], x);
-          x = fmin(best[q], x);
-          best[q] = more;
+          for (int q = 0; q < N; ++q) {
+            const double was = best[q];
+            const bool more = x > was;
+            best[q] = more ? x : was;
+            x = more ? was : x;
+          }
+        };
+        if (own) {
+#pragma unroll
+          for (int i = 0; i < NE; ++i) insert(cand[i] ? key[i] : NEG);
+        } else if (grp < G) {
+          for (int j0 = at; j0 < per; j0 += 4 * team) {  // four reads in flight
+            double x[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[q] = j0 + q * team < per ? val[grp * per + j0 + q * team] : NEG;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) insert(x[q]);
+          }
         }
+        auto merge = [&](auto from) {
+          double other[N];
+#pragma unroll
+          for (int q = 0; q < N; ++q) other[q] = from(best[q]);
+#pragma unroll
+          for (int q = 0; q < N; ++q) insert(other[q]);
+        };
+        // with the neighbour, the other pair, the other four, the other eight (whose
+        // lanes all have the same list, so that a mirror will do)
+        if (team > 1) merge([](double x) { return dpp_d<0xb1>(x); });
+        if (team > 2) merge([](double x) { return dpp_d<0x4e>(x); });
+        if (team > 4) merge([](double x) { return dpp_d<0x141>(x); });
+        if (team > 8) merge([](double x) { return dpp_d<0x140>(x); });
+        for (int d = 16; d < team; d <<= 1) merge([d](double x) { return __shfl_xor(x, d, kWave); });
+        double sum = best[0];
+#pragma unroll
+        for (int q = 1; q < N; ++q)
+          if (q < n && best[q] > NEG) sum += best[q];
+        return sum;
       };
-      if (grp < G)
-        for (int j0 = at; j0 < per; j0 += 4 * team) {    // four reads in flight
-          double x[4];
+      if (!own) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) x[q] = j0 + q * team < per ? val[grp * per + j0 + q * team] : NEG;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) insert(x[q]);
-        }
-      for (int d = 1; d < team; d <<= 1) {
-        double other[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (q < n) other[q] = __shfl_xor(best[q], d, kWave);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (q < n) insert(other[q]);
+        for (int i = 0; i < NE; ++i)
+          if (i < have) val[e0 + i] = cand[i] ? key[i] : NEG;
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        __builtin_amdgcn_wave_barrier();
       }
-      double score = best[0];
-#pragma unroll
-      for (int q = 1; q < 4; ++q)
-        if (q < n && best[q] > NEG) score += best[q];
+      const double score = n <= 2 ? score_of(std::integral_constant<int, 2>{}) : score_of(std::integral_constant<int, 4>{});
+      __builtin_amdgcn_wave_barrier();                   // val is read by all before it is written again
       // its place among the groups
       int place = 0;
       for (int o = 0; o < G; ++o) {
@@ -234,18 +269,14 @@ __global__ __launch_bounds__(64 * kSelTokens) void k_select(SelectParams p) {
       }
       const uint64_t kept = __ballot(grp < G && place < p.rp.topk_groups);
 #pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        const int e = lane + 64 * i;
-        if (e < E) cand[i] = cand[i] && (kept >> (e / per * team) & 1ull);
-      }
-      __builtin_amdgcn_wave_barrier();                   // val is read by all before it is written again
+      for (int i = 0; i < NE; ++i) cand[i] = cand[i] && (kept >> ((own ? grp : (e0 + i) / per) * team) & 1ull);
     }
 
     uint32_t u[NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       u[i] = cand[i] ? ordered(static_cast<float>(key[i])) : 0;
-      if (lane + 64 * i < E) val[lane + 64 * i] = pr[i];
+      if (i < have) val[e0 + i] = pr[i];
     }
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -258,32 +289,41 @@ __global__ __launch_bounds__(64 * kSelTokens) void k_select(SelectParams p) {
       m = wave_max_u32(m);
       if (m == 0) break;                       // no candidate is left
       uint64_t who[NE];
-      int have = 0;
+      int many = 0;
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
         who[i] = __ballot(u[i] == m);
-        have += __popcll(who[i]);
+        many += __popcll(who[i]);
       }
-      auto lowest = [&](double* its) {         // the lowest expert of who, and its key
+      auto lowest = [&](double& its) {         // the lowest expert of who, and its key
+        uint64_t any = 0;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) any |= who[i];
+        const int src = __ffsll(static_cast<unsigned long long>(any)) - 1;
         int be = 0;
 #pragma unroll
         for (int i = NE - 1; i >= 0; --i)
-          if (who[i]) {
-            const int src = __ffsll(static_cast<unsigned long long>(who[i])) - 1;
-            be = src + 64 * i;
-            if (its) *its = lane_of(key[i], src);
+          if (who[i] >> src & 1) {
+            be = src * NE + i;
+            its = lane_of(key[i], src);
           }
         return be;
       };
-      int be;
-      if (have == 1) {
-        be = lowest(nullptr);
+      int be = 0;
+      if (many == 1) {
+        uint64_t it = 0;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+          it |= who[i];
+          if (who[i]) be = i;
+        }
+        be += (__ffsll(static_cast<unsigned long long>(it)) - 1) * NE;
       } else {
         // those above the lowest one's key, until there are none
         bool more = true;
         while (more) {
           double its = 0.0;
-          be = lowest(&its);
+          be = lowest(its);
           more = false;
           uint64_t above[NE];
 #pragma unroll
@@ -298,7 +338,7 @@ __global__ __launch_bounds__(64 * kSelTokens) void k_select(SelectParams p) {
       }
 #pragma unroll
       for (int i = 0; i < NE; ++i)
-        if (lane + 64 * i == be) u[i] = 0;
+        if (e0 + i == be) u[i] = 0;
       if (lane == real) my_e = be;
     }
     // the slots without a candidate: the first experts not chosen, weight 0

@@ -41,7 +41,12 @@ CASES = [(1, 1, 1, {}), (1, 8, 8, {}), (3, 64, 6, {}), (5, 65, 1, dict(renormali
          (67, 256, 8, dict(score="sigmoid", renormalize=True, groups=8, kept=4, topn=2, scale=2.5)),
          (9, 160, 6, dict(groups=8, kept=3, topn=1)), (9, 160, 6, dict(groups=32, kept=7, topn=4, score="sigmoid")),
          (5, 64, 1, dict(groups=64, kept=1, topn=1)), (5, 128, 16, dict(groups=64, kept=8, topn=2)),
-         (7, 93, 5, dict(groups=3, kept=2, topn=3, renormalize=True))]
+         (7, 93, 5, dict(groups=3, kept=2, topn=3, renormalize=True)),
+         # groups of 32, 16, 8 and 4 lanes, of 6, 12 and 3 lanes, of parts of lanes
+         (9, 256, 8, dict(groups=2, kept=1, topn=4)), (9, 128, 8, dict(groups=4, kept=2, topn=3, score="sigmoid")),
+         (601, 256, 8, dict(groups=16, kept=5, topn=4, score="sigmoid", renormalize=True)), (9, 64, 6, dict(groups=2, kept=1, topn=2)),
+         (9, 192, 8, dict(groups=8, kept=4, topn=2)), (9, 60, 4, dict(groups=5, kept=2, topn=2)), (9, 180, 9, dict(groups=15, kept=4, topn=1)),
+         (9, 252, 8, dict(groups=14, kept=5, topn=3, score="sigmoid"))]
 
 
 @pytest.mark.parametrize("T,E,k,kw", CASES)
