@@ -35,6 +35,7 @@
 #include <mutex>
 
 #include "fp8_act.h"
+#include "int8_rows.h"
 
 namespace dbomoe {
 
@@ -708,8 +709,8 @@ __device__ __forceinline__ int block_excl_scan_waves(int v, int* s_wsum) {
 //  4. it ranks its pairs in pair order (ballot groups in each wave: lanes
 //     holding the same expert, rank = popcount of the lower ones; then the
 //     counts of the lower waves) and writes perm and inv;
-//  5. each wave moves its token's row to the token's positions (bf16 rows, or
-//     fp8 codes and E8M0 bytes).
+//  5. each wave moves its token's row to the token's positions (rows, fp8 codes
+//     and E8M0 bytes, or 8-bit integers and a scale).
 // The positions are those of the stable counting sort, as in
 // k_disp_rank_scan + k_disp_gather.
 // TOK = 16 tokens per workgroup; 4 when that leaves fewer than 256
@@ -718,14 +719,17 @@ __device__ __forceinline__ int block_excl_scan_waves(int v, int* s_wsum) {
 constexpr int kFusedMaxK = 64;
 constexpr int64_t kFusedMaxHist = 16384;   // blocks x local experts summed by each workgroup
 
-template <bool Q8, int TOK, bool DIRECT>
+// What a row becomes: itself, fp8 codes, or 8-bit integers.
+enum GatherTo { TO_ROWS, TO_FP8, TO_INT8_BF16, TO_INT8_F32 };
+
+template <int TO, int TOK, bool DIRECT>
 __global__ __launch_bounds__(64 * TOK) void k_disp_rank_gather(
     const int32_t* __restrict__ ids, int64_t T, int k, int E_total, int e_begin, int E_loc, int64_t nb, int parts,
     int tile_m,
     const int32_t* __restrict__ block_hist, const int32_t* __restrict__ block_err, int32_t* __restrict__ counts,
     int32_t* __restrict__ offsets, int32_t* __restrict__ tile_offsets, int32_t* __restrict__ err,
     int32_t* __restrict__ perm, int32_t* __restrict__ inv, const u32x4_t* __restrict__ x, int row_chunks,
-    void* __restrict__ x_perm, uint8_t* __restrict__ xs) {
+    void* __restrict__ x_perm, void* __restrict__ scales) {
   __shared__ int s_pre[kMidMaxELoc];                // pairs of expert e before this workgroup's first pair
   __shared__ int s_run[kMidMaxELoc];                // pairs of expert e in all blocks, then the first position
   constexpr int kThreads = 64 * TOK;
@@ -843,14 +847,51 @@ __global__ __launch_bounds__(64 * TOK) void k_disp_rank_gather(
   if (t < T && lane < k) inv[t * k + lane] = pos;
   // 5. the row (no barrier from here on)
   if (!token_local) return;
+  if constexpr (TO == TO_INT8_BF16 || TO == TO_INT8_F32) {
+    constexpr bool BF16 = TO == TO_INT8_BF16;
+    uint32_t m = 0;
+    for (int c0 = 0; c0 < row_chunks; c0 += 64 * kChunks) {
+      if (c0 > 0) load_row_chunks(src, c0, row_chunks, lane, v);
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) m = max(m, chunk_max_bits<BF16>(v[i]));
+    }
+    const RowQuant rq(row_max_bits<1>(m, nullptr));
+    const int64_t row_bytes = static_cast<int64_t>(row_chunks) * Chunk<BF16>::N;
+    for (int c0 = 0; c0 < row_chunks; c0 += 64 * kChunks) {
+      if (row_chunks > 64 * kChunks) load_row_chunks(src, c0, row_chunks, lane, v);
+      uint32_t w[kChunks][Chunk<BF16>::N / 4];
+      bool again = !rq.plain();
+      if (!again) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) again |= codes_plain<BF16>(v[i], rq, w[i]);
+      }
+      if (again) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) codes_any<BF16>(v[i], rq, w[i]);
+      }
+      for (int j = 0; j < k; ++j) {
+        const int pj = __shfl(pos, j, kWave);
+        if (pj < 0) continue;
+        int8_t* dst = static_cast<int8_t*>(x_perm) + pj * row_bytes;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int c = c0 + i * 64 + lane;
+          if (c < row_chunks) put_codes<BF16>(dst, c, w[i]);
+        }
+        if (c0 == 0 && lane == 0) static_cast<float*>(scales)[pj] = rq.scale;
+      }
+    }
+    return;
+  }
   for (int c0 = 0; c0 < row_chunks; c0 += 64 * kChunks) {
     if (c0 > 0) load_row_chunks(src, c0, row_chunks, lane, v);
-    if constexpr (Q8) {
+    if constexpr (TO == TO_FP8) {
       uint32_t q[kChunks][2], sb[kChunks];
       quant_row_chunks(v, q, sb);
       for (int j = 0; j < k; ++j) {
         const int pj = __shfl(pos, j, kWave);
-        if (pj >= 0) store_q8_chunks(static_cast<uint8_t*>(x_perm), xs, pj, c0, row_chunks, lane, q, sb);
+        if (pj >= 0)
+          store_q8_chunks(static_cast<uint8_t*>(x_perm), static_cast<uint8_t*>(scales), pj, c0, row_chunks, lane, q, sb);
       }
     } else {
       store_row_chunks(static_cast<u32x4_t*>(x_perm), c0, row_chunks, k, pos, lane, v);
@@ -965,7 +1006,10 @@ moe_status launch_dispatch(const DispatchArgs& a, hipStream_t s) {
   // Few pairs (decode): one kernel whose workgroups each count all the pairs
   // from the ids themselves.
   const bool small = n_pairs <= kSmallMaxPairs && E_loc <= kSmallMaxELoc;
-  const bool fused = !a.beside_ffn && !a.x_scale_i8 && a.T > 0 && E_loc <= kMidMaxELoc && a.k <= kFusedMaxK &&
+  const int row_chunks = static_cast<int>(static_cast<int64_t>(a.H) * dtype_size(a.act) / 16);
+  // (8-bit integers: a row that one wave does not hold in registers is read twice here)
+  const bool held = !a.x_scale_i8 || small || row_chunks <= 64 * kChunks;
+  const bool fused = !a.beside_ffn && held && a.T > 0 && E_loc <= kMidMaxELoc && a.k <= kFusedMaxK &&
                      (small || nb_mid * E_loc <= kFusedMaxHist) && (a.max_blocks <= 0 || groups <= a.max_blocks);
   if (!fused) {
     const moe_status st = launch_dispatch_send(a, s);
@@ -980,32 +1024,28 @@ moe_status launch_dispatch(const DispatchArgs& a, hipStream_t s) {
     DBOMOE_CHECK_LAUNCH();
   }
   const int parts = static_cast<int>(std::min<int64_t>(std::max(1, 64 * tok / E_loc), nb_mid));
-  const int row_chunks = static_cast<int>(static_cast<int64_t>(a.H) * dtype_size(a.act) / 16);
   const int tile_m = a.tile_m > 0 ? a.tile_m : 1;
   int32_t* tile_offsets = a.tile_m > 0 ? a.tile_offsets : nullptr;
-  auto launch_fused = [&](auto q8, auto tk) {
-    constexpr bool Q8 = decltype(q8)::value;
-    constexpr int TOK = decltype(tk)::value;
-    if (small)
-      hipLaunchKernelGGL((k_disp_rank_gather<Q8, TOK, true>), dim3(static_cast<unsigned>(groups)), dim3(64 * TOK), 0,
-                         s, a.ids, a.T, a.k, a.E_total, a.e_begin, E_loc, nb_mid, parts, tile_m, w.block_hist,
-                         w.block_err, a.counts, a.offsets, tile_offsets, w.err, a.perm, a.inv,
-                         static_cast<const u32x4_t*>(a.x), row_chunks, a.x_perm, Q8 ? a.x_scale : nullptr);
-    else
-      hipLaunchKernelGGL((k_disp_rank_gather<Q8, TOK, false>), dim3(static_cast<unsigned>(groups)), dim3(64 * TOK), 0,
-                         s, a.ids, a.T, a.k, a.E_total, a.e_begin, E_loc, nb_mid, parts, tile_m, w.block_hist,
-                         w.block_err, a.counts, a.offsets, tile_offsets, w.err, a.perm, a.inv,
-                         static_cast<const u32x4_t*>(a.x), row_chunks, a.x_perm, Q8 ? a.x_scale : nullptr);
+  void* scales = a.x_scale_i8 ? static_cast<void*>(a.x_scale_i8) : a.x_scale;
+  auto launch_fused = [&](auto to, auto tk, auto direct) {
+    constexpr int TO = decltype(to)::value, TOK = decltype(tk)::value;
+    hipLaunchKernelGGL((k_disp_rank_gather<TO, TOK, decltype(direct)::value>), dim3(static_cast<unsigned>(groups)),
+                       dim3(64 * TOK), 0, s, a.ids, a.T, a.k, a.E_total, a.e_begin, E_loc, nb_mid, parts, tile_m,
+                       w.block_hist, w.block_err, a.counts, a.offsets, tile_offsets, w.err, a.perm, a.inv,
+                       static_cast<const u32x4_t*>(a.x), row_chunks, a.x_perm, scales);
   };
-  using T16 = std::integral_constant<int, 16>;
-  using T4 = std::integral_constant<int, 4>;
-  using Yes = std::integral_constant<bool, true>;
-  using No = std::integral_constant<bool, false>;
-  if (a.x_scale) {
-    if (tok == 16) launch_fused(Yes{}, T16{}); else launch_fused(Yes{}, T4{});
-  } else {
-    if (tok == 16) launch_fused(No{}, T16{}); else launch_fused(No{}, T4{});
-  }
+  auto pick = [&](auto to) {
+    using T16 = std::integral_constant<int, 16>;
+    using T4 = std::integral_constant<int, 4>;
+    if (small)
+      tok == 16 ? launch_fused(to, T16{}, std::true_type{}) : launch_fused(to, T4{}, std::true_type{});
+    else
+      tok == 16 ? launch_fused(to, T16{}, std::false_type{}) : launch_fused(to, T4{}, std::false_type{});
+  };
+  if (a.x_scale_i8)
+    a.act == MOE_BF16 ? pick(std::integral_constant<int, TO_INT8_BF16>{}) : pick(std::integral_constant<int, TO_INT8_F32>{});
+  else
+    a.x_scale ? pick(std::integral_constant<int, TO_FP8>{}) : pick(std::integral_constant<int, TO_ROWS>{});
   DBOMOE_CHECK_LAUNCH();
   return MOE_OK;
 }

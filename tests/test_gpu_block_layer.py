@@ -54,7 +54,11 @@ def _composed(layer, x):
     sh = None
     if layer.shared_w13 is not None:
         sh, shI = new(T, H, dt=t), layer.shared_w2.shape[1]
-        B.moe_grouped_ffn(xn, shI, None, 1, layer.shared_w13, layer.shared_w2, sh, new(B.moe_ffn_workspace_size(T, shI, B.MOE_BF16), dt=u8))
+        # (the layer's own choice of tiles for these: the order of the fp32 sums is the tile's)
+        tiles = lambda bm: -(-T // bm) * -(-shI // 64)
+        tile = 128 if tiles(128) >= 512 else 64 if tiles(64) >= 256 else 32
+        B.moe_grouped_ffn(xn, shI, None, 1, layer.shared_w13, layer.shared_w2, sh, new(B.moe_ffn_workspace_size(T, shI, B.MOE_BF16), dt=u8),
+                          tile_m=tile)
     out = new(T, H, dt=t)
     if b:
         B.moe_combine_post_norm(y, inv, w, x if b["residual"] else None, out, b["eps"], b["post_norm"], b["gate"], b["scale"], shared_out=sh)
