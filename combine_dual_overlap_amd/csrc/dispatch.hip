@@ -860,15 +860,7 @@ __global__ __launch_bounds__(64 * TOK) void k_disp_rank_gather(
     for (int c0 = 0; c0 < row_chunks; c0 += 64 * kChunks) {
       if (row_chunks > 64 * kChunks) load_row_chunks(src, c0, row_chunks, lane, v);
       uint32_t w[kChunks][Chunk<BF16>::N / 4];
-      bool again = !rq.plain();
-      if (!again) {
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) again |= codes_plain<BF16>(v[i], rq, w[i]);
-      }
-      if (again) {
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) codes_any<BF16>(v[i], rq, w[i]);
-      }
+      codes_of<BF16>(v, rq, w);
       for (int j = 0; j < k; ++j) {
         const int pj = __shfl(pos, j, kWave);
         if (pj < 0) continue;

@@ -56,17 +56,7 @@ __global__ __launch_bounds__(RowShape<W>::THREADS) void k_quant_int8(const u32x4
     }
     const RowQuant rq(row_max_bits<W>(m, s_max));
     uint32_t w[CH > 0 ? CH : 1][Chunk<BF16>::N / 4];
-    if constexpr (CH > 0) {
-      bool again = !rq.plain();                               // (the same in every lane of the row)
-      if (!again) {
-#pragma unroll
-        for (int i = 0; i < CH; ++i) again |= codes_plain<BF16>(v[i], rq, w[i]);
-      }
-      if (again) {
-#pragma unroll
-        for (int i = 0; i < CH; ++i) codes_any<BF16>(v[i], rq, w[i]);
-      }
-    }
+    if constexpr (CH > 0) codes_of<BF16>(v, rq, w);
     const int n = inv ? k : 1;
     for (int j = 0; j < n; ++j) {
       const int64_t pos = inv ? static_cast<int64_t>(__shfl(my_pos, j, kWave)) : t;

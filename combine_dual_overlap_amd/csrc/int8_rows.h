@@ -4,7 +4,8 @@
 // the nearest integer in the sum's low bits; it can only be wrong next to a half, which
 // the exact remainder x - code * scale (one fma) shows, and is then put right.  So codes
 // depend on the values alone, for six instructions each.  65536 x 2048 bf16: 73 us (5.5
-// TB/s); with conversions and the comparisons in every one, 16 instructions, 85.
+// TB/s); with conversions and the comparisons in every one, 16 instructions, 85.  8192 x
+// 2048 11.4 us; where a lane with a tie did all its chunks again, 15.4.
 // A row that holds an infinity or NaN gets the scale NaN and codes 0: everything
 // computed from it is NaN.
 #pragma once
@@ -40,20 +41,27 @@ struct RowQuant {
   }
 };
 
-// A chunk's codes, four to a word: of any row, or of one whose scale is plain(), where
-// the result says whether one is next to a half.
+// A chunk's codes, four to a word, of any row.  A loop: it is not run often, and code
+// that is read for the first time takes longer than what it does.
 template <bool BF16>
-__device__ __forceinline__ void codes_any(const u32x4_t& v, const RowQuant& rq, uint32_t (&w)[Chunk<BF16>::N / 4]) {
-  float f[Chunk<BF16>::N];
-  Chunk<BF16>::unpack(v, f);
-#pragma unroll
-  for (int i = 0; i < Chunk<BF16>::N / 4; ++i) {
-    w[i] = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[i] |= static_cast<uint32_t>(rq.code(f[4 * i + j]) & 0xff) << (8 * j);
+__device__ __forceinline__ void codes_any(u32x4_t v, const RowQuant& rq, uint32_t (&w)[Chunk<BF16>::N / 4]) {
+  uint64_t all = 0;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = v[0];
+    if constexpr (BF16) {
+      const uint32_t lo = rq.code(__uint_as_float(x << 16)) & 0xff, hi = rq.code(__uint_as_float(x & 0xffff0000u)) & 0xff;
+      all = all >> 16 | static_cast<uint64_t>(lo | hi << 8) << 48;
+    } else {
+      all = all >> 8 | static_cast<uint64_t>(rq.code(__uint_as_float(x)) & 0xff) << 56;
+    }
+    v = u32x4_t{v[1], v[2], v[3], x};
   }
+  if constexpr (BF16) w[0] = static_cast<uint32_t>(all);
+  w[Chunk<BF16>::N / 4 - 1] = static_cast<uint32_t>(all >> 32);
 }
 
+// The same of a row whose scale is plain(); true where one is next to a half.
 template <bool BF16>
 __device__ __forceinline__ bool codes_plain(const u32x4_t& v, const RowQuant& rq, uint32_t (&w)[Chunk<BF16>::N / 4]) {
   constexpr int N = Chunk<BF16>::N;
@@ -74,6 +82,45 @@ __device__ __forceinline__ bool codes_plain(const u32x4_t& v, const RowQuant& rq
     w[i] = lo | hi << 16;
   }
   return most >= rq.half;
+}
+
+// The same with those put right: the remainder is more than half the scale, or half
+// and the code odd (as one comparison of bit patterns).
+template <bool BF16>
+__device__ __forceinline__ void codes_near(const u32x4_t& v, const RowQuant& rq, uint32_t (&w)[Chunk<BF16>::N / 4]) {
+  constexpr int N = Chunk<BF16>::N;
+  float f[N];
+  Chunk<BF16>::unpack(v, f);
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) w[i] = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float t = fmaf(f[i], rq.inv, 12582912.0f);
+    const int d = __float_as_int(fmaf(12582912.0f - t, rq.s, f[i]));
+    uint32_t y = __float_as_uint(t);
+    if ((d & 0x7fffffff) + static_cast<int>(y & 1) > __float_as_int(rq.half)) y += d >> 31 | 1;
+    w[i / 4] |= (y & 0xff) << (8 * (i & 3));
+  }
+}
+
+// Those of a lane's CH chunks.  Ties are common: a row of bf16 numbers as often as not
+// holds half of its largest one, 63.5 times the scale.  Only the chunks that have one
+// are done again.
+template <bool BF16, int CH>
+__device__ __forceinline__ void codes_of(const u32x4_t (&v)[CH], const RowQuant& rq, uint32_t (&w)[CH][Chunk<BF16>::N / 4]) {
+  if (!rq.plain()) {                             // (the same in every lane of the row)
+#pragma unroll
+    for (int i = 0; i < CH; ++i) codes_any<BF16>(v[i], rq, w[i]);
+    return;
+  }
+  uint32_t again = 0;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) again |= static_cast<uint32_t>(codes_plain<BF16>(v[i], rq, w[i])) << i;
+  if (again) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (again >> i & 1) codes_near<BF16>(v[i], rq, w[i]);
+  }
 }
 
 template <bool BF16>
