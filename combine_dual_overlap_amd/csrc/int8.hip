@@ -6,10 +6,10 @@
 // bf16 product with two integers in the place of one bf16: twice the operations
 // for the same bytes.
 // Few rows an expert: HBM-bound, 193 MB of weights in 40 us (4.8 TB/s).  Many: bound by
-// the matrix pipes at the clock that random integers leave (2.0 - 2.1 GHz): 8192^3 1975
-// TOP/s, 2600 with zeros; 65536 rows of 128 experts, 2048 -> 2 x 768 with SwiGLU 270 us
-// (1526 TOP/s), 768 -> 2048 173 us: 2.2 us a stage of 256 x 256 x 128, and 6 - 7 us of
-// scaling and stores a tile.  No LDS bank conflicts by the counters.
+// the matrix pipes at the clock that random integers leave (2.0 - 2.1 GHz): 8192^3 2040
+// TOP/s, 2780 with zeros; 65536 rows of 128 experts, 2048 -> 2 x 768 with SwiGLU 264 us
+// (1560 TOP/s), 768 -> 2048 165 us, 50 of these its stores, which all workgroups make at
+// about the same time.  No LDS bank conflicts by the counters.
 #include "grouped_tile.h"
 #include "int8_rows.h"
 
