@@ -534,12 +534,14 @@ __global__ __launch_bounds__(512) void k_grouped_int8_few(I8Params ip) {
 //   32 x 128 for up to 32 rows an expert, and while their grid is no more than what
 //   runs at once: 512 rows x 2048 x 2048 9.8 against 14.9 with 128 x 128, 1024 rows
 //   12.7 / 15.5, 2048 rows 22.4 / 16.8; 451 rows of 8 experts x 784 x 1504 8.4 / 12.0.
-//   256 x 256 where there are 256 of them, from 129 rows an expert on: 64 experts x 2048
-//   x 1408, 156 rows 47 against 52, 192 rows 51 / 55, 375 rows 101 / 111, 512 rows 131 /
-//   148; but 256 rows 89 / 73 and 312 rows 92 / 91 (1408 x 2048 gate/up: 161 / 148):
-//   about half of such experts need a second, short tile.
+//   256 x 256 where there are more than 192 of them, from 129 rows an expert on: 64
+//   experts x 2048 x 1408, 136 rows each 48 against 53, 192 rows 52 / 56, 256 rows 62 / 72,
+//   290 rows 90 / 94, 512 rows 116 / 150; of 128 rows 46 / 41.  With rows drawn at random,
+//   so that half of the experts need a second, short tile, 256 rows 78 / 81; Zipf (1.2)
+//   256 rows 91 / 81, 562 rows 154 / 170.  Dense, 2048 wide: 192 tiles 35 / 35, 196 tiles
+//   35 / 40, 112 tiles 33 / 25.
 //   (64 x 128 lies between its neighbours; 256 x 256 and 128 x 128 in four half stages
-//   are 5 to 15 % slower.)
+//   are 5 to 15 % slower: rows of 64 bytes come to LDS at 15 TB/s, of 128 at 25.)
 template <int EPI>
 static moe_status launch_int8(I8Params& p, hipStream_t s) {
   const int64_t cap = p.g.cap, rows = cap / p.g.E;
@@ -554,7 +556,7 @@ static moe_status launch_int8(I8Params& p, hipStream_t s) {
     BM = BN = 32;
   else if (rows <= 32 || tiles(32, 128) <= 512)
     BM = 32;
-  else if (rows > 128 && !(rows > 224 && rows <= 320) && tiles(256, 256) >= 256)
+  else if (rows > 128 && tiles(256, 256) > 192)
     BM = BN = 256;
   const int width = EPI == EPI_SWIGLU ? BN / 2 : BN;
   p.g.n_tiles = (p.g.N + width - 1) / width;
