@@ -230,3 +230,38 @@ def test_norms_in_the_place_of_their_operands(T, H, dt, kind):
     there = res.clone()
     B.moe_pre_norm_backward(d, y, rstd, w, there, dw2, ws, dres=there)
     assert torch.equal(there, dx) and torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,H,k,E,lo,hi", [(3, 8208, 6, 8, 0, 8), (70, 4112, 4, 300, 0, 300), (3000, 4112, 3, 16, 4, 9), (1025, 2048, 8, 128, 0, 128),
+                                           (130, 2048, 16, 16, 0, 16), (4100, 32, 2, 260, 2, 260), (17, 16384, 2, 4, 1, 4)])
+def test_dispatch_to_integers_on_every_path(T, H, k, E, lo, hi, dt):
+    """Long rows, many experts, the same expert twice in a token, ties, zeros and rows that are not finite; tile offsets."""
+    from combine_dual_overlap_amd import binding as B
+    g = torch.Generator().manual_seed(T + H)
+    x = torch.randn(T, H, generator=g)
+    x[0] = 0
+    x[1, 5], x[1, 6] = 4.0, 2.0                          # 2 = 63.5 scales where 4 is the largest
+    x[1].clamp_(-4, 4)
+    x[2, H - 1] = float("nan")
+    x = x.to(dt)
+    ids = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)      # any expert, also twice
+    E_loc, n = hi - lo, T * k
+    i32 = lambda m: torch.full((m,), -9, dtype=torch.int32, device=DEV)
+    meta = [i32(E_loc), i32(E_loc + 1), i32(n), i32(n), i32(E_loc + 1)]
+    ws = torch.empty(max(256, B.moe_dispatch_workspace_size(T, k, E_loc)), dtype=torch.uint8, device=DEV)
+    plain = torch.zeros(n, H, dtype=dt, device=DEV)
+    args = (x.to(DEV), ids.to(DEV), E, lo, hi)
+    B.moe_dispatch(*args, *meta[:4], plain, ws, tile_m=32, tile_offsets=meta[4])
+    want = [t.clone() for t in meta]
+    for t in meta:
+        t.fill_(-9)
+    xq, xs = torch.full((n, H), 77, dtype=torch.int8, device=DEV), torch.full((n,), -5.0, device=DEV)
+    B.moe_dispatch_int8(*args, *meta[:4], xq, xs, ws, tile_m=32, tile_offsets=meta[4])
+    M = int(meta[1][-1])
+    for i in (0, 1, 3, 4):
+        assert torch.equal(meta[i], want[i])
+    assert torch.equal(meta[2][:M], want[2][:M])
+    rq, rs = O.quantize(plain[:M].cpu())
+    assert torch.equal(xq[:M].cpu(), rq) and torch.equal(xs[:M].cpu().nan_to_num(-1), rs.nan_to_num(-1))
+    assert (xq[M:] == 77).all() and (xs[M:] == -5).all()
