@@ -265,3 +265,34 @@ def test_dispatch_to_integers_on_every_path(T, H, k, E, lo, hi, dt):
     rq, rs = O.quantize(plain[:M].cpu())
     assert torch.equal(xq[:M].cpu(), rq) and torch.equal(xs[:M].cpu().nan_to_num(-1), rs.nan_to_num(-1))
     assert (xq[M:] == 77).all() and (xs[M:] == -5).all()
+
+
+def test_shared_experts_of_many_tokens():
+    """From 2048 tokens on the shared experts beside integer ones are grouped products: the layer is its steps with these."""
+    from combine_dual_overlap_amd import DeviceLayer, binding as B
+    from test_gpu_block_layer import _composed
+    cfg, inp = _inputs(2, T=2100)
+    layer = DeviceLayer(inp, int8=True)
+    x, T, H, b = inp["x"].to(DEV), cfg.T, cfg.H, layer.block
+    got = layer.run("unsplit").clone()
+    near, mid = _composed(layer, x)
+    shI = layer.shared_w2.shape[1]
+    h, sh = torch.empty(T, shI, dtype=x.dtype, device=DEV), torch.empty_like(x)
+    B.moe_grouped_swiglu(mid["xn"], layer.shared_w13[None], None, h)
+    B.moe_grouped_gemm("nt", h, layer.shared_w2[None], None, sh, torch.empty(256, dtype=torch.uint8, device=DEV))
+    # the shared part is the same but for the order of fp32 sums: h and the output are rounded once each
+    assert float((sh.double() - mid["sh"].double()).norm() / mid["sh"].double().norm()) < 2 * 2.0 ** -8
+    assert float((got.double() - near.double()).norm() / near.double().norm()) < 2 * 2.0 ** -8
+    # a split layer's microbatches have fewer: the same values again, near enough
+    two = layer.run("dbo", out=torch.empty_like(x))
+    torch.cuda.synchronize()
+    assert float((got.double() - two.double()).norm() / two.double().norm()) < 2 * 2.0 ** -8
+    # and to the bit: what is left of out without the residual and the norms is the shared part's
+    layer2 = DeviceLayer({**inp, "block": None}, int8=True)
+    bare, routed = layer2.run("unsplit").clone(), DeviceLayer({**inp, "block": None, "shared_w13": [], "shared_w2": []}, int8=True).run("unsplit")
+    h2 = torch.empty_like(h)
+    B.moe_grouped_swiglu(x, layer.shared_w13[None], None, h2)
+    B.moe_grouped_gemm("nt", h2, layer.shared_w2[None], None, sh, torch.empty(256, dtype=torch.uint8, device=DEV))
+    want = routed.double() + sh.double()
+    # routed is rounded here and not in the layer (half a step), and the sum once more
+    assert ((bare.double() - want).abs() <= 2.0 ** -8 * (routed.double().abs() + want.abs()) + 1e-30).all()
