@@ -356,8 +356,9 @@ __global__ __launch_bounds__(RowShape<W>::THREADS) void k_norm_bwd(NormBwdParams
 }
 
 // Column sums of the partial rows: S_h; dw = S g (g per channel, else 1), dgate = S w.
-// 16 columns by 64 parts of the rows in a workgroup, eight rows' loads in flight.
-constexpr int kColWidth = 16, kColParts = 64;
+// 32 columns by 32 parts of the rows in a workgroup, eight rows' loads in flight (16 by 64:
+// 2047 x 7168 31.3 us in all, not 29.1).
+constexpr int kColWidth = 32, kColParts = 32;
 template <bool BF16>
 __global__ __launch_bounds__(kColWidth * kColParts) void k_norm_cols(const float* __restrict__ part, int rows, int H,
                                                                      const void* __restrict__ w,
@@ -394,12 +395,16 @@ __global__ __launch_bounds__(kColWidth * kColParts) void k_norm_cols(const float
   if (dgate) dgate[h] = (accumulate ? dgate[h] : 0.f) + v * get(w);
 }
 
-static int64_t norm_bwd_blocks(int64_t T) { return std::min<int64_t>((T + 3) / 4, 512); }
+// A workgroup is one row of parts.  Few rows have a workgroup each (64 x 7168 11.9 -> 7.4 us,
+// 256 x 2048 7.4 -> 6.2), up to 256; 512 x 7168 with 128, 256 and 512: 16.0, 14.6 and 16.7.
+static int64_t norm_bwd_blocks(int64_t T) {
+  return std::max<int64_t>(std::min<int64_t>((T + 3) / 4, 512), std::min<int64_t>(T, 256));
+}
 
 static moe_status launch_norm_bwd(NormBwdParams& p, bool bf16, int32_t H, float* dw, float* dgate_cols, bool accumulate,
                                   void* ws, hipStream_t s) {
   const bool cols = dw || dgate_cols;
-  const int blocks = static_cast<int>(norm_bwd_blocks(p.T));
+  const int blocks = static_cast<int>(cols ? norm_bwd_blocks(p.T) : std::min<int64_t>(p.T, 512));
   p.part = cols ? static_cast<float*>(ws) : nullptr;
   if (p.T > 0) {
     // past the caches (see kStreamBytes) from 24 MB an operand on: 16384 x 2048 41 -> 37 us,
