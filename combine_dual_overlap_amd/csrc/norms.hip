@@ -10,7 +10,7 @@
 // in what follows from it in the same pass.
 // HBM-bound: each row is read once into registers and written once.  8192 tokens x 8
 // rows of 2048 bf16 combined, normed and normed again 67 us (5.5 TB/s); gradients of
-// 8192 x 2048 22 us (4.7 TB/s) and 4 for the columns' sums, of 2047 x 7168 25 and 6.5.
+// 8192 x 2048 22 us (4.7 TB/s) and 3 for the columns' sums, of 2047 x 7168 25 and 4.
 #include "rows.h"
 
 namespace dbomoe {
