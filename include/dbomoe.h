@@ -498,7 +498,8 @@ moe_status moe_route_balance_loss(const float* logits, int64_t T, const int32_t*
  *   once to ct.
  *
  * moe_grouped_swiglu_int8 - that product with w13 [E_loc, 2I, H] (gate rows over up
- *   rows, w13_scale [E_loc, 2I]) and h = silu(g) * u [cap_rows, I], fp32 or bf16 (ht).
+ *   rows, w13_scale [E_loc, 2I]) and h = silu(g) * u [cap_rows, I], fp32 or bf16 (ht);
+ *   silu(g) = g / (1 + exp(-g)) with every step rounded to fp32.
  *
  * moe_grouped_ffn_int8 - a whole expert: moe_grouped_swiglu_int8 with h in fp32,
  *   h quantised as moe_quant_int8_rows does, and the product with w2 [E_loc, H, I],
