@@ -83,7 +83,12 @@ __global__ __launch_bounds__(256) void k_route_bwd(const float* __restrict__ log
     if (id < 0 || id >= E) id = -1;          // such a slot's weight is the constant 0
     if (id >= 0) d = dw[t * k + lane] * rp.routed_scale;
   }
-  const float mine = id >= 0 ? row[id] : -INFINITY;
+  // A logit of -inf or NaN is a masked expert's, +inf the largest finite one.
+  auto logit = [&](int e) {
+    const float l = row[e];
+    return l > -INFINITY ? fminf(l, 3.402823466e38f) : -INFINITY;
+  };
+  const float mine = id >= 0 ? logit(id) : -INFINITY;
   const bool softmax = rp.score == MOE_SCORE_SOFTMAX;
   float p4[4] = {0.f, 0.f, 0.f, 0.f};
   float p = 0.f, slope = 1.f;               // the slot's score; for sigmoid its 1 - p
@@ -91,7 +96,7 @@ __global__ __launch_bounds__(256) void k_route_bwd(const float* __restrict__ log
   if (softmax) {
     float v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = lane + 64 * i < E ? row[lane + 64 * i] : -INFINITY;
+    for (int i = 0; i < 4; ++i) v[i] = lane + 64 * i < E ? logit(lane + 64 * i) : -INFINITY;
     const float lmax = wave_max_f(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
     dead = lmax == -INFINITY;
     float denom = 0.f;

@@ -355,7 +355,9 @@ moe_status moe_combine_backward(const void* dout, const void* y_perm, moe_dtype 
  *   dtopk_w [T, k] fp32; params as given to moe_route_topk
  *   dlogits [T, E] out, fp32 or bf16 (dl): rounded once
  * Ids outside [0, E) contribute nothing; an id that occurs twice in a row
- * counts twice.  A softmax row without a finite logit gets zeros.  The bias's
+ * counts twice.  A logit of -inf or NaN is a masked expert's, whose score is 0; +inf
+ * is taken as the largest finite one.  A softmax row without a logit that is not
+ * masked gets zeros.  The bias's
  * gradient is the sum of dlogits over tokens; x's and w_router's are
  * moe_grouped_gemm products (NN and TN) of dlogits with offsets NULL.
  * ------------------------------------------------------------------------- */
