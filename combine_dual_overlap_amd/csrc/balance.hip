@@ -16,7 +16,7 @@ namespace dbomoe {
 // instructions; 256 tokens x 6 of 64 3 us, 4096 x 8 of 256 in 4 of 8 groups 9.2 (a lane
 // has neighbouring experts, so that a group is a team of lanes; by way of LDS 11.2).
 // An expert whose logit is -inf or NaN has score 0 and is chosen only when no
-// other is left; a logit of +inf counts as the largest finite one.
+// candidate is left; a logit of +inf counts as the largest finite one.
 struct SelectParams {
   const float* part;       // [S][T][E] partial logits (S == 1: the logits)
   int S;
@@ -194,8 +194,8 @@ __global__ __launch_bounds__(64 * kSelTokens) void k_select(SelectParams p) {
     }
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      key[i] = pr[i] + static_cast<double>(bias[i]);
-      cand[i] = l[i] > -INFINITY && key[i] > NEG;        // a bias of -inf or NaN masks too
+      key[i] = l[i] > -INFINITY ? pr[i] + static_cast<double>(bias[i]) : NEG;
+      cand[i] = key[i] > NEG;                  // (a bias of -inf or NaN, which has no place here, masks too)
     }
 
     if (p.rp.n_groups > 1) {
@@ -341,25 +341,25 @@ __global__ __launch_bounds__(64 * kSelTokens) void k_select(SelectParams p) {
         if (e0 + i == be) u[i] = 0;
       if (lane == real) my_e = be;
     }
-    // the slots without a candidate: the first experts not chosen, weight 0
+    // The slots without a candidate: the first masked experts, weight 0.  There are enough, since
+    // the kept groups have k experts or more.  (Not the others of groups that were dropped: their
+    // score is not 0, and the gradient of the weights would count them.)
     if (real < k) {
-      uint64_t taken[NE];
+      uint64_t masked[NE];
 #pragma unroll
-      for (int i = 0; i < NE; ++i) taken[i] = 0;
-      for (int j = 0; j < real; ++j) {
-        const int e = __builtin_amdgcn_readlane(my_e, j);
-#pragma unroll
-        for (int i = 0; i < NE; ++i)
-          if (e >> 6 == i) taken[i] |= 1ull << (e & 63);
-      }
+      for (int i = 0; i < NE; ++i) masked[i] = __ballot(i < have && !(key[i] > NEG));
       for (int j = real; j < k; ++j) {
+        uint64_t any = 0;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) any |= masked[i];
+        const int src = __ffsll(static_cast<unsigned long long>(any)) - 1;
         int e = 0;
 #pragma unroll
         for (int i = NE - 1; i >= 0; --i)
-          if (~taken[i]) e = 64 * i + __ffsll(static_cast<unsigned long long>(~taken[i])) - 1;
+          if (masked[i] >> src & 1) e = src * NE + i;
 #pragma unroll
         for (int i = 0; i < NE; ++i)
-          if (e >> 6 == i) taken[i] |= 1ull << (e & 63);
+          if (src * NE + i == e) masked[i] &= ~(1ull << src);
         if (lane == j) my_e = e;
       }
     }

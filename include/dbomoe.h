@@ -447,7 +447,8 @@ moe_status moe_adamw_step(const void* table_host, const void* table_dev, const m
  * chosen where fewer than k candidates are left, then lowest index first, with
  * weight 0 and not counted in load; it does not count in a group's score, nor
  * for a group that has no other expert.  A logit of +inf is taken as the largest
- * finite one.  moe_route_backward gives the gradient of the weights.
+ * finite one.  moe_route_backward gives the gradient of the weights (that of a masked
+ * expert's is 0).
  *
  * moe_route_balanced - moe_route_topk with this selection: the router's product,
  *   then moe_route_select of logits + logit_bias.  Arguments and workspace as

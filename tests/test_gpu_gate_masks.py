@@ -112,7 +112,7 @@ KINDS = [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", 
 
 
 @pytest.mark.parametrize("score,renormalize", KINDS)
-@pytest.mark.parametrize("groups,kept,topn", [(1, 1, 1)])
+@pytest.mark.parametrize("groups,kept,topn", [(1, 1, 1), (4, 2, 2)])
 def test_rows_that_are_not_finite(score, renormalize, groups, kept, topn):
     low = torch.finfo(torch.float32).min
     logits = torch.randn(12, 80, generator=torch.Generator().manual_seed(5))
@@ -128,3 +128,97 @@ def test_rows_that_are_not_finite(score, renormalize, groups, kept, topn):
     logits[9, :79] = -INF
     logits[10, [1, 2, 3]] = torch.tensor([INF, NAN, -INF])
     _check(logits, None, 5, score, renormalize, groups, kept, topn)
+
+
+@pytest.mark.parametrize("score,renormalize", KINDS)
+def test_one_short_group(score, renormalize):
+    logits = torch.tensor([[1, .5, .2, .1, 3, 2, -INF, -INF], [3, -INF, NAN, 2, 1, 1, 1, 1], [0, 0, 0, 0, -INF, -INF, -INF, -INF],
+                           [-INF] * 8, [-INF, 1, -INF, -INF, -INF, -INF, -INF, -INF]])
+    _check(logits, None, 4, score, renormalize, groups=2, kept=1, topn=1)
+    _check(logits, torch.linspace(0.1, -0.1, 8), 4, score, renormalize, groups=2, kept=1, topn=2, scale=2.5)
+
+
+@pytest.mark.parametrize("score,renormalize", KINDS)
+@pytest.mark.parametrize("E,groups,kept,k", [(64, 8, 1, 5), (93, 3, 1, 8), (160, 32, 2, 6), (128, 4, 1, 16), (256, 8, 4, 8), (256, 2, 1, 16)])
+def test_short_groups(E, groups, kept, k, score, renormalize):
+    """Rows whose kept groups hold fewer unmasked experts than slots, while dropped groups hold others."""
+    T, per = 37, E // groups
+    g = torch.Generator().manual_seed(E + k)
+    logits = torch.randn(T, E, generator=g) - 4.0
+    for t in range(T):
+        strong = torch.randperm(groups, generator=g)[:kept]
+        for i, q in enumerate(strong.tolist()):
+            row = logits[t, q * per:(q + 1) * per]
+            row[:] = NAN if t % 3 == 1 else -INF
+            if i == 0 or t % 2:
+                row[int(torch.randint(per, (1,), generator=g))] = 3.0 + float(torch.rand(1, generator=g))
+        if t % 5 == 0:                     # some masked experts outside, too
+            logits[t, torch.randperm(E, generator=g)[:E // 8]] = -INF
+    ids, real = _chosen(logits, None, k, score, groups, kept, 1)
+    lowest = torch.isfinite(logits).int().argmax(1)
+    assert int(((real < k) & (lowest < ids.gather(1, real.clamp(max=k - 1)[:, None]).squeeze(1))).sum()) > 5
+    _check(logits, None, k, score, renormalize, groups, kept, 1)
+    _check(logits, torch.randn(E, generator=g) * 1e-3, k, score, renormalize, groups, kept, 1, 2.5)
+
+
+@pytest.mark.parametrize("score,renormalize", KINDS)
+def test_balanced_route_and_its_gradient(score, renormalize):
+    """The whole gate, with a logit bias that masks experts: a product, the choice, and the gradient of the weights."""
+    B = _B()
+    T, H, E, k, groups = 61, 256, 64, 6, 8
+    g = torch.Generator().manual_seed(9)
+    x, wr = torch.randn(T, H, generator=g).to(torch.bfloat16), (torch.randn(E, H, generator=g) * H ** -0.5).to(torch.bfloat16)
+    lb = torch.randn(E, generator=g) * 0.1
+    lb[16:24] += 4.0
+    lb[17:24] = -INF                       # the best group is left with one expert
+    rp = B.route_params(E, k, score, renormalize, groups, 1, 1, 1.5)
+    ids, w = torch.empty(T, k, dtype=torch.int32, device=DEV), torch.empty(T, k, device=DEV)
+    logits, load = torch.empty(T, E, device=DEV), torch.zeros(E, dtype=torch.int32, device=DEV)
+    ws = torch.empty(max(256, B.moe_route_workspace_size(T, H, E)), dtype=torch.uint8, device=DEV)
+    B.moe_route_balanced(x.to(DEV), wr.to(DEV), rp, ids, w, ws, load=load, logits_out=logits, logit_bias=lb.to(DEV))
+    l, dw = logits.cpu(), torch.randn(T, k, generator=g)
+    rid, rw, rload, rg, bound = _reference(l, None, k, dw, score, renormalize, groups, 1, 1, 1.5)
+    assert int(((rw == 0).sum(1) == k - 1).sum()) > T // 2
+    assert torch.equal(ids.cpu(), rid) and torch.equal(load.cpu(), rload)
+    assert ((w.cpu().double() - rw).abs() <= 1.01 * O.U * rw + 2.0 ** -149).all()
+    dl = torch.empty(T, E, device=DEV)
+    B.moe_route_backward(logits, ids, dw.to(DEV), rp, dl)
+    assert ((dl.cpu().double() - rg).abs() <= bound + O.rounding(torch.float32, rg)).all()
+
+
+@pytest.mark.parametrize("score,renormalize", KINDS)
+def test_train_layer_with_masked_experts(score, renormalize):
+    """TrainLayer with groups and -inf in logit_bias against 64-bit autograd at the experts of the header's rule."""
+    import workloads as W
+    from combine_dual_overlap_amd import TrainLayer
+    cfg = W.get_config(1, small=True).replace(k=3, n_groups=2, topk_groups=1, group_topn=1, score=score, renormalize=renormalize)
+    inp = W.make_inputs(cfg, 5)
+    inp["forced_ids"] = None
+    lb = torch.zeros(cfg.E)
+    lb[4:] = torch.tensor([3.0, 2.0, -INF, -INF])      # two experts in the second group, which most tokens prefer
+    inp["logit_bias"], inp["select_bias"] = lb, torch.zeros(cfg.E)
+    layer = TrainLayer(inp)
+    x = inp["x"].to(DEV)
+    dout = torch.randn(x.shape, generator=torch.Generator().manual_seed(8))
+    out = layer.forward(x).clone()
+    logits, ids = layer.buf["logits"][:cfg.T].cpu(), layer.buf["ids"][:cfg.T].cpu().long()
+    rid, real = _chosen(logits, None, cfg.k, score, 2, 1, 1)
+    assert int((real < cfg.k).sum()) > cfg.T // 2
+    assert torch.equal(ids, rid)
+    dx = layer.backward(dout.to(DEV))
+    P = {n: t.cpu().double().requires_grad_(True) for n, t in layer.weights.items()}
+    x64 = inp["x"].double().requires_grad_(True)
+    masked = ~torch.isfinite(lb)[None].expand(cfg.T, cfg.E)
+    l = x64 @ P["w_router"][0].T + torch.where(masked, torch.zeros_like(lb), lb).double()
+    w = _weights(l, masked, ids, real, score, renormalize, cfg.routed_scale)
+    y = torch.zeros_like(x64)
+    for e in range(cfg.E):
+        t, j = torch.nonzero(ids == e, as_tuple=True)
+        a, b = (x64[t] @ P["w13"][e].T).chunk(2, dim=1)
+        y = y.index_add(0, t, (a * torch.sigmoid(a) * b) @ P["w2"][e].T * w[t, j, None])
+    grads = torch.autograd.grad((y * dout.double()).sum(), [x64, *P.values()])
+    # fp32: five products of at most 256 terms one after the other, each off by at most terms * 2^-24: 8e-5
+    near = lambda a, r: float((a.cpu().double() - r).norm() / r.norm()) < 8e-5
+    assert near(out, y.detach()) and near(dx, grads[0])
+    for n, r in zip(P, grads[1:]):
+        assert near(layer.grads[n], r), n
