@@ -113,7 +113,15 @@ __global__ __launch_bounds__(256) void k_route_bwd(const float* __restrict__ log
     p = 1.0f / (1.0f + expf(-mine));
     slope = 1.0f / (1.0f + expf(mine));
   }
-  const float wsum = wave_sum_f(lane < k ? p : 0.f);
+  float wsum = wave_sum_f(lane < k ? p : 0.f);
+  // Scores that fp32 hardly holds, or not at all: only their ratios count.
+  if (rp.renormalize != 0 && wsum < 0x1p-60f) {
+    const float top = wave_max_f(mine);
+    if (top > -INFINITY) {
+      p = expf(mine - top);
+      wsum = wave_sum_f(p);
+    }
+  }
   const bool renorm = rp.renormalize != 0 && wsum > 0.f;
   const float w = renorm ? p / wsum : p;
   const float dot = wave_sum_f(lane < k && id >= 0 ? w * d : 0.f);

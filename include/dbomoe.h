@@ -357,7 +357,8 @@ moe_status moe_combine_backward(const void* dout, const void* y_perm, moe_dtype 
  * Ids outside [0, E) contribute nothing; an id that occurs twice in a row
  * counts twice.  A logit of -inf or NaN is a masked expert's, whose score is 0; +inf
  * is taken as the largest finite one.  A softmax row without a logit that is not
- * masked gets zeros.  The bias's
+ * masked gets zeros.  Weights that are divided by their sum have their gradient however
+ * small the scores are.  The bias's
  * gradient is the sum of dlogits over tokens; x's and w_router's are
  * moe_grouped_gemm products (NN and TN) of dlogits with offsets NULL.
  * ------------------------------------------------------------------------- */

@@ -222,3 +222,25 @@ def test_train_layer_with_masked_experts(score, renormalize):
     assert near(out, y.detach()) and near(dx, grads[0])
     for n, r in zip(P, grads[1:]):
         assert near(layer.grads[n], r), n
+
+
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_scores_below_fp32(renormalize):
+    """Sigmoid scores whose weights are ordinary numbers only because they are divided by their sum."""
+    g = torch.Generator().manual_seed(6)
+    logits = torch.cat([torch.randn(1, 64, generator=g) + s for s in (-30.0, -60, -86, -90, -95, -100, -110, -200, -600)])
+    logits = torch.cat([logits, logits + 20 * torch.rand(logits.shape, generator=g)])
+    _check(logits, None, 6, "sigmoid", renormalize)
+    _check(logits, None, 6, "sigmoid", renormalize, groups=8, kept=3, topn=2, scale=2.5)
+
+
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_softmax_scores_below_fp32(renormalize):
+    """A bias that keeps a token from its one large expert: the others' weights are ordinary once divided by their sum."""
+    g = torch.Generator().manual_seed(7)
+    logits = torch.cat([torch.randn(4, 64, generator=g) + s for s in (-10.0, -40, -60, -90, -104, -120, -600)])
+    logits[:, 9] = 0.0
+    bias = torch.zeros(64)
+    bias[9] = -2.0
+    _check(logits, bias, 6, "softmax", renormalize)
+    _check(logits, bias, 6, "softmax", renormalize, groups=8, kept=3, topn=2, scale=2.5)
