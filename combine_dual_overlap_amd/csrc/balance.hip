@@ -519,6 +519,21 @@ __global__ __launch_bounds__(256) void k_balance_loss(const float* __restrict__ 
 #pragma unroll
     for (int i = 0; i < NE; ++i) norm += q[i];
     norm = wave_sum_dpp(norm);
+    // Sigmoid scores that fp32 hardly holds, or not at all: relative to the largest (the sum is
+    // then 1 at least; 1 + e^l is 1 here).  Above that, what fp32 loses of a score is 2^-66 of the sum.
+    if (!softmax && norm < 0x1p-60f) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) top = max(top, ordered(l[i]));
+      const float lmax = unordered(wave_max_u32(top));
+      norm = 0.f;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        q[i] = l[i] > -INFINITY ? expf(l[i] - lmax) : 0.f;
+        norm += q[i];
+      }
+      norm = wave_sum_dpp(norm);
+    }
     const float inv = norm > 0.f ? 1.0f / norm : 0.f;
     float dot = 0.f;
 #pragma unroll

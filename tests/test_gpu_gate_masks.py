@@ -244,3 +244,40 @@ def test_softmax_scores_below_fp32(renormalize):
     bias[9] = -2.0
     _check(logits, bias, 6, "softmax", renormalize)
     _check(logits, bias, 6, "softmax", renormalize, groups=8, kept=3, topn=2, scale=2.5)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E", [8, 64, 200])
+def test_balance_loss_of_scores_below_fp32(E, dt):
+    """q = p / sum p is an ordinary number, however small a token's sigmoid scores are."""
+    B = _B()
+    g = torch.Generator().manual_seed(E)
+    rows = [torch.randn(1, E, generator=g) + s for s in (-20.0, -60, -88, -90, -95, -100, -104, -110, -200, -1000)]
+    rows += [r + 30 * torch.rand(1, E, generator=g) for r in rows]
+    logits = torch.cat(rows)
+    logits = torch.cat([logits, logits, logits])
+    n = len(rows)
+    logits[n:2 * n, 1:] = -INF                           # one expert each
+    logits[2 * n:, ::2] = NAN
+    T = logits.shape[0]
+    load = torch.randint(0, 50, (E,), generator=g, dtype=torch.int32)
+    load[0] += 1
+    before = (torch.randn(T, E, generator=g) * 0.01 / T).to(dt)
+    coef = 0.25
+    d, loss = before.to(DEV), torch.full((1,), NAN, device=DEV)
+    ws = torch.empty(B.moe_route_balance_loss_workspace_size(T, E), dtype=torch.uint8, device=DEV)
+    B.moe_route_balance_loss(logits.to(DEV), load.to(DEV), B.route_params(E, 1, "sigmoid"), coef, loss, d, ws, accumulate=True)
+    masked = ~torch.isfinite(logits)
+    l = torch.where(masked, torch.zeros_like(logits), logits).double()
+    q = torch.softmax(torch.nn.functional.logsigmoid(l).masked_fill(masked, -INF), 1)
+    f = load.double() * (E / int(load.sum()))
+    inner = (q * f).sum(1, keepdim=True)
+    want = before.double() + coef / T * q * (f - inner) * torch.sigmoid(-l)
+    # q: the argument of its exponential is off by half a step for each unit that it is long, and a few more of the
+    # exponentials, the sum (pairs) and the division; f - 1 and the inner sum carry such an error of their own
+    top = l.masked_fill(masked, -INF).amax(1, keepdim=True)
+    far = torch.where(masked, torch.zeros_like(l), (top - l + l.abs()).clamp(max=208.0))
+    err = 48 + 2 * far
+    bound = coef / T * O.U * q * (err * ((f - 1).abs() + (inner - 1).abs()) + ((q * err) * (f - 1).abs()).sum(1, keepdim=True))
+    assert ((d.cpu().double() - want).abs() <= bound + O.U * want.abs() + O.rounding(dt, want) + 1e-45).all()
+    assert abs(loss.item() - coef / T * float((q * f).sum())) <= 4 * O.U * coef / T * float((q * (f - 1).abs() * err).sum() + T)
