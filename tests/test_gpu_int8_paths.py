@@ -34,3 +34,69 @@ def test_swiglu_is_rounded_like_fp32_arithmetic(rows, N):
     # for their products.  (Below -87 the quotient is of a number above 2^126, and may be off by all that is left of it.)
     bound = 5.1 * O.U * want.abs() + (gate * up).abs().double() * 2.0 ** -126 + 2.0 ** -126
     assert ((h.cpu().double() - want).abs() <= bound).all()
+
+
+def _ragged(g, experts, mean):
+    """Rows of each expert around `mean`, every ninth without any."""
+    n = torch.randint(max(1, mean // 2), mean + mean // 2 + 1, (experts,), generator=g)
+    n[4::9] = 0
+    return n.tolist()
+
+
+# 64 experts of about 24 rows are tiles of 32 x 128 (512 workgroups, three stages in flight), 48 of about 90 rows tiles of
+# 128 x 128 (512 workgroups, two stages); with 2048 columns there are more tiles than workgroups.  A tile is one stage, two
+# with a short one, and four.
+WALKS = [(64, 24, 2048), (64, 24, 2056), (48, 90, 2048), (48, 90, 2184)]
+STAGES = [16, 128, 144, 400]
+
+
+@pytest.mark.parametrize("K", STAGES)
+@pytest.mark.parametrize("experts,mean,N", WALKS)
+def test_products_of_many_tiles(experts, mean, N, K):
+    """Bit for bit: whole sums, then an fp32 rounding for each scale, then one to the result's type."""
+    B = _B()
+    g = torch.Generator().manual_seed(experts + N + K)
+    n = _ragged(g, experts, mean)
+    M = sum(n)
+    high = 32 if mean <= 32 else 128
+    assert sum(-(-r // high) for r in n) * -(-N // 128) > 640
+    cap = M + 5
+    a, b = _int8(g, cap, K), _int8(g, experts, N, K)
+    s, t = 0.01 * (1 + torch.rand(cap, generator=g)), 0.01 * (1 + torch.rand(experts, N, generator=g))
+    off = torch.tensor([sum(n[:e]) for e in range(experts + 1)], dtype=torch.int32)
+    want = torch.full((cap, N), 9.0)
+    for e in range(experts):
+        i, j = int(off[e]), int(off[e + 1])
+        if j > i:
+            want[i:j] = O.int8_product(a[i:j], s[i:j], b[e], t[e])
+    dev = [v.to(DEV) for v in (a, s, b, t, off)]
+    for dt in (torch.float32, torch.bfloat16):
+        for _ in range(3):
+            c = torch.full((cap, N), 9.0, dtype=dt, device=DEV)
+            B.moe_grouped_gemm_int8(*dev, c)
+            assert torch.equal(c.cpu(), want.to(dt)), dt
+
+
+@pytest.mark.parametrize("K", STAGES)
+@pytest.mark.parametrize("experts,mean,I", [(64, 24, 1032), (48, 90, 1024)])
+def test_swiglu_of_many_tiles(experts, mean, I, K):
+    B = _B()
+    g = torch.Generator().manual_seed(experts + I + K)
+    n = _ragged(g, experts, mean)
+    cap = sum(n) + 5
+    a, b = _int8(g, cap, K), _int8(g, experts, 2 * I, K)
+    s, t = 1e-3 * (1 + torch.rand(cap, generator=g)), 0.01 * (1 + torch.rand(experts, 2 * I, generator=g))
+    off = torch.tensor([sum(n[:e]) for e in range(experts + 1)], dtype=torch.int32)
+    want, bound = torch.full((cap, I), 9.0, dtype=torch.float64), torch.zeros(cap, I, dtype=torch.float64)
+    for e in range(experts):
+        i, j = int(off[e]), int(off[e + 1])
+        if j > i:
+            gate, up = O.int8_product(a[i:j], s[i:j], b[e], t[e]).double().chunk(2, dim=1)
+            want[i:j] = gate * torch.sigmoid(gate) * up
+            bound[i:j] = 5.1 * O.U * want[i:j].abs() + 2.0 ** -126 * (1 + (gate * up).abs())      # as above
+    dev = [v.to(DEV) for v in (a, s, b, t, off)]
+    for dt in (torch.float32, torch.bfloat16):
+        h = torch.full((cap, I), 9.0, dtype=dt, device=DEV)
+        B.moe_grouped_swiglu_int8(*dev, h)
+        far = (h.cpu().double() - want).abs()
+        assert (far <= bound + (O.rounding(dt, want.abs() + bound) if dt == torch.bfloat16 else 0.0)).all(), dt
