@@ -173,16 +173,22 @@ struct HipBackend {
     if (ctx->timing) {
       a.t0 = ctx->tev[ctx->slot][mb][0];
       a.t1 = ctx->tev[ctx->slot][mb][1];
-      a.t2 = ctx->tev[ctx->slot][mb][2];
+      if (d->shared_I == 0) a.t2 = ctx->tev[ctx->slot][mb][2];
       ctx->timed[ctx->slot][mb] = true;
     }
     moe_status st = launch_ffn_int8(a, s);
     if (st != MOE_OK || d->shared_I == 0) return st;
+    st = launch_shared_experts(mb, xm, T, s);
+    if (st != MOE_OK) return st;
+    return ctx->timing && hipEventRecord(ctx->tev[ctx->slot][mb][2], s) != hipSuccess ? MOE_ERR_HIP : MOE_OK;
+  }
+
+  moe_status launch_shared_experts(int mb, const char* xm, int64_t T, hipStream_t s) const {
     // The shared experts, by themselves.  Many tokens: the products of 256 x 256 tiles, 2048 ->
     // 2 x 2816 -> 2048 for 4096 tokens 154 us against 184 with the FFN's, 8192 tokens 238 / 371.
     if (T >= 2048 && (static_cast<int64_t>(d->shared_I) + 256) * d->H * 2 < (int64_t{1} << 32) &&
         moe_grouped_gemm_workspace_size(MOE_GEMM_NT, d->act, 1, 1, T, d->H, d->shared_I) == 0) {
-      st = moe_grouped_swiglu(xm, d->shared_w13, d->act, nullptr, 1, T, d->H, d->shared_I, nullptr, buf<void>(mb, B_SHH), s);
+      const moe_status st = moe_grouped_swiglu(xm, d->shared_w13, d->act, nullptr, 1, T, d->H, d->shared_I, nullptr, buf<void>(mb, B_SHH), s);
       if (st != MOE_OK) return st;
       return moe_grouped_gemm(MOE_GEMM_NT, buf<void>(mb, B_SHH), d->shared_w2, d->act, nullptr, 1, T, d->H, d->shared_I,
                               buf<void>(mb, B_SHOUT), d->act, 0, nullptr, 0, s);

@@ -679,7 +679,8 @@ void dbo_ctx_destroy(dbo_ctx* ctx);
 moe_status dbo_ctx_set_timing(dbo_ctx* ctx, int32_t enable);
 /* Elapsed ms of the expert GEMM kernels of the timed call `back` calls ago
  * (0 = the last), ms4 = {A gate/up, A down, B gate/up, B down}; zeros for a
- * microbatch that did not run or a call not remembered.  Waits for the end
+ * microbatch that did not run or a call not remembered.  With integer experts the
+ * shared experts, which run after them, are part of `down`.  Waits for the end
  * events of that call. */
 moe_status dbo_ctx_ffn_times(dbo_ctx* ctx, int32_t back, float* ms4);
 /* The same for the comm-side steps: ms4 = {A dispatch, B dispatch, A combine,
