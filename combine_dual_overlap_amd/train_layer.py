@@ -159,8 +159,6 @@ class TrainLayer:
         self.table = table(slice(0, n))
         self.hyper = B.adamw_params(**hyper)
         self.norm_table = table(slice(n, None)) if len(ws) > n else None
-        # (another seed: the tables number their tensors from 0 each)
-        self.norm_hyper = B.adamw_params(**{**hyper, "weight_decay": 0.0, "seed": hyper.get("seed", 0) ^ 0x5bd1e995})
         self.steps = torch.zeros(1, dtype=i32, device=d)
         self.T = 0
 
@@ -301,6 +299,11 @@ class TrainLayer:
                 g.zero_()
         self.fresh = True
 
+    def _norm_hyper(self):
+        """Those of the norms and the gate: no decay, and another seed (the tables number their tensors from 0 each)."""
+        h = self.hyper
+        return B.adamw_params(h.lr, h.beta1, h.beta2, h.eps, 0.0, h.seed ^ 0x5bd1e995)
+
     def step(self, lr_scale=None, grad_scale=None):
         """One AdamW update from the gradients added since zero_grad(); lr_scale, grad_scale: device scalars."""
         if self.fresh and not self.captured:
@@ -309,7 +312,7 @@ class TrainLayer:
         try:
             B.moe_adamw_step(self.table, self.hyper, self.steps, lr_scale=lr_scale, grad_scale=grad_scale)
             if self.norm_table is not None:
-                B.moe_adamw_step(self.norm_table, self.norm_hyper, self.steps, lr_scale=lr_scale, grad_scale=grad_scale)
+                B.moe_adamw_step(self.norm_table, self._norm_hyper(), self.steps, lr_scale=lr_scale, grad_scale=grad_scale)
         except Exception:
             self.steps.sub_(1)                # refused: no update has been made
             raise

@@ -34,3 +34,32 @@ def test_ffn_times_hold_the_shared_experts_of_integer_layers():
         (w0, f0), (w2, f2) = times[0, schedule], times[2, schedule]
         assert w2 > 1.5 * w0                       # they are most of this layer,
         assert f2 - f0 > 0.5 * (w2 - w0), (schedule, times)      # and the expert time grows by what the layer's does
+
+
+def _train(**kw):
+    from combine_dual_overlap_amd import TrainLayer
+    cfg, inp = _inputs(1, "f32")
+    layer = TrainLayer(inp, **kw)
+    x = inp["x"].to(DEV)
+    return layer, x, torch.randn(x.shape, generator=torch.Generator().manual_seed(2)).to(DEV)
+
+
+def test_the_norms_and_the_gate_follow_the_layers_hyperparameters():
+    """layer.hyper changed between steps, as a schedule does: every weight takes it."""
+    from combine_dual_overlap_amd import binding as B
+    layer, x, dout = _train(lr=1e-2, weight_decay=0.0)
+
+    def step():
+        old = {n: w.clone() for n, w in layer.weights.items()}
+        layer.forward(x)
+        layer.backward(dout)
+        layer.step()
+        return {n: float((w - old[n]).abs().max()) for n, w in layer.weights.items()}
+
+    layer.hyper.lr = 0.0
+    assert set(step().values()) == {0.0}
+    layer.hyper.lr = 1e-3
+    # a step's m / sqrt(v) is at most (1 - beta1^2) / (1 - beta1) / ... = 1 where the gradients are alike; 2 leaves room
+    assert all(0.0 < d < 2e-3 for d in step().values())
+    layer.hyper = B.adamw_params(lr=0.0)
+    assert set(step().values()) == {0.0}
