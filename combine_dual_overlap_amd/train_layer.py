@@ -311,11 +311,11 @@ class TrainLayer:
         self.steps.add_(1)
         try:
             B.moe_adamw_step(self.table, self.hyper, self.steps, lr_scale=lr_scale, grad_scale=grad_scale)
-            if self.norm_table is not None:
-                B.moe_adamw_step(self.norm_table, self._norm_hyper(), self.steps, lr_scale=lr_scale, grad_scale=grad_scale)
         except Exception:
             self.steps.sub_(1)                # refused: no update has been made
             raise
+        if self.norm_table is not None:       # (what the first takes this takes too; after a failed launch the step counts)
+            B.moe_adamw_step(self.norm_table, self._norm_hyper(), self.steps, lr_scale=lr_scale, grad_scale=grad_scale)
         if self.bias_rate > 0:
             B.moe_route_bias_update(self.select_bias, self.load_sum, self.bias_rate)
         self.zero_grad()

@@ -63,3 +63,28 @@ def test_the_norms_and_the_gate_follow_the_layers_hyperparameters():
     assert all(0.0 < d < 2e-3 for d in step().values())
     layer.hyper = B.adamw_params(lr=0.0)
     assert set(step().values()) == {0.0}
+
+
+def test_a_step_that_fails_half_way_keeps_the_count_of_what_was_done(monkeypatch):
+    from combine_dual_overlap_amd import binding as B
+    layer, x, dout = _train(lr=1e-2)
+    real, calls = B.moe_adamw_step, []
+
+    def fails(at):
+        def call(*args, **kw):
+            calls.append(1)
+            if len(calls) == at:
+                raise B.MoEError(B.MOE_ERR_HIP, "moe_adamw_step")
+            return real(*args, **kw)
+        return call
+
+    for at, steps in ((1, 0), (2, 1)):
+        calls.clear()
+        layer.forward(x)
+        layer.backward(dout)
+        old = layer.weights["w2"].clone()
+        monkeypatch.setattr(B, "moe_adamw_step", fails(at))
+        with pytest.raises(B.MoEError):
+            layer.step()
+        monkeypatch.setattr(B, "moe_adamw_step", real)
+        assert layer.steps.item() == steps and torch.equal(layer.weights["w2"], old) == (steps == 0)
