@@ -46,8 +46,8 @@ class TrainLayer:
 
     Balance of the experts: inp["select_bias"] [E] float32 is added to the scores
     when experts are chosen; bias_rate > 0: step() moves it by bias_rate towards the
-    experts that got fewer tokens than the mean since the last step (starting from
-    zeros if it was not given); balance_coef > 0: backward() adds the gradient of the
+    experts that got fewer tokens than the mean in the passes since the last step that
+    backward() followed (starting from zeros if it was not given); balance_coef > 0: backward() adds the gradient of the
     balance loss of its tokens, and balance_loss [1] holds that loss.  `load` [E]
     counts the tokens of the last forward() by expert.  Not with forced ids.
 
@@ -202,8 +202,6 @@ class TrainLayer:
             self.load.zero_()
             B.moe_route_balanced(x, W["w_router"], self.route, ids, w, self.ws_route, select_bias=self.select_bias,
                                  load=self.load, logits_out=logits, logit_bias=self.logit_bias)
-            if self.bias_rate > 0:
-                self.load_sum.add_(self.load)
         else:
             B.moe_route_topk(x, W["w_router"], self.route, ids, w, self.ws_route, logits_out=logits,
                              logit_bias=self.logit_bias, forced_ids=forced)
@@ -244,6 +242,8 @@ class TrainLayer:
 
     def _backward(self, dout):
         W, G, more = self.weights, self.grads, self._captured() or not self.fresh
+        if self.bias_rate > 0:
+            self.load_sum.add_(self.load)
         logits, ids, w, inv, x_perm, gu, h, y_perm, dy, dw, dgu, dx_perm, dlogits, dx_dense, dx = self._rows(
             "logits", "ids", "w", "inv", "x_perm", "gu", "h", "y_perm", "dy_perm", "dw", "dgu", "dx_perm", "dlogits",
             "dx_dense", "dx")

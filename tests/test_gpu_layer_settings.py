@@ -88,3 +88,18 @@ def test_a_step_that_fails_half_way_keeps_the_count_of_what_was_done(monkeypatch
             layer.step()
         monkeypatch.setattr(B, "moe_adamw_step", real)
         assert layer.steps.item() == steps and torch.equal(layer.weights["w2"], old) == (steps == 0)
+
+
+def test_passes_that_are_not_trained_on_do_not_move_the_bias():
+    """forward() for evaluation, then two that backward() follows: the bias goes by the tokens of these."""
+    layer, x, dout = _train(lr=1e-3, bias_rate=0.125)
+    bias, load = layer.select_bias.clone(), torch.zeros_like(layer.load)
+    for i in range(6):
+        layer.forward((x * (i + 1) - i).contiguous() if i not in (2, 4) else x)
+        if i in (2, 4):
+            load += layer.load
+            layer.backward(dout)
+    layer.step()
+    want = bias + 0.125 * torch.sign(load.float().mean() - load.float())
+    assert torch.equal(layer.select_bias, want)
+    assert layer.load_sum.abs().sum() == 0
