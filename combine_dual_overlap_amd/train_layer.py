@@ -96,8 +96,8 @@ class TrainLayer:
             for name in ("pre_norm", "post_norm", "gate"):
                 if self.block[name] is not None:
                     self.weights[name] = own(name, self.block[name], H)
-        if not (balance_coef >= 0.0 and bias_rate >= 0.0):
-            raise ValueError("balance_coef and bias_rate: not negative")
+        if not (0.0 <= balance_coef < 3.4e38 and 0.0 <= bias_rate < 3.4e38):      # (fp32 numbers)
+            raise ValueError("balance_coef and bias_rate: not negative, and finite")
         self.balance_coef, self.bias_rate = balance_coef, bias_rate
         self.select_bias = inp.get("select_bias")
         if self.select_bias is not None:
