@@ -101,6 +101,13 @@ class DeviceLayer:
             self.w2 = _dev(inp["w2"], d)
             self.w13_scale = _dev(inp.get("w13_scale"), d)
             self.w2_scale = _dev(inp.get("w2_scale"), d)
+        if self.w13.dtype == torch.int8:
+            E_loc = cfg.expert_end - cfg.expert_begin
+            for name, w, s, shape in (("w13", self.w13, self.w13_scale, (E_loc, 2 * cfg.I, cfg.H)),
+                                      ("w2", self.w2, self.w2_scale, (E_loc, cfg.H, cfg.I))):
+                if (w.dtype != torch.int8 or w.shape != shape or s is None or s.dtype != torch.float32 or
+                        s.shape != shape[:2]):
+                    raise ValueError(f"{name}: int8 {list(shape)}, {name}_scale: float32 {list(shape[:2])}")
         self.select_bias = _dev(inp.get("select_bias"), d)
         if self.select_bias is not None and (self.select_bias.dtype != torch.float32 or self.select_bias.shape != (cfg.E,)):
             raise ValueError(f"select_bias: float32 [{cfg.E}]")

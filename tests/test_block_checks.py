@@ -17,3 +17,23 @@ def test_train_layer_refuses_rates_that_its_steps_refuse():
         for name in ("bias_rate", "balance_coef"):
             with pytest.raises(ValueError, match="balance_coef and bias_rate"):
                 TrainLayer(inp, device="cpu", **{name: bad})
+
+
+def test_integer_weights_come_with_a_scale_per_row():
+    """int8 weights were run with whatever scales stood beside them: shorter ones were read behind their end."""
+    import workloads as W
+    from combine_dual_overlap_amd import DeviceLayer
+    cfg = W.get_config(2, small=True)
+    inp = W.make_inputs(cfg)
+    E, H, I = cfg.E, cfg.H, cfg.I
+    good = dict(w13=torch.zeros(E, 2 * I, H, dtype=torch.int8), w2=torch.zeros(E, H, I, dtype=torch.int8),
+                w13_scale=torch.ones(E, 2 * I), w2_scale=torch.ones(E, H))
+    with pytest.raises(ValueError, match="device tensor"):           # nothing wrong but the device
+        DeviceLayer({**inp, **good}, device="cpu")
+    for name, bad in (("w13", torch.ones(E, 2 * I // 128, H // 128)), ("w2", torch.ones(E, 1)), ("w2", torch.ones(E, H).double()),
+                      ("w13", None), ("w2", torch.ones(E - 1, H))):
+        with pytest.raises(ValueError, match=f"{name}: int8"):
+            DeviceLayer({**inp, **good, name + "_scale": bad}, device="cpu")
+    for name, bad in (("w2", inp["w2"]), ("w13", good["w13"][:, :-16]), ("w2", good["w2"][:-1])):
+        with pytest.raises(ValueError, match=f"{name}: int8"):
+            DeviceLayer({**inp, **good, name: bad}, device="cpu")
