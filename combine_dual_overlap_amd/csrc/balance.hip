@@ -586,7 +586,11 @@ extern "C" moe_status moe_route_select(const float* logits, int64_t T, const flo
   if (T == 0) return MOE_OK;
   if (!logits || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
   if (static_cast<const void*>(topk_w) == logits || static_cast<const void*>(topk_ids) == logits ||
-      static_cast<const void*>(topk_ids) == topk_w || (load && (load == topk_ids || static_cast<const void*>(load) == logits)))
+      static_cast<const void*>(topk_ids) == topk_w ||
+      (load && (load == topk_ids || static_cast<const void*>(load) == topk_w || static_cast<const void*>(load) == logits)))
+    return MOE_ERR_INVALID_ARG;
+  if (select_bias && (select_bias == topk_w || static_cast<const void*>(select_bias) == topk_ids ||
+                      static_cast<const void*>(select_bias) == load))
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(logits) || (select_bias && !aligned16(select_bias)) || !aligned16(topk_ids) || !aligned16(topk_w) ||
       (load && !aligned16(load)))
@@ -607,6 +611,15 @@ extern "C" moe_status moe_route_balanced(const void* x, moe_dtype act, int64_t T
   if (T >= (int64_t{1} << 26)) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !w_router || !topk_ids || !topk_w || !ws) return MOE_ERR_INVALID_ARG;
+  const void* outs[] = {topk_ids, topk_w, ws, logits_out, load};
+  const void* ins[] = {x, w_router, logit_bias, select_bias};
+  for (int i = 0; i < 5; ++i) {
+    if (!outs[i]) continue;
+    for (int j = 0; j < i; ++j)
+      if (outs[i] == outs[j]) return MOE_ERR_INVALID_ARG;
+    for (const void* in : ins)
+      if (outs[i] == in) return MOE_ERR_INVALID_ARG;
+  }
   if (!aligned16(x) || !aligned16(w_router) || !aligned16(topk_ids) || !aligned16(topk_w) ||
       (logit_bias && !aligned16(logit_bias)) || (select_bias && !aligned16(select_bias)) ||
       (logits_out && !aligned16(logits_out)) || (load && !aligned16(load)) || !aligned256(ws))
@@ -651,7 +664,8 @@ extern "C" moe_status moe_route_balance_loss(const float* logits, int64_t T, con
   if (!logits || !load || !dlogits || !ws) return MOE_ERR_INVALID_ARG;
   if (static_cast<const void*>(logits) == dlogits || static_cast<const void*>(load) == dlogits ||
       static_cast<const void*>(loss) == dlogits || static_cast<const void*>(loss) == logits ||
-      static_cast<const void*>(loss) == load || static_cast<const void*>(ws) == dlogits)
+      static_cast<const void*>(loss) == load || static_cast<const void*>(ws) == dlogits || ws == logits || ws == load ||
+      ws == loss)
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(logits) || !aligned16(load) || !aligned16(dlogits) || !aligned256(ws)) return MOE_ERR_MISALIGNED;
   if (ws_bytes < moe_route_balance_loss_workspace_size(T, params->E)) return MOE_ERR_WORKSPACE;

@@ -37,3 +37,36 @@ def test_integer_weights_come_with_a_scale_per_row():
     for name, bad in (("w2", inp["w2"]), ("w13", good["w13"][:, :-16]), ("w2", good["w2"][:-1])):
         with pytest.raises(ValueError, match=f"{name}: int8"):
             DeviceLayer({**inp, **good, name: bad}, device="cpu")
+
+
+def test_gate_refuses_buffers_that_stand_for_two():
+    from combine_dual_overlap_amd import binding as B
+    L = B.lib()
+    p = B.route_params(64, 6)
+    bad = B.MOE_ERR_INVALID_ARG
+
+    def select(l=A, b=2 * A, ids=3 * A, w=4 * A, load=5 * A):
+        return L.moe_route_select(l, 8, b, ctypes.byref(p), ids, w, load, None)
+
+    for kw in (dict(load=4 * A), dict(load=2 * A), dict(b=4 * A), dict(b=3 * A)):
+        assert select(**kw) == bad, kw
+
+    need = B.moe_route_workspace_size(8, 256, 64)
+
+    def balanced(**kw):
+        a = dict(x=A, wr=2 * A, lb=3 * A, sb=4 * A, lo=5 * A, ids=6 * A, w=7 * A, load=8 * A, ws=9 * A)
+        a.update(kw)
+        return L.moe_route_balanced(a["x"], B.MOE_BF16, 8, 256, a["wr"], a["lb"], a["sb"], ctypes.byref(p), a["lo"], a["ids"],
+                                    a["w"], a["load"], a["ws"], need, None)
+
+    outs, ins = ("ids", "w", "ws", "lo", "load"), ("x", "wr", "lb", "sb")
+    for i, o in enumerate(outs):
+        for other in outs[:i] + ins:
+            assert balanced(**{o: 10 * A, other: 10 * A}) == bad, (o, other)
+
+    def loss(l=A, load=2 * A, out=3 * A, d=4 * A, ws=5 * A):
+        return L.moe_route_balance_loss(l, 100, load, ctypes.byref(p), 0.1, out, d, B.MOE_F32, 0, ws,
+                                        B.moe_route_balance_loss_workspace_size(100, 64), None)
+
+    for ws in (A, 2 * A, 3 * A, 4 * A):
+        assert loss(ws=ws) == bad
