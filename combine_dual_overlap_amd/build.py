@@ -18,7 +18,12 @@ LIB = os.path.join(HERE, "libdbomoe.so")
 SOURCES = ["route.hip", "dispatch.hip", "ffn.hip", "combine.hip", "layer.hip", "grouped_gemm.hip", "backward.hip",
            "adamw.hip", "balance.hip", "int8.hip", "norms.hip"]
 ARCH = "gfx950"
-JOBS = min(8, int(os.environ.get("MAX_JOBS", os.cpu_count() or 1)))
+
+
+def jobs() -> int:
+    """Compilers at a time: MAX_JOBS if that is a whole number from 1 on, else the CPUs; at most 8."""
+    most = os.environ.get("MAX_JOBS", "").strip()
+    return min(8, int(most) if most.isdecimal() and int(most) > 0 else os.cpu_count() or 1)
 
 
 def hipcc() -> str:
@@ -43,7 +48,7 @@ def build(verbose: bool = False) -> str:
 
     if verbose:
         print(" ".join(cc), flush=True)
-    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(JOBS) as pool:
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(jobs()) as pool:
         objects = [os.path.join(tmp, s + ".o") for s in SOURCES]
         outs = list(pool.map(lambda s, o: run(cc + ["-c", os.path.join(CSRC, s), "-o", o]), SOURCES, objects))
         outs.append(run([cc[0], f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", LIB + ".tmp"] + objects))

@@ -70,3 +70,16 @@ def test_gate_refuses_buffers_that_stand_for_two():
 
     for ws in (A, 2 * A, 3 * A, 4 * A):
         assert loss(ws=ws) == bad
+
+
+def test_compilers_at_a_time(monkeypatch):
+    from combine_dual_overlap_amd import build
+    for value, want in (("3", 3), (" 2 ", 2), ("64", 8)):
+        monkeypatch.setenv("MAX_JOBS", value)
+        assert build.jobs() == want
+    monkeypatch.delenv("MAX_JOBS")
+    default = build.jobs()
+    assert 1 <= default <= 8
+    for value in ("", "0", "-2", "many", "1.5"):
+        monkeypatch.setenv("MAX_JOBS", value)
+        assert build.jobs() == default
