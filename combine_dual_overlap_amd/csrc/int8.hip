@@ -154,16 +154,15 @@ struct I8Shape {
 };
 
 // The quotient of the hardware's reciprocal is put right by its exact remainder, so h is what fp32
-// arithmetic makes it, and its codes with it.  (With that reciprocal alone and the hardware's
-// exponential, three of ten h were off in the last places, and one code in thousands: the prefill
-// experts in 525 us, not 540; with an IEEE division 562.)  1 + e^-g stays finite: the remainder of
-// an infinite one would be NaN.  From 2^126 on, g < -87, the reciprocal and h are 0.
+// arithmetic makes it, and its codes with it; the fixup gives what is infinite or NaN its value.
+// (With that reciprocal alone and the hardware's exponential, three of ten h were off in the last
+// places, and one code in thousands: the prefill experts in 525 us, not 540; with an IEEE division
+// 562.)  From 1 + e^-g = 2^126 on, g < -87, the reciprocal and h are 0.
 __device__ __forceinline__ float silu(float g) {
-  const float d = fminf(1.0f + expf(-g), 3.402823466e38f);
+  const float d = 1.0f + expf(-g);
   const float r = __builtin_amdgcn_rcpf(d), q = g * r;
-  return fmaf(fmaf(-d, q, g), r, q);
+  return __builtin_amdgcn_div_fixupf(fmaf(fmaf(-d, q, g), r, q), d, g);
 }
-
 
 struct I8Tile {
   int e, m_n, nt, tm;

@@ -36,6 +36,32 @@ def test_swiglu_is_rounded_like_fp32_arithmetic(rows, N):
     assert ((h.cpu().double() - want).abs() <= bound).all()
 
 
+@pytest.mark.filterwarnings("ignore:.*encountered:RuntimeWarning")      # (infinities, on purpose)
+def test_swiglu_of_gates_that_overflow():
+    """Gates that are infinite, NaN or at fp32's ends: what g / (1 + exp(-g)) * u is in fp32."""
+    B = _B()
+    g = torch.Generator().manual_seed(3)
+    rows, K, N = 40, 64, 32
+    a, b = _int8(g, rows, K), _int8(g, 1, 2 * N, K)
+    s, t = torch.full((rows,), 1e-3), torch.full((1, 2 * N), 1e-2)
+    s[1::5], s[2::5], s[3::5] = 1e36, torch.inf, torch.nan
+    t[0, :N:3] = 1e36
+    t[0, 1:N:3] = 10.0
+    h = torch.full((rows, N), 9.0, device=DEV)
+    B.moe_grouped_swiglu_int8(a.to(DEV), s.to(DEV), b.to(DEV), t.to(DEV), None, h)
+    gate, up = O.int8_product(a, s, b[0], t[0]).chunk(2, dim=1)
+    assert (gate == torch.inf).any() and (gate == -torch.inf).any() and gate.isnan().any()
+    want, got = gate / (1.0 + torch.exp(-gate)) * up, h.cpu()
+    # (between -87 and -88.8 the quotient is 0 where it is below 2^-126, and up may be infinite)
+    near = (gate > -87.0) | (gate < -88.8) | gate.isnan()
+    assert torch.equal(got.isnan()[near], want.isnan()[near])
+    wild = near & want.isinf()
+    assert torch.equal(got[wild], want[wild])
+    fine = near & want.isfinite()
+    # two such calculations of at most 5.1 half steps each
+    assert ((got[fine].double() - want[fine].double()).abs() <= 10.2 * O.U * want[fine].abs().double() + 2.0 ** -126).all()
+
+
 def _ragged(g, experts, mean):
     """Rows of each expert around `mean`, every ninth without any."""
     n = torch.randint(max(1, mean // 2), mean + mean // 2 + 1, (experts,), generator=g)
