@@ -84,28 +84,34 @@ __global__ __launch_bounds__(256) void k_route_bwd(const float* __restrict__ log
     if (id >= 0) d = dw[t * k + lane] * rp.routed_scale;
   }
   // A logit of -inf or NaN is a masked expert's, +inf the largest finite one.
-  auto logit = [&](int e) {
-    const float l = row[e];
-    return l > -INFINITY ? fminf(l, 3.402823466e38f) : -INFINITY;
-  };
-  const float mine = id >= 0 ? logit(id) : -INFINITY;
+  auto usable = [](float l) { return l > -INFINITY ? fminf(l, 3.402823466e38f) : -INFINITY; };
+  const float mine = id >= 0 ? usable(row[id]) : -INFINITY;
   const bool softmax = rp.score == MOE_SCORE_SOFTMAX;
   float p4[4] = {0.f, 0.f, 0.f, 0.f};
   float p = 0.f, slope = 1.f;               // the slot's score; for sigmoid its 1 - p
-  bool dead = false;                        // no expert has a finite logit
+  bool dead = false;                        // no expert has a logit that is not masked
   if (softmax) {
     float v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = lane + 64 * i < E ? logit(lane + 64 * i) : -INFINITY;
-    const float lmax = wave_max_f(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
-    dead = lmax == -INFINITY;
-    float denom = 0.f;
+    for (int i = 0; i < 4; ++i) v[i] = lane + 64 * i < E ? row[lane + 64 * i] : -INFINITY;
+    float lmax, denom;
+    auto terms = [&] {
+      lmax = wave_max_f(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
+      denom = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      p4[i] = lane + 64 * i < E ? expf(v[i] - lmax) : 0.f;
-      denom += p4[i];
+      for (int i = 0; i < 4; ++i) {
+        p4[i] = lane + 64 * i < E ? expf(v[i] - lmax) : 0.f;
+        denom += p4[i];
+      }
+      denom = wave_sum_f(denom);
+    };
+    terms();
+    if (!(denom < INFINITY)) {              // NaN: a logit was NaN or +inf, or all are -inf
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = usable(v[i]);
+      terms();
     }
-    denom = wave_sum_f(denom);
+    dead = lmax == -INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; ++i) p4[i] /= denom;
     if (id >= 0) p = expf(mine - lmax) / denom;
