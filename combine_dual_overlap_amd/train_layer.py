@@ -242,8 +242,6 @@ class TrainLayer:
 
     def _backward(self, dout):
         W, G, more = self.weights, self.grads, self._captured() or not self.fresh
-        if self.bias_rate > 0:
-            self.load_sum.add_(self.load)
         logits, ids, w, inv, x_perm, gu, h, y_perm, dy, dw, dgu, dx_perm, dlogits, dx_dense, dx = self._rows(
             "logits", "ids", "w", "inv", "x_perm", "gu", "h", "y_perm", "dy_perm", "dw", "dgu", "dx_perm", "dlogits",
             "dx_dense", "dx")
@@ -272,6 +270,8 @@ class TrainLayer:
         B.moe_combine(dx_perm, self.T, self.cfg.k, inv, self.ones[:self.T], dx, shared_out=dx_dense)
         if self.block is not None:
             dx = self._block_dx(dx, dblock if self.block["residual"] else None, more)
+        if self.bias_rate > 0:
+            self.load_sum.add_(self.load)
         self.fresh = False
         return dx
 

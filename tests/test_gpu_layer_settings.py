@@ -98,6 +98,8 @@ def test_passes_that_are_not_trained_on_do_not_move_the_bias():
         layer.forward((x * (i + 1) - i).contiguous() if i not in (2, 4) else x)
         if i in (2, 4):
             load += layer.load
+            with pytest.raises(ValueError):                # refused: not counted
+                layer.backward(torch.stack([dout, dout], 2)[..., 0])
             layer.backward(dout)
     layer.step()
     want = bias + 0.125 * torch.sign(load.float().mean() - load.float())
