@@ -13,8 +13,9 @@ namespace dbomoe {
 // experts close to each other on purpose, and what is chosen must not hang on the
 // rounding of a score.  4096 x 256 logits are 4 MB, under 1 us of HBM time: the steps
 // of the selection bound it.  One wave takes a token, so that a maximum is six DPP
-// instructions; 256 tokens x 6 of 64 3 us, 4096 x 8 of 256 in 4 of 8 groups 9.2 (a lane
-// has neighbouring experts, so that a group is a team of lanes; by way of LDS 11.2).
+// instructions; 256 tokens x 6 of 64 3.4 us (4.6 with the load), 4096 x 8 of 256 in 4 of 8
+// groups 9.6 (11.8; a lane has neighbouring experts, so that a group is a team of lanes; by way of
+// LDS two more).
 // An expert whose logit is -inf or NaN has score 0 and is chosen only when no
 // candidate is left; a logit of +inf counts as the largest finite one.
 struct SelectParams {
@@ -125,7 +126,7 @@ __device__ __forceinline__ double inverse(double x) {
 
 constexpr int kSelTokens = 4;      // tokens of a workgroup, one wave each
 
-// One wave per token, NE experts in a lane: expert lane + 64 i.
+// One wave per token, NE neighbouring experts in a lane.
 // A slot's expert is found by the keys rounded to fp32 (which keeps their order):
 // the wave's largest, then a ballot for who has it; only where several do, the keys
 // themselves are compared.

@@ -7,9 +7,10 @@
 // for the same bytes.
 // Few rows an expert: HBM-bound, 193 MB of weights in 40 us (4.8 TB/s).  Many: bound by
 // the matrix pipes at the clock that random integers leave (2.0 - 2.1 GHz): 8192^3 2040
-// TOP/s, 2780 with zeros; 65536 rows of 128 experts, 2048 -> 2 x 768 with SwiGLU 264 us
-// (1560 TOP/s), 768 -> 2048 165 us, 50 of these its stores, which all workgroups make at
-// about the same time.  No LDS bank conflicts by the counters.
+// TOP/s, 2780 with zeros; 65536 rows of 128 experts, 2048 -> 2 x 768 with SwiGLU 272 us
+// (1515 TOP/s), 768 -> 2048 165 us, 50 of these its stores, which all workgroups make at
+// about the same time.  LDS bank conflicts by the counters: 12 to 25 thousand cycles a call on all
+// compute units together, less than one in a thousand.
 #include "grouped_tile.h"
 #include "int8_rows.h"
 
@@ -127,7 +128,7 @@ struct I8Params {
 //  - The tile's scales come to LDS as its first stage does.
 //  - Of eight waves four load, one on each SIMD: while a stage's DMAs queue up (64 of
 //    16 clocks), the SIMD's other wave goes on with its MFMAs.  All eight loading
-//    against four: prefill gate/up 284 / 266 us, down 170 / 165, 8192^3 of zeros 423 /
+//    against four: prefill gate/up 284 / 266 us (with a shorter SwiGLU), down 170 / 165, 8192^3 of zeros 423 /
 //    395 (of random integers 545 / 538: the clock gives way to the power).
 //  - The second operand's rows are dealt to the MFMA's positions so that a lane ends
 //    up with 16 bytes of consecutive columns of its row and stores them as they are

@@ -3,7 +3,7 @@
 // ties to even.  x times the rounded 1 / scale, added to 1.5 * 2^23 in one fma, leaves
 // the nearest integer in the sum's low bits; it can only be wrong next to a half, which
 // the exact remainder x - code * scale (one fma) shows, and is then put right.  So codes
-// depend on the values alone, for six instructions each.  65536 x 2048 bf16: 73 us (5.5
+// depend on the values alone, for six instructions each.  65536 x 2048 bf16: 67 us (5.9
 // TB/s); with conversions and the comparisons in every one, 16 instructions, 85.  8192 x
 // 2048 11.4 us; where a lane with a tie did all its chunks again, 15.4.
 // A row that holds an infinity or NaN gets the scale NaN and codes 0: everything
