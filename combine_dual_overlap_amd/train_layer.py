@@ -109,8 +109,10 @@ class TrainLayer:
         self.balanced = self.select_bias is not None or balance_coef > 0
         if self.balanced and self.forced_ids is not None:
             raise ValueError("forced_ids: not with a selection bias or a balance loss")
-        self.route = B.route_params(cfg.E, cfg.k, cfg.score, cfg.renormalize, cfg.n_groups, cfg.topk_groups,
-                                    cfg.group_topn, cfg.routed_scale)
+        # (without a selection bias a softmax gate has no groups; the balanced gate, which counts the load, has)
+        groups = 1 if self.balanced and self.select_bias is None and cfg.score == "softmax" else cfg.n_groups
+        self.route = B.route_params(cfg.E, cfg.k, cfg.score, cfg.renormalize, groups, cfg.topk_groups, cfg.group_topn,
+                                    cfg.routed_scale)
 
         k, E, T = cfg.k, cfg.E, self.T_max
         n = T * k

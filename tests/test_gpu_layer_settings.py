@@ -105,3 +105,23 @@ def test_passes_that_are_not_trained_on_do_not_move_the_bias():
     want = bias + 0.125 * torch.sign(load.float().mean() - load.float())
     assert torch.equal(layer.select_bias, want)
     assert layer.load_sum.abs().sum() == 0
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_balance_loss_does_not_change_the_choice_of_experts(score):
+    """Softmax scores are not limited to groups without a selection bias, in training as in serving."""
+    import workloads as W
+    from combine_dual_overlap_amd import DeviceLayer, TrainLayer
+    cfg = W.get_config(1, small=True).replace(k=3, n_groups=4, topk_groups=2, group_topn=1, score=score)
+    inp = W.make_inputs(cfg, 5)
+    inp["forced_ids"] = None
+    x = inp["x"].to(DEV)
+    plain, loss = TrainLayer(inp), TrainLayer(inp, balance_coef=0.1)
+    want, got = plain.forward(x), loss.forward(x)
+    ids = plain.buf["ids"][:cfg.T]
+    assert torch.equal(loss.buf["ids"][:cfg.T], ids)
+    # the weights are fp32's of one gate and 64 bits' of the other: a few half steps
+    assert (got - want).abs().max() <= 2.0 ** -20 * want.abs().max()
+    serve = DeviceLayer(inp)
+    serve.run("unsplit")
+    assert torch.equal(serve.view(0, "topk_ids", torch.int32, (cfg.T, cfg.k)), ids)
