@@ -105,8 +105,8 @@ class DeviceLayer:
             E_loc = cfg.expert_end - cfg.expert_begin
             for name, w, s, shape in (("w13", self.w13, self.w13_scale, (E_loc, 2 * cfg.I, cfg.H)),
                                       ("w2", self.w2, self.w2_scale, (E_loc, cfg.H, cfg.I))):
-                if (w.dtype != torch.int8 or w.shape != shape or s is None or s.dtype != torch.float32 or
-                        s.shape != shape[:2]):
+                if (w.dtype != torch.int8 or w.dim() != 3 or w.shape[0] < E_loc or w.shape[1:] != shape[1:] or s is None or
+                        s.dtype != torch.float32 or s.shape != w.shape[:2]):
                     raise ValueError(f"{name}: int8 {list(shape)}, {name}_scale: float32 {list(shape[:2])}")
         self.select_bias = _dev(inp.get("select_bias"), d)
         if self.select_bias is not None and (self.select_bias.dtype != torch.float32 or self.select_bias.shape != (cfg.E,)):

@@ -30,6 +30,9 @@ def test_integer_weights_come_with_a_scale_per_row():
                 w13_scale=torch.ones(E, 2 * I), w2_scale=torch.ones(E, H))
     with pytest.raises(ValueError, match="device tensor"):           # nothing wrong but the device
         DeviceLayer({**inp, **good}, device="cpu")
+    more = dict(good, w13=torch.zeros(E + 1, 2 * I, H, dtype=torch.int8), w13_scale=torch.ones(E + 1, 2 * I))
+    with pytest.raises(ValueError, match="device tensor"):           # (experts behind the last are not used)
+        DeviceLayer({**inp, **more}, device="cpu")
     for name, bad in (("w13", torch.ones(E, 2 * I // 128, H // 128)), ("w2", torch.ones(E, 1)), ("w2", torch.ones(E, H).double()),
                       ("w13", None), ("w2", torch.ones(E - 1, H))):
         with pytest.raises(ValueError, match=f"{name}: int8"):
